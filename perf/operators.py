@@ -338,7 +338,8 @@ def _own_dispatch(state):
 
 def _own_attend(state):
     import sparse_selection_primitive_amd as L
-    out = L.cache_attend(state["q"], state["k"], state["v"], state["lengths"], state["acc"], acc_out=state["acc_out"])
+    out = L.cache_attend(state["q"], state["k"], state["v"], state["lengths"], state["acc"],
+                         account_out=state["acc_out"])
     return dict(out=out, acc=state["acc_out"])
 
 
@@ -347,7 +348,7 @@ def _own_evict(state):
     case = state["case"]
     kept, lengths = L.cache_evict(state["k"], state["v"], state["acc"], state["positions"], state["lengths"],
                                   case["keep"], next_position=state["next_position"], sinks=case["sinks"],
-                                  recent=case["recent"], acc_out=state["acc_out"],
+                                  recent=case["recent"], account_out=state["acc_out"],
                                   positions_out=state["positions_out"])
     return dict(kept=kept, lengths=lengths, k=state["k"], v=state["v"], acc=state["acc_out"],
                 positions=state["positions_out"])
