@@ -67,8 +67,9 @@ typedef enum lapsum_status {
     LAPSUM_ERR_PATH = 6,      /* the requested path cannot run this shape */
     LAPSUM_ERR_OPTION = 7,    /* an option is out of range */
     LAPSUM_ERR_HIP = 8,       /* a HIP launch or runtime query failed */
-    LAPSUM_ERR_SCRATCH = 9    /* lapsum_backward_noalloc: the call needs more scratch than the
+    LAPSUM_ERR_SCRATCH = 9,   /* lapsum_backward_noalloc: the call needs more scratch than the
                                  library's fixed buffer (LAPSUM_NOALLOC_SCRATCH_BYTES) holds */
+    LAPSUM_ERR_LAYOUT = 10    /* hard selections: a stride or a pointer's alignment the kernels cannot read */
 } lapsum_status;
 
 /* Longest row: sample indices use 32x32-bit products and tile counts fit int32.
@@ -291,6 +292,161 @@ lapsum_status lapsum_midpoint_mass(const float *r, int64_t rows, int64_t n, int6
  *   by the caller. */
 lapsum_status lapsum_backward_noalloc(const float *g, const float *p, const double *b, int64_t rows, int64_t n,
                                       double t, float *dr, float *dk, const lapsum_options *opt, void *stream);
+
+/* ===================================================== hard selections
+ * The hard counterparts of the soft top-k in its two uses: routing of tokens
+ * to experts (short rows, a small budget) with the dispatch of the tokens to
+ * the experts and back, and a cache that keeps the entries which received
+ * the most attention (long rows, a large budget) with the attention that
+ * reads it and keeps the account.  The conventions at the top of this file
+ * hold, with these differences:
+ *   - Values come in three types (lapsum_dtype); every sum, softmax statistic
+ *     and weight is held in fp32 and each output is rounded once.
+ *   - Scores need not be finite; what that means is said at each entry point.
+ *   - Index arrays on the device (chosen, slot, lengths, ...) are checked by
+ *     the kernels: an entry out of range counts as absent, never as an
+ *     address.
+ * Errors: LAPSUM_ERR_NULL, _SHAPE, _OPTION, _LAYOUT, _WORKSPACE (nothing
+ * launched), LAPSUM_ERR_HIP (launch failed). */
+typedef enum lapsum_dtype { LAPSUM_F32 = 0, LAPSUM_BF16 = 1, LAPSUM_F16 = 2 } lapsum_dtype;
+
+#define LAPSUM_MAX_EXPERTS 1024
+#define LAPSUM_MAX_CHOICES 32 /* experts chosen per token, at most */
+#define LAPSUM_MAX_GROUPS 64
+#define LAPSUM_MAX_PAIRS ((int64_t)1 << 23) /* (token, choice) pairs of one dispatch */
+#define LAPSUM_MAX_CACHE ((int64_t)1 << 30) /* entries per key head of a cache */
+
+enum { LAPSUM_SCORE_SOFTMAX = 0, LAPSUM_SCORE_SIGMOID = 1 };
+
+typedef struct lapsum_route_options {
+    int32_t k;           /* experts per token, 1 <= k <= min(experts, LAPSUM_MAX_CHOICES) */
+    int32_t score;       /* LAPSUM_SCORE_* */
+    int32_t groups;      /* 1: none; else it divides experts */
+    int32_t top_groups;  /* groups left open, 1..groups */
+    int32_t renormalise; /* 1: the chosen scores are divided by their sum */
+    float scale;         /* factor of the weights, finite */
+} lapsum_route_options;
+
+/* Routing.  With x the token's logits,
+ *     s = softmax(x)  or  1/(1 + e^-x),     c = s + bias,
+ * each group of experts scores the sum of its two largest c, the top_groups
+ * best groups stay open, the k largest c of the open groups are chosen, and
+ *     w_j = scale * s_j / S,   S = sum of the chosen s (renormalise) or 1.
+ * The bias balances the load: it takes part in the choice, not in the
+ * weights.  Equal c (and equal group scores) go to the lowest index; choices
+ * are in descending order of c.
+ *   logits  device [tokens, experts] of `dtype`, rows `row_stride` elements apart
+ *   bias    device [experts] fp32, or NULL
+ *   weights device [tokens, k] fp32;   chosen device [tokens, k] int32
+ * An expert whose logit or c is -inf or NaN is not available.  A slot that no
+ * available expert fills gets chosen = -1 and weight 0, so a row of -inf
+ * gives -1 and 0 throughout.  The softmax with logits of +inf is its limit
+ * (they share the mass equally).  A NaN logit makes the row's weights NaN
+ * (the choice is made among the others).  S = 0 gives weights 0. */
+lapsum_status lapsum_route_forward(const void *logits, int32_t dtype, int64_t tokens, int64_t experts,
+                                   int64_t row_stride, const float *bias, const lapsum_route_options *opt,
+                                   float *weights, int32_t *chosen, void *stream);
+
+/* Gradient of the weights with respect to the logits, the choice held fixed:
+ * with g_j = scale (dw_j - m)/S on the chosen, m = sum_i dw_i s_i / S when
+ * renormalised and 0 otherwise,
+ *     softmax  dx_i = s_i (g_i - sum_j g_j s_j),    sigmoid  dx_i = g_i s_i (1 - s_i).
+ *   dweights device [tokens, k] fp32;  chosen from the forward (distinct per row)
+ *   dlogits  device [tokens, experts] of `dtype`, contiguous */
+lapsum_status lapsum_route_backward(const float *dweights, const void *logits, int32_t dtype, int64_t tokens,
+                                    int64_t experts, int64_t row_stride, const int32_t *chosen,
+                                    const lapsum_route_options *opt, void *dlogits, void *stream);
+
+/* Dispatch plan: a stable counting sort of the tokens * k (token, choice)
+ * pairs by expert.
+ *   chosen  device [tokens, k] int32 (entries outside [0, experts) are dropped)
+ *   offsets device [experts + 1]: expert e's rows are offsets[e] .. offsets[e+1] - 1
+ *   slot    device [tokens, k]: the pair's row in expert order, -1 if dropped
+ *   order   device [tokens * k]: the pair t * k + j of each row, -1 behind the last one
+ * tokens * k <= LAPSUM_MAX_PAIRS, here and below. */
+size_t lapsum_dispatch_plan_workspace_bytes(int64_t tokens, int64_t k, int64_t experts);
+lapsum_status lapsum_dispatch_plan(const int32_t *chosen, int64_t tokens, int64_t k, int64_t experts,
+                                   int32_t *offsets, int32_t *slot, int32_t *order, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* Token rows into expert order: xs[slot[t, j]] = x[t]; rows behind the last
+ * pair (offsets[experts] and on) are zero.
+ *   x  device [tokens, width] of `dtype`, rows `row_stride` elements apart
+ *   xs device [tokens * k, width], contiguous
+ * The backward sums: dx[t] = sum_j dxs[slot[t, j]]. */
+lapsum_status lapsum_dispatch_forward(const void *x, int32_t dtype, int64_t tokens, int64_t k, int64_t width,
+                                      int64_t row_stride, const int32_t *slot, const int32_t *offsets,
+                                      int64_t experts, void *xs, void *stream);
+lapsum_status lapsum_dispatch_backward(const void *dxs, int32_t dtype, int64_t tokens, int64_t k, int64_t width,
+                                       const int32_t *slot, void *dx, void *stream);
+
+/* The experts' outputs back to the tokens: y[t] = sum_j w[t, j] ys[slot[t, j]]
+ * (dropped pairs leave no trace, whatever their weight).  The backward:
+ *     dys[slot[t, j]] = w[t, j] dy[t],    dweights[t, j] = <dy[t], ys[slot[t, j]]>,
+ * 0 for dropped pairs, rows behind the last pair zero.
+ *   ys, dys device [tokens * k, width] contiguous;  y device [tokens, width] contiguous;
+ *   dy device [tokens, width], rows `row_stride` elements apart */
+lapsum_status lapsum_combine_forward(const void *ys, int32_t dtype, int64_t tokens, int64_t k, int64_t width,
+                                     const int32_t *slot, const float *weights, void *y, void *stream);
+lapsum_status lapsum_combine_backward(const void *dy, int64_t row_stride, const void *ys, int32_t dtype,
+                                      int64_t tokens, int64_t k, int64_t width, const int32_t *slot,
+                                      const float *weights, const int32_t *offsets, int64_t experts, void *dys,
+                                      float *dweights, void *stream);
+
+/* A cache of keys and values per sequence and key head: entry s of head h of
+ * sequence b is the `width` contiguous elements at
+ * b * stride_batch + h * stride_head + s * stride_entry. */
+typedef struct lapsum_cache {
+    void *k, *v;          /* device */
+    int32_t dtype;        /* LAPSUM_BF16 or LAPSUM_F16 */
+    int32_t width;        /* elements per entry, a multiple of 8, at most 256 */
+    int64_t batch, heads; /* sequences, key heads */
+    int64_t capacity;     /* entries per head, at most LAPSUM_MAX_CACHE */
+    int64_t k_stride_batch, k_stride_head, k_stride_entry; /* elements, multiples of 8 */
+    int64_t v_stride_batch, v_stride_head, v_stride_entry;
+} lapsum_cache;
+
+/* Attention of the newest tokens over the cache, with the account of the
+ * weight that each entry received.  The `news` newest tokens of a sequence
+ * are its last `news` entries; token i sees the entries 0 .. length - news + i,
+ *     z = scale q.k,   p = softmax(z),   out = sum_s p_s v_s,
+ *     account_out[b, h, s] = account[b, h, s] + sum of p_s over the tokens and
+ *                            the query heads that read key head h.
+ * A token that sees nothing (length < news) gets out = 0 and adds nothing.
+ * Entries at length and behind are not read, and neither are their accounts
+ * written; what a token does not see does not reach its output, NaN and
+ * infinities included.
+ *   q, out   device [batch, news, q_heads, width] contiguous, of the cache's type;
+ *            q_heads a multiple of heads, query head j reads key head j / (q_heads / heads);
+ *            news * q_heads / heads <= 65536
+ *   lengths  device [batch] int32, taken as 0 .. capacity
+ *   account, account_out  device [batch, heads, capacity] fp32 contiguous (may be
+ *            the same array), or both NULL
+ * Pointers of k, v, q and out are 16-byte aligned (else LAPSUM_ERR_LAYOUT). */
+size_t lapsum_cache_attend_workspace_bytes(const lapsum_cache *cache, int64_t news, int64_t q_heads, int32_t accounts);
+lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, const int32_t *lengths, int64_t news,
+                                  int64_t q_heads, float scale, const float *account, float *account_out, void *out,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Eviction: of the entries 0 .. length - 1 of each sequence and head the
+ * first `keep` in this order stay: protected entries, then by account
+ * descending (NaN last), then by slot ascending.  An entry is protected if
+ * its position is below `sinks`, or at least next_position[b] - recent.
+ * Survivors at slot `keep` and behind move into the holes before it, the
+ * n-th survivor into the n-th hole; the others stay where they are.  k and v
+ * are changed in place.
+ *   account, positions          device [batch, heads, capacity]
+ *   account_out, positions_out  same shape (each may be its input): the
+ *                  slots below min(length, keep) are written
+ *   next_position  device [batch] int32, or NULL when recent = 0
+ *   kept           device [batch, heads, keep] int32: the slot each entry came
+ *                  from, -1 at min(length, keep) and behind
+ *   lengths_out    device [batch]: min(length, keep); may be lengths */
+size_t lapsum_cache_evict_workspace_bytes(const lapsum_cache *cache, int64_t keep);
+lapsum_status lapsum_cache_evict(const lapsum_cache *cache, const float *account, const int32_t *positions,
+                                 const int32_t *lengths, int64_t keep, const int32_t *next_position, int32_t sinks,
+                                 int32_t recent, float *account_out, int32_t *positions_out, int32_t *kept,
+                                 int32_t *lengths_out, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,9 @@ library is missing or the tensors are not on a GPU, the calls raise.
     p, b = lapsum_forward(r, k, t)          # r: [rows, n] fp32 on cuda
     dr, dk = lapsum_backward(g, p, b, t)
 
+The hard selections beside it (routing to experts, dispatch, cache attention
+and eviction) are in ``hard`` and are named here too.
+
 Source of the operator: "Fast LapSum: Exact Differentiable Top-k at Million
 Scale", section 2.1 (eqs. (1)-(2), analytic VJP) and section 2.2 (full-sort
 solver and probabilistic bracketing).
@@ -37,7 +40,11 @@ STAGE_NAMES = ["onchip_fwd", "init", "sample", "select", "filter", "band", "buck
 
 EXPORTED = ["lapsum_options_init", "lapsum_status_string", "lapsum_plan", "lapsum_bracket_indices",
             "lapsum_workspace_bytes", "lapsum_forward", "lapsum_backward", "lapsum_backward_noalloc",
-            "lapsum_midpoint_workspace_bytes", "lapsum_midpoint_mass"]
+            "lapsum_midpoint_workspace_bytes", "lapsum_midpoint_mass",
+            "lapsum_route_forward", "lapsum_route_backward", "lapsum_dispatch_plan_workspace_bytes",
+            "lapsum_dispatch_plan", "lapsum_dispatch_forward", "lapsum_dispatch_backward",
+            "lapsum_combine_forward", "lapsum_combine_backward", "lapsum_cache_attend_workspace_bytes",
+            "lapsum_cache_attend", "lapsum_cache_evict_workspace_bytes", "lapsum_cache_evict"]
 NOALLOC_SCRATCH_BYTES = 1 << 20  # LAPSUM_NOALLOC_SCRATCH_BYTES
 
 
@@ -110,6 +117,7 @@ def load_library():
     lib.lapsum_midpoint_workspace_bytes.restype = ctypes.c_size_t
     lib.lapsum_midpoint_mass.argtypes = [vp, i64, i64, i64, dbl, vp, vp, vp, ctypes.c_size_t, vp]
     lib.lapsum_midpoint_mass.restype = ctypes.c_int
+    hard.declare(lib)
     _lib = lib
     return lib
 
@@ -449,3 +457,9 @@ class Operator:
                                       self.stream if stream is None else stream)
         if rc:
             _check(rc, "lapsum_backward")
+
+
+from . import hard  # noqa: E402  (the hard selections use the helpers above)
+from .hard import (  # noqa: E402,F401
+    cache_attend, cache_evict, combine, combine_backward, combine_forward, dispatch, dispatch_backward,
+    dispatch_forward, dispatch_plan, route, route_backward, route_forward)

@@ -487,6 +487,7 @@ const char *lapsum_status_string(lapsum_status st) {
     case LAPSUM_ERR_PATH: return "the requested path cannot run this shape";
     case LAPSUM_ERR_OPTION: return "an option is out of range";
     case LAPSUM_ERR_HIP: return "HIP launch or runtime error";
+    case LAPSUM_ERR_LAYOUT: return "a stride or an alignment that the kernels cannot read";
     case LAPSUM_ERR_SCRATCH: return "the call needs more scratch than the fixed no-alloc buffer holds";
   }
   return "unknown status";

@@ -1,0 +1,370 @@
+// Dispatch of tokens to experts and back: the expert order of the chosen
+// (token, choice) pairs, the token rows laid out in it, and the weighted sum
+// of the experts' outputs, each with its gradient.
+//
+// The plan is a stable counting sort by expert.  A wave ranks its 64 pairs by
+// matching experts bit by bit with ballots, so a pair's place depends on its
+// index alone and the result is the same on every run.
+//
+// The row kernels only move data: k rows of `width` elements per token.  A
+// thread owns 16 bytes of a token's row and goes through the token's
+// k slots, so the token's side is read or written once and the experts' side
+// is touched in whole rows.
+#include "hard_dev.hpp"
+#include "hard_internal.hpp"
+
+namespace lapsum {
+namespace {
+
+constexpr int kPlanWaves = kPlanTile / 64;
+
+// Lanes of the wave that hold the same value below 2^bits (dead lanes: none).
+LDEV unsigned long long same_lanes(uint32_t v, bool live, int bits) {
+  unsigned long long m = __ballot(live);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = ((v >> b) & 1u) != 0;
+    const unsigned long long set = __ballot(one);
+    m &= one ? set : ~set;
+  }
+  return m;
+}
+LDEV int lanes_below(unsigned long long m) {
+  return __popcll(m & ((1ull << (threadIdx.x % 64)) - 1ull));
+}
+
+// Counts of a tile: count[wave][expert] pairs per wave (LDS, cleared by the
+// caller); returns the pair's rank among its expert's pairs of its wave.
+LDEV int rank_in_wave(uint16_t *count, int experts, int e, bool live, int bits) {
+  const unsigned long long same = same_lanes((uint32_t)e, live, bits);
+  const int rank = lanes_below(same);
+  if (live && rank == 0) count[(threadIdx.x / 64) * experts + e] = (uint16_t)__popcll(same);
+  return rank;
+}
+
+// Pairs per expert of each tile: counts[expert][tile].
+__global__ __launch_bounds__(kPlanTile) void plan_count_kernel(const int32_t *chosen, int64_t pairs, int experts,
+                                                               int bits, int tiles, uint32_t *counts) {
+  extern __shared__ uint16_t count[];  // [kPlanWaves][experts]
+  for (int i = threadIdx.x; i < kPlanWaves * experts; i += kPlanTile) count[i] = 0;
+  __syncthreads();
+  const int64_t i = (int64_t)blockIdx.x * kPlanTile + threadIdx.x;
+  const int e = i < pairs ? chosen[i] : -1;
+  rank_in_wave(count, experts, e, (uint32_t)e < (uint32_t)experts, bits);
+  __syncthreads();
+  for (int x = threadIdx.x; x < experts; x += kPlanTile) {
+    uint32_t n = 0;
+    for (int w = 0; w < kPlanWaves; ++w) n += count[w * experts + x];
+    counts[(int64_t)x * tiles + blockIdx.x] = n;
+  }
+}
+
+// One workgroup per expert: its tile counts become the pairs in earlier
+// tiles; its total goes behind them (totals[expert]).
+__global__ __launch_bounds__(256) void plan_scan_kernel(uint32_t *counts, int experts, int tiles, uint32_t *totals) {
+  struct Shared {
+    uint32_t wave[4];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  uint32_t *c = counts + (int64_t)blockIdx.x * tiles;
+  uint32_t carry = 0;
+  for (int base = 0; base < tiles; base += 256) {
+    const int i = base + (int)threadIdx.x;
+    const uint32_t v = i < tiles ? c[i] : 0;
+    uint32_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const uint32_t u = __shfl_up(inc, o, 64);
+      if ((int)(threadIdx.x % 64) >= o) inc += u;
+    }
+    if (threadIdx.x % 64 == 63) sh.wave[threadIdx.x / 64] = inc;
+    __syncthreads();
+    uint32_t before = carry, all = 0;
+    for (int w = 0; w < 4; ++w) {
+      if (w < (int)(threadIdx.x / 64)) before += sh.wave[w];
+      all += sh.wave[w];
+    }
+    if (i < tiles) c[i] = before + inc - v;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) totals[blockIdx.x] = carry;
+}
+
+// Exclusive sums of n <= kPlanTile values, one per thread, by the whole
+// workgroup; `all` gets the total.
+LDEV uint32_t exclusive_sum(uint32_t v, uint32_t *wave_sums, uint32_t &all) {
+  uint32_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const uint32_t u = __shfl_up(inc, o, 64);
+    if ((int)(threadIdx.x % 64) >= o) inc += u;
+  }
+  if (threadIdx.x % 64 == 63) wave_sums[threadIdx.x / 64] = inc;
+  __syncthreads();
+  uint32_t before = 0;
+  all = 0;
+  for (int w = 0; w < kPlanWaves; ++w) {
+    if (w < (int)(threadIdx.x / 64)) before += wave_sums[w];
+    all += wave_sums[w];
+  }
+  __syncthreads();
+  return before + inc - v;
+}
+
+// The places of a tile's pairs.  counts == NULL: the only tile, whose own
+// counts are the totals.
+__global__ __launch_bounds__(kPlanTile) void plan_place_kernel(const int32_t *chosen, int64_t pairs, int experts,
+                                                               int bits, int tiles, const uint32_t *counts,
+                                                               const uint32_t *totals, int32_t *offsets,
+                                                               int32_t *slot, int32_t *order) {
+  extern __shared__ uint16_t count[];  // [kPlanWaves][experts], then the experts' starts [experts]
+  __shared__ uint32_t wave_sums[kPlanWaves];
+  uint32_t *start = reinterpret_cast<uint32_t *>(count + kPlanWaves * experts);
+  for (int i = threadIdx.x; i < kPlanWaves * experts; i += kPlanTile) count[i] = 0;
+  __syncthreads();
+  const int64_t i = (int64_t)blockIdx.x * kPlanTile + threadIdx.x;
+  const int e = i < pairs ? chosen[i] : -1;
+  const bool live = (uint32_t)e < (uint32_t)experts;
+  const int rank = rank_in_wave(count, experts, e, live, bits);
+  __syncthreads();
+  // one thread per expert (experts <= kPlanTile): waves' counts to the pairs before them
+  const int x = threadIdx.x;
+  uint32_t here = 0;
+  if (x < experts) {
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const uint32_t n = count[w * experts + x];
+      count[w * experts + x] = (uint16_t)here;
+      here += n;
+    }
+  }
+  uint32_t all = 0;
+  const uint32_t total = x < experts ? (counts != nullptr ? totals[x] : here) : 0;
+  const uint32_t first = exclusive_sum(total, wave_sums, all);
+  if (x < experts) {
+    start[x] = first + (counts != nullptr ? counts[(int64_t)x * tiles + blockIdx.x] : 0);
+    if (blockIdx.x == 0) offsets[x] = (int32_t)first;
+  }
+  if (blockIdx.x == 0 && x == 0) offsets[experts] = (int32_t)all;
+  __syncthreads();
+  if (i < pairs) {
+    int at = -1;
+    if (live) {
+      at = (int)(start[e] + count[(threadIdx.x / 64) * experts + e]) + rank;
+      order[at] = (int32_t)i;
+    }
+    slot[i] = at;
+    if (i >= (int64_t)all) order[i] = -1;  // behind the last pair: no place there
+  }
+}
+
+int bits_for(int experts) {
+  int b = 0;
+  while ((1 << b) < experts) ++b;
+  return b;
+}
+
+// ----------------------------------------------------------------- rows
+// Threads per token by the row's length in 16-byte packs; a workgroup of 256
+// threads takes 256 / G tokens.
+template <class T, bool PACKS>
+struct Unit {  // what a thread moves at a time: a pack, or one element where rows are not 16-byte aligned
+  static constexpr int N = PACKS ? Pack<T>::N : 1;
+  float f[N];
+  LDEV void load(const T *p) {
+    if constexpr (PACKS) {
+      const pack_t<T> w = load_pack(p);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = (float)w[i];
+    } else {
+      f[0] = (float)*p;
+    }
+  }
+  LDEV void store(T *p) const {
+    if constexpr (PACKS) {
+      pack_t<T> w;
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = (T)f[i];
+      store_pack(p, w);
+    } else {
+      *p = (T)f[0];
+    }
+  }
+  LDEV void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = 0.0f;
+  }
+};
+
+LDEV int slot_at(const RowsArgs &a, int64_t pair) {
+  const int s = a.slot[pair];
+  return (uint64_t)(int64_t)s < (uint64_t)a.pairs ? s : -1;
+}
+
+// xs[slot[t][j]] = x[t]; the rows behind the last pair are zeroed by the
+// tokens whose pairs have those indices.
+template <class T, bool PACKS, int G>
+__global__ __launch_bounds__(256) void dispatch_rows_kernel(const RowsArgs a) {
+  using U = Unit<T, PACKS>;
+  const int64_t token = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  if (token >= a.tokens) return;
+  const int64_t placed = *a.placed;
+  const T *src = static_cast<const T *>(a.src) + token * a.stride;
+  T *dst = static_cast<T *>(a.dst);
+  for (int64_t c = (int64_t)(threadIdx.x % G) * U::N; c < a.width; c += (int64_t)G * U::N) {
+    U u, z;
+    u.load(src + c);
+    z.zero();
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t pair = token * a.k + j;
+      const int s = slot_at(a, pair);
+      if (s >= 0) u.store(dst + (int64_t)s * a.width + c);
+      if (pair >= placed) z.store(dst + pair * a.width + c);
+    }
+  }
+}
+
+// y[t] = sum_j w[t][j] ys[slot[t][j]], in the order of j, in fp32
+template <class T, bool PACKS, int G>
+__global__ __launch_bounds__(256) void sum_rows_kernel(const RowsArgs a) {
+  using U = Unit<T, PACKS>;
+  const int64_t token = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  if (token >= a.tokens) return;
+  const T *src = static_cast<const T *>(a.src);
+  T *dst = static_cast<T *>(a.dst) + token * a.width;
+  for (int64_t c = (int64_t)(threadIdx.x % G) * U::N; c < a.width; c += (int64_t)G * U::N) {
+    U sum;
+    sum.zero();
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t pair = token * a.k + j;
+      const int s = slot_at(a, pair);
+      if (s < 0) continue;
+      U u;
+      u.load(src + (int64_t)s * a.width + c);
+      const float w = a.weights != nullptr ? a.weights[pair] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < U::N; ++i) sum.f[i] = __builtin_fmaf(w, u.f[i], sum.f[i]);
+    }
+    sum.store(dst + c);
+  }
+}
+
+// dys[slot] = w dy[t], dweights = <dy[t], ys[slot]>: one pass over both.  The
+// products' sum goes over the team's lanes in a fixed order.
+template <class T, bool PACKS, int G>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const RowsArgs a) {
+  using U = Unit<T, PACKS>;
+  constexpr int kWavesPer = G > 64 ? G / 64 : 1;
+  struct Shared {
+    float part[LAPSUM_MAX_CHOICES][4];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  const int64_t token = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const bool live = token < a.tokens;
+  const int64_t placed = *a.placed;
+  const T *dy = static_cast<const T *>(a.dy) + (live ? token : 0) * a.stride;
+  const T *ys = static_cast<const T *>(a.src);
+  T *dys = static_cast<T *>(a.dst);
+  const int lane = threadIdx.x % G;
+  for (int j = 0; j < a.k; ++j) {
+    float dot = 0.0f;
+    if (live) {
+      const int64_t pair = token * a.k + j;
+      const int s = slot_at(a, pair);
+      const float w = a.weights[pair];
+      for (int64_t c = (int64_t)lane * U::N; c < a.width; c += (int64_t)G * U::N) {
+        if (s >= 0) {
+          U g, u;
+          g.load(dy + c);
+          u.load(ys + (int64_t)s * a.width + c);
+#pragma unroll
+          for (int i = 0; i < U::N; ++i) {
+            dot = __builtin_fmaf(g.f[i], u.f[i], dot);
+            g.f[i] *= w;
+          }
+          g.store(dys + (int64_t)s * a.width + c);
+        }
+        if (pair >= placed) {
+          U z;
+          z.zero();
+          z.store(dys + pair * a.width + c);
+        }
+      }
+    }
+    dot = team_sum<(G < 64 ? G : 64)>(dot);
+    if constexpr (G <= 64) {
+      if (live && lane == 0) a.dweights[token * a.k + j] = dot;
+    } else {
+      if (threadIdx.x % 64 == 0) sh.part[j][threadIdx.x / 64] = dot;
+    }
+  }
+  if constexpr (G > 64) {
+    __syncthreads();
+    if (live && lane < a.k) {
+      float dot = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWavesPer; ++w) dot += sh.part[lane][(threadIdx.x / G) * kWavesPer + w];
+      a.dweights[token * a.k + lane] = dot;
+    }
+  }
+}
+
+enum Kind { kDispatch, kSum, kBackward };
+
+template <class T, bool PACKS, int G>
+hipError_t rows(const RowsArgs &a, Kind kind, hipStream_t s) {
+  constexpr int per = 256 / G;
+  const dim3 grid((unsigned)((a.tokens + per - 1) / per));
+  if (kind == kDispatch) dispatch_rows_kernel<T, PACKS, G><<<grid, dim3(256), 0, s>>>(a);
+  else if (kind == kSum) sum_rows_kernel<T, PACKS, G><<<grid, dim3(256), 0, s>>>(a);
+  else combine_backward_kernel<T, PACKS, G><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+template <class T>
+hipError_t rows_of(const RowsArgs &a, Kind kind, hipStream_t s) {
+  const auto aligned = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const bool packs = a.width % Pack<T>::N == 0 && a.stride % Pack<T>::N == 0 && aligned(a.src) && aligned(a.dst) &&
+                     aligned(a.dy);
+  const int64_t units = packs ? a.width / Pack<T>::N : a.width;
+  if (packs) return units <= 64 ? rows<T, true, 64>(a, kind, s) : rows<T, true, 256>(a, kind, s);
+  return units <= 64 ? rows<T, false, 64>(a, kind, s) : rows<T, false, 256>(a, kind, s);
+}
+hipError_t rows_any(const RowsArgs &a, Kind kind, int dtype, hipStream_t s) {
+  if (dtype == LAPSUM_F32) return rows_of<f32>(a, kind, s);
+  if (dtype == LAPSUM_BF16) return rows_of<bf16>(a, kind, s);
+  return rows_of<f16>(a, kind, s);
+}
+
+}  // namespace
+
+int64_t plan_tiles(int64_t pairs) { return (pairs + kPlanTile - 1) / kPlanTile; }
+
+hipError_t launch_dispatch_plan(const int32_t *chosen, int64_t pairs, int experts, int32_t *offsets, int32_t *slot,
+                                int32_t *order, uint32_t *counts, hipStream_t s) {
+  const int tiles = (int)plan_tiles(pairs), bits = bits_for(experts);
+  const size_t lds = (size_t)kPlanWaves * experts * sizeof(uint16_t), start = (size_t)experts * sizeof(uint32_t);
+  uint32_t *totals = nullptr;
+  if (tiles > 1) {
+    totals = counts + (size_t)experts * tiles;
+    plan_count_kernel<<<dim3(tiles), dim3(kPlanTile), lds, s>>>(chosen, pairs, experts, bits, tiles, counts);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    plan_scan_kernel<<<dim3(experts), dim3(256), 0, s>>>(counts, experts, tiles, totals);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } else {
+    counts = nullptr;
+  }
+  plan_place_kernel<<<dim3(tiles), dim3(kPlanTile), lds + start, s>>>(chosen, pairs, experts, bits, tiles, counts,
+                                                                      totals, offsets, slot, order);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch_rows(const RowsArgs &a, int dtype, hipStream_t s) { return rows_any(a, kDispatch, dtype, s); }
+hipError_t launch_sum_rows(const RowsArgs &a, int dtype, hipStream_t s) { return rows_any(a, kSum, dtype, s); }
+hipError_t launch_combine_backward(const RowsArgs &a, int dtype, hipStream_t s) {
+  return rows_any(a, kBackward, dtype, s);
+}
+
+}  // namespace lapsum

@@ -1,0 +1,469 @@
+"""The hard selections beside the soft top-k: Python binding.
+
+Routing of tokens to experts and back, with gradients:
+
+    weights, chosen = route_forward(logits, k, bias, score="sigmoid", groups=8, top_groups=4)
+    offsets, slot, order = dispatch_plan(chosen, experts)
+    xs = dispatch_forward(x, slot, offsets)          # expert e's rows: xs[offsets[e]:offsets[e + 1]]
+    y = combine_forward(ys, slot, weights)           # ys: the experts' outputs, in the rows of xs
+    route / dispatch / combine                       # the same, differentiable
+
+A cache that keeps the entries which received the most attention:
+
+    out = cache_attend(q, k, v, lengths, account)    # adds each entry's weight to account
+    kept, lengths = cache_evict(k, v, account, positions, lengths, keep, next_position=n, recent=256)
+
+As in the rest of the package this only marshals arguments; the formulas and
+what happens to masked, infinite and missing values stand in
+``include/lapsum.h``.  Calls run on torch's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+from . import LapsumError, _check, _torch, _workspace, load_library
+
+F32, BF16, F16 = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
+MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
+
+
+class RouteOptions(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("batch", ctypes.c_int64), ("heads", ctypes.c_int64), ("capacity", ctypes.c_int64),
+                ("k_stride_batch", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+                ("k_stride_entry", ctypes.c_int64), ("v_stride_batch", ctypes.c_int64),
+                ("v_stride_head", ctypes.c_int64), ("v_stride_entry", ctypes.c_int64)]
+
+
+def declare(lib):
+    i32, i64, vp, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    opt, cache = ctypes.POINTER(RouteOptions), ctypes.POINTER(Cache)
+    for name, res, args in [
+        ("route_forward", ctypes.c_int, [vp, i32, i64, i64, i64, vp, opt, vp, vp, vp]),
+        ("route_backward", ctypes.c_int, [vp, vp, i32, i64, i64, i64, vp, opt, vp, vp]),
+        ("dispatch_plan_workspace_bytes", size, [i64, i64, i64]),
+        ("dispatch_plan", ctypes.c_int, [vp, i64, i64, i64, vp, vp, vp, vp, size, vp]),
+        ("dispatch_forward", ctypes.c_int, [vp, i32, i64, i64, i64, i64, vp, vp, i64, vp, vp]),
+        ("dispatch_backward", ctypes.c_int, [vp, i32, i64, i64, i64, vp, vp, vp]),
+        ("combine_forward", ctypes.c_int, [vp, i32, i64, i64, i64, vp, vp, vp, vp]),
+        ("combine_backward", ctypes.c_int, [vp, i64, vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp]),
+        ("cache_attend_workspace_bytes", size, [cache, i64, i64, i32]),
+        ("cache_attend", ctypes.c_int, [vp, cache, vp, i64, i64, ctypes.c_float, vp, vp, vp, vp, size, vp]),
+        ("cache_evict_workspace_bytes", size, [cache, i64]),
+        ("cache_evict", ctypes.c_int, [cache, vp, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp, vp, size, vp]),
+    ]:
+        f = getattr(lib, "lapsum_" + name)
+        f.restype, f.argtypes = res, args
+
+
+# ----------------------------------------------------------------- checks
+def _dtype(x, name, only=None):
+    torch = _torch()
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(x.dtype)
+    if code is None or (only is not None and code not in only):
+        kinds = "bfloat16 or float16" if only else "float32, bfloat16 or float16"
+        raise LapsumError(f"{name} must be {kinds}")
+    return code
+
+
+def _gpu(x, name, dim=None, dev=None):
+    if not isinstance(x, _torch().Tensor) or not x.is_cuda:
+        raise LapsumError(f"{name} must be a GPU tensor (no CPU path exists)")
+    if dim is not None and x.dim() != dim:
+        raise LapsumError(f"{name} must have {dim} dimensions")
+    if dev is not None and x.device != dev:
+        raise LapsumError(f"{name} must be on {dev}")
+    return x
+
+
+def _array(x, name, dtype, shape, dev):
+    """A contiguous device tensor of exactly this type and shape."""
+    _gpu(x, name, dev=dev)
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape):
+        raise LapsumError(f"{name} must be {dtype} {list(shape)}")
+    return x.contiguous()
+
+
+def _out(x, name, dtype, shape, dev):
+    """An output: the caller's tensor (used as it is, so it must be contiguous), or a new one."""
+    if x is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    _gpu(x, name, dev=dev)
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+        raise LapsumError(f"{name} must be contiguous {dtype} {list(shape)}")
+    return x
+
+
+def _rows(x, name):
+    """[tokens, n] with contiguous rows (any distance between them): (x, stride)."""
+    _gpu(x, name, 2)
+    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        x = x.contiguous()
+    return x, (x.stride(0) if x.shape[0] > 1 else x.shape[1])
+
+
+class _on:
+    """Makes a device current for the length of a call (nothing to do when it is)."""
+
+    def __init__(self, dev):
+        torch = _torch()
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self.dev = dev
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _torch().cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+# ---------------------------------------------------------------- routing
+@functools.lru_cache(maxsize=256)
+def _route_options(k, score, groups, top_groups, renormalise, scale):
+    if score not in SCORES:
+        raise LapsumError(f"score must be one of {sorted(SCORES)}")
+    return RouteOptions(k, SCORES[score], groups, groups if top_groups is None else top_groups, int(bool(renormalise)),
+                        scale)
+
+
+def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, renormalise=True, scale=1.0,
+                  out=None):
+    """weights fp32 [tokens, k] and chosen int32 [tokens, k] for a router's logits [tokens, experts].
+
+    The k largest of score + bias are chosen, in descending order (ties to the
+    lowest index), among the experts of the top_groups best groups (all groups
+    by default); the weights are the chosen scores (without the bias), divided
+    by their sum if renormalise, times scale.  A slot without an available
+    expert holds -1 and weight 0.  out: (weights, chosen) to write into."""
+    torch = _torch()
+    lib = load_library()
+    code = _dtype(_gpu(logits, "logits", 2), "logits")
+    x, stride = _rows(logits, "logits")
+    (tokens, experts), dev = x.shape, x.device
+    opt = _route_options(int(k), score, int(groups), top_groups, renormalise, float(scale))
+    if bias is not None:
+        bias = _array(bias, "bias", torch.float32, (experts,), dev)
+    weights = _out(None if out is None else out[0], "weights", torch.float32, (tokens, opt.k), dev)
+    chosen = _out(None if out is None else out[1], "chosen", torch.int32, (tokens, opt.k), dev)
+    if tokens == 0:
+        return weights, chosen
+    with _on(dev) as stream:
+        _check(lib.lapsum_route_forward(x.data_ptr(), code, tokens, experts, stride,
+                                        None if bias is None else bias.data_ptr(), opt, weights.data_ptr(),
+                                        chosen.data_ptr(), stream), "lapsum_route_forward")
+    return weights, chosen
+
+
+def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=True, scale=1.0, out=None):
+    """dlogits [tokens, experts], of the logits' type: the gradient of the weights, the choice held fixed
+    (score, renormalise and scale as in the forward)."""
+    torch = _torch()
+    lib = load_library()
+    code = _dtype(_gpu(logits, "logits", 2), "logits")
+    x, stride = _rows(logits, "logits")
+    (tokens, experts), dev = x.shape, x.device
+    chosen = _array(_gpu(chosen, "chosen", 2), "chosen", torch.int32, (tokens, chosen.shape[1]), dev)
+    dweights = _array(dweights, "dweights", torch.float32, chosen.shape, dev)
+    opt = _route_options(chosen.shape[1], score, 1, 1, renormalise, float(scale))
+    dlogits = _out(out, "dlogits", logits.dtype, (tokens, experts), dev)
+    if tokens == 0:
+        return dlogits
+    with _on(dev) as stream:
+        _check(lib.lapsum_route_backward(dweights.data_ptr(), x.data_ptr(), code, tokens, experts, stride,
+                                         chosen.data_ptr(), opt, dlogits.data_ptr(), stream),
+               "lapsum_route_backward")
+    return dlogits
+
+
+def route(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, renormalise=True, scale=1.0):
+    """Differentiable route_forward: the weights' gradient reaches the logits.  The choice is not differentiable, so
+    the bias, which takes part in nothing else, gets no gradient."""
+    torch = _torch()
+
+    class _Route(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            weights, chosen = route_forward(x, k, bias, score=score, groups=groups, top_groups=top_groups,
+                                            renormalise=renormalise, scale=scale)
+            ctx.save_for_backward(x, chosen)
+            ctx.mark_non_differentiable(chosen)
+            return weights, chosen
+
+        @staticmethod
+        def backward(ctx, dweights, _):
+            x, chosen = ctx.saved_tensors
+            return route_backward(dweights.contiguous(), x, chosen, score=score, renormalise=renormalise, scale=scale)
+
+    return _Route.apply(logits)
+
+
+# --------------------------------------------------------------- dispatch
+@functools.lru_cache(maxsize=1024)
+def _plan_bytes(tokens, k, experts):
+    return int(load_library().lapsum_dispatch_plan_workspace_bytes(tokens, k, experts))
+
+
+def dispatch_plan(chosen, experts):
+    """The expert order of the (token, choice) pairs of chosen [tokens, k]:
+    offsets int32 [experts + 1] (expert e's rows are offsets[e]:offsets[e + 1]), slot int32 [tokens, k] (a pair's row, -1
+    for entries that name no expert) and order int32 [tokens * k] (the pair t * k + j of a row, -1 behind the last)."""
+    torch = _torch()
+    lib = load_library()
+    _gpu(chosen, "chosen", 2)
+    (tokens, k), dev, experts = chosen.shape, chosen.device, int(experts)
+    chosen = _array(chosen, "chosen", torch.int32, (tokens, k), dev)
+    if tokens * k == 0:
+        return (torch.zeros(experts + 1, dtype=torch.int32, device=dev), torch.empty_like(chosen),
+                torch.empty(0, dtype=torch.int32, device=dev))
+    # one allocation for the three small arrays
+    both = torch.empty(2 * tokens * k + experts + 1, dtype=torch.int32, device=dev)
+    slot, order, offsets = both[:tokens * k].view(tokens, k), both[tokens * k:2 * tokens * k], both[2 * tokens * k:]
+    with _on(dev) as stream:
+        ws, wptr, wlen = _workspace(_plan_bytes(tokens, k, experts), dev)
+        rc = lib.lapsum_dispatch_plan(chosen.data_ptr(), tokens, k, experts, offsets.data_ptr(), slot.data_ptr(),
+                                      order.data_ptr(), wptr, wlen, stream)
+        del ws
+        _check(rc, "lapsum_dispatch_plan")
+    return offsets, slot, order
+
+
+def _slot_of(slot, dev, tokens=None):
+    _gpu(slot, "slot", 2)
+    return _array(slot, "slot", _torch().int32, (slot.shape[0] if tokens is None else tokens, slot.shape[1]), dev)
+
+
+def _offsets_of(offsets, dev):
+    return _array(_gpu(offsets, "offsets", 1), "offsets", _torch().int32, offsets.shape, dev)
+
+
+def dispatch_forward(x, slot, offsets, *, out=None):
+    """xs [tokens * k, width]: token rows in expert order, xs[slot[t, j]] = x[t] (rows behind the last pair zero)."""
+    lib = load_library()
+    code = _dtype(_gpu(x, "x", 2), "x")
+    x, stride = _rows(x, "x")
+    (tokens, width), dev = x.shape, x.device
+    slot, offsets = _slot_of(slot, dev, tokens), _offsets_of(offsets, dev)
+    k = slot.shape[1]
+    xs = _out(out, "xs", x.dtype, (tokens * k, width), dev)
+    if xs.numel() == 0:
+        return xs
+    with _on(dev) as stream:
+        _check(lib.lapsum_dispatch_forward(x.data_ptr(), code, tokens, k, width, stride, slot.data_ptr(),
+                                           offsets.data_ptr(), offsets.numel() - 1, xs.data_ptr(), stream),
+               "lapsum_dispatch_forward")
+    return xs
+
+
+def dispatch_backward(dxs, slot, *, out=None):
+    """dx [tokens, width]: the sum of each token's rows of dxs."""
+    lib = load_library()
+    code = _dtype(_gpu(dxs, "dxs", 2), "dxs")
+    dev = dxs.device
+    slot = _slot_of(slot, dev)
+    (tokens, k), width = slot.shape, dxs.shape[1]
+    dxs = _array(dxs, "dxs", dxs.dtype, (tokens * k, width), dev)
+    dx = _out(out, "dx", dxs.dtype, (tokens, width), dev)
+    if dxs.numel() == 0:
+        return dx.zero_()
+    with _on(dev) as stream:
+        _check(lib.lapsum_dispatch_backward(dxs.data_ptr(), code, tokens, k, width, slot.data_ptr(), dx.data_ptr(),
+                                            stream), "lapsum_dispatch_backward")
+    return dx
+
+
+def combine_forward(ys, slot, weights, *, out=None):
+    """y [tokens, width]: y[t] = sum_j weights[t, j] ys[slot[t, j]]."""
+    torch = _torch()
+    lib = load_library()
+    code = _dtype(_gpu(ys, "ys", 2), "ys")
+    dev = ys.device
+    slot = _slot_of(slot, dev)
+    (tokens, k), width = slot.shape, ys.shape[1]
+    ys = _array(ys, "ys", ys.dtype, (tokens * k, width), dev)
+    weights = _array(weights, "weights", torch.float32, (tokens, k), dev)
+    y = _out(out, "y", ys.dtype, (tokens, width), dev)
+    if ys.numel() == 0:
+        return y.zero_()
+    with _on(dev) as stream:
+        _check(lib.lapsum_combine_forward(ys.data_ptr(), code, tokens, k, width, slot.data_ptr(), weights.data_ptr(),
+                                          y.data_ptr(), stream), "lapsum_combine_forward")
+    return y
+
+
+def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
+    """dys [tokens * k, width] and dweights fp32 [tokens, k]: dys[slot] = w dy[t], dweights = <dy[t], ys[slot]>."""
+    torch = _torch()
+    lib = load_library()
+    code = _dtype(_gpu(dy, "dy", 2), "dy")
+    dy, stride = _rows(dy, "dy")
+    (tokens, width), dev = dy.shape, dy.device
+    slot, offsets = _slot_of(slot, dev, tokens), _offsets_of(offsets, dev)
+    k = slot.shape[1]
+    ys = _array(ys, "ys", dy.dtype, (tokens * k, width), dev)
+    weights = _array(weights, "weights", torch.float32, (tokens, k), dev)
+    dys = _out(None if out is None else out[0], "dys", dy.dtype, (tokens * k, width), dev)
+    dweights = _out(None if out is None else out[1], "dweights", torch.float32, (tokens, k), dev)
+    if ys.numel() == 0:
+        return dys, dweights.zero_()
+    with _on(dev) as stream:
+        _check(lib.lapsum_combine_backward(dy.data_ptr(), stride, ys.data_ptr(), code, tokens, k, width,
+                                           slot.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
+                                           offsets.numel() - 1, dys.data_ptr(), dweights.data_ptr(), stream),
+               "lapsum_combine_backward")
+    return dys, dweights
+
+
+def dispatch(x, slot, offsets):
+    """Differentiable dispatch_forward."""
+    torch = _torch()
+
+    class _Dispatch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return dispatch_forward(x, slot, offsets)
+
+        @staticmethod
+        def backward(ctx, dxs):
+            return dispatch_backward(dxs.contiguous(), slot)
+
+    return _Dispatch.apply(x)
+
+
+def combine(ys, weights, slot, offsets):
+    """Differentiable combine_forward: gradients reach the experts' outputs and the weights."""
+    torch = _torch()
+
+    class _Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ys, weights):
+            ctx.save_for_backward(ys, weights)
+            return combine_forward(ys, slot, weights)
+
+        @staticmethod
+        def backward(ctx, dy):
+            ys, weights = ctx.saved_tensors
+            return combine_backward(dy, ys, slot, weights, offsets)
+
+    return _Combine.apply(ys, weights)
+
+
+# ------------------------------------------------------------------ cache
+@functools.lru_cache(maxsize=1024)
+def _cache_shape(code, k_shape, k_strides, v_strides):
+    """The layout of a cache (everything but its pointers)."""
+    batch, heads, capacity, width = k_shape
+    return Cache(None, None, code, width, batch, heads, capacity, *k_strides, *v_strides)
+
+
+def _cache_of(k, v):
+    code = _dtype(_gpu(k, "k", 4), "k", (BF16, F16))
+    _gpu(v, "v", 4, k.device)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise LapsumError("k and v must have the same type and shape")
+    if k.stride(3) != 1 or v.stride(3) != 1:
+        raise LapsumError("the entries of k and v must be contiguous (last stride 1)")
+    shape = _cache_shape(code, tuple(k.shape), tuple(k.stride()[:3]), tuple(v.stride()[:3]))
+    cache = Cache.from_buffer_copy(shape)
+    cache.k, cache.v = k.data_ptr(), v.data_ptr()
+    return cache
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_bytes(code, k_shape, news, q_heads, accounts):
+    batch, heads, capacity, width = k_shape
+    cache = Cache(None, None, code, width, batch, heads, capacity, 0, 0, 0, 0, 0, 0)
+    return int(load_library().lapsum_cache_attend_workspace_bytes(cache, news, q_heads, accounts))
+
+
+def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None, out=None):
+    """out [batch, news, q_heads, width]: attention of the newest tokens q over a cache k, v
+    [batch, heads, capacity, width] whose first lengths[b] entries are filled, the new tokens' own last (token i sees
+    the entries up to lengths[b] - news + i).  account fp32 [batch, heads, capacity]: each entry's weight, summed over
+    the new tokens and the query heads of its key head, is added to it, in place or into account_out.  scale: 1/sqrt(width) by default."""
+    torch = _torch()
+    lib = load_library()
+    cache = _cache_of(k, v)
+    dev = k.device
+    _gpu(q, "q", 4, dev)
+    batch, news, q_heads, width = q.shape
+    if q.dtype != k.dtype or batch != k.shape[0] or width != k.shape[3]:
+        raise LapsumError("q must be [batch, news, q_heads, width] of the cache's type")
+    q = q.contiguous()
+    lengths = _array(lengths, "lengths", torch.int32, (batch,), dev)
+    out = _out(out, "out", q.dtype, q.shape, dev)
+    if account is not None:
+        if account_out is None:
+            account_out = account  # written in place: not a copy of it
+        else:
+            account = _array(account, "account", torch.float32, k.shape[:3], dev)
+        account_out = _out(account_out, "account", torch.float32, k.shape[:3], dev)
+    elif account_out is not None:
+        raise LapsumError("account_out needs an account")
+    if q.numel() == 0:
+        return out
+    with _on(dev) as stream:
+        nbytes = _attend_bytes(cache.dtype, tuple(k.shape), news, q_heads, int(account is not None))
+        ws, wptr, wlen = _workspace(nbytes, dev)
+        rc = lib.lapsum_cache_attend(q.data_ptr(), cache, lengths.data_ptr(), news, q_heads,
+                                     width ** -0.5 if scale is None else float(scale),
+                                     None if account is None else account.data_ptr(),
+                                     None if account is None else account_out.data_ptr(), out.data_ptr(), wptr, wlen,
+                                     stream)
+        del ws
+        _check(rc, "lapsum_cache_attend")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _evict_bytes(code, k_shape, keep):
+    batch, heads, capacity, width = k_shape
+    cache = Cache(None, None, code, width, batch, heads, capacity, 0, 0, 0, 0, 0, 0)
+    return int(load_library().lapsum_cache_evict_workspace_bytes(cache, keep))
+
+
+def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, sinks=0, recent=0, account_out=None,
+                positions_out=None):
+    """Brings every cache row down to `keep` entries: protected entries (position below sinks, or at least
+    next_position[b] - recent) stay first, then those of the highest account (ties: the lowest slot).  Survivors
+    behind slot keep move into the holes before it, keys, values, accounts and positions; k and v are changed in
+    place, account and positions too unless account_out and positions_out are given.
+
+    Returns kept int32 [batch, heads, keep] (the slot each entry came from, -1 behind the last) and the new lengths
+    (a new tensor)."""
+    torch = _torch()
+    lib = load_library()
+    cache = _cache_of(k, v)
+    dev, batch, keep = k.device, k.shape[0], int(keep)
+    shape = tuple(k.shape[:3])
+    # arrays that are written in place have to be usable as they are
+    account = _out(account, "account", torch.float32, shape, dev) if account_out is None else _array(
+        account, "account", torch.float32, shape, dev)
+    positions = _out(positions, "positions", torch.int32, shape, dev) if positions_out is None else _array(
+        positions, "positions", torch.int32, shape, dev)
+    account_out = _out(account if account_out is None else account_out, "account_out", torch.float32, shape, dev)
+    positions_out = _out(positions if positions_out is None else positions_out, "positions_out", torch.int32, shape,
+                         dev)
+    lengths = _array(lengths, "lengths", torch.int32, (batch,), dev)
+    if next_position is not None:
+        next_position = _array(next_position, "next_position", torch.int32, (batch,), dev)
+    with _on(dev) as stream:
+        kept = torch.empty(shape[:2] + (max(keep, 0),), dtype=torch.int32, device=dev)
+        lengths_out = torch.empty_like(lengths)
+        ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, tuple(k.shape), keep), dev)
+        rc = lib.lapsum_cache_evict(cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,
+                                    None if next_position is None else next_position.data_ptr(), int(sinks),
+                                    int(recent), account_out.data_ptr(), positions_out.data_ptr(), kept.data_ptr(),
+                                    lengths_out.data_ptr(), wptr, wlen, stream)
+        del ws
+        _check(rc, "lapsum_cache_evict")
+    return kept, lengths_out

@@ -1,0 +1,303 @@
+"""Routing to experts on the GPU against a plain 64-bit form.
+
+Logits lie on a grid of 1/8 and biases on one of 1/64, so equal scores are
+exactly equal and different ones far apart (rows where sums of two come
+close by chance are left out): the choice is compared exactly.  Tolerances: a score is exp or 1/(1 + exp) of a difference
+whose rounding is 2^-24 of its size, plus a few roundings of the sums and the
+quotient, so weights are within (16 + 4 range) 2^-24 of their size, range
+the spread of the row's logits; a gradient within the same of the sum of its
+terms' sizes, and half an ulp of its type.
+"""
+import math
+
+import pytest
+
+import hard_plain as plain
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+HALF_ULP = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+TINY = {"fp32": 1e-38, "bf16": 1e-38, "fp16": 2.0 ** -25}
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import sparse_selection_primitive_amd as lib
+    lib.load_library()
+    return lib
+
+
+def grid_logits(tokens, experts, seed, spread=24):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(-spread, spread + 1, (tokens, experts), generator=g).double() / 8
+
+
+def grid_bias(experts, seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+    return torch.randint(-8, 9, (experts,), generator=g).double() / 64
+
+
+def settled(x, bias, kw):
+    """The rows whose scores, and group sums, differ by 0 or by far more than the roundings."""
+    s = torch.softmax(x, 1) if kw["score"] == "softmax" else torch.sigmoid(x)
+    c = s if bias is None else s + bias
+    lists = [c]
+    if kw["groups"] > 1:
+        lists.append(torch.topk(c.view(len(x), kw["groups"], -1), min(2, c.shape[1] // kw["groups"]), 2).values.sum(2))
+    ok = torch.ones(len(x), dtype=torch.bool)
+    for v in lists:
+        v = torch.sort(v, 1).values
+        gap = v[:, 1:] - v[:, :-1]
+        ok &= ~((gap > 1e-12) & (gap < 1e-6 * v.abs().amax(1, keepdim=True).clamp(1e-3))).any(1)
+    assert ok.float().mean() > 0.9
+    return ok
+
+
+def check(L, x, k, bias=None, dtype="fp32", grad=True, **kw):
+    kw = dict(dict(score="softmax", groups=1, top_groups=1, renormalise=True, scale=1.0), **kw)
+    xt = x.to(TYPES[dtype]).cuda() if x.device.type == "cpu" else x
+    x = xt.double().cpu()
+    bt = None if bias is None else bias.float().cuda()
+    w, c = L.route_forward(xt, k, bt, **kw)
+    pw, pc, s = plain.route(x, k, bias, **kw)
+    assert torch.equal(c.cpu(), pc)
+    finite = x[torch.isfinite(x)]
+    spread = float(finite.max() - finite.min()) if finite.numel() else 0.0
+    rel = (16 + 4 * spread) * 2.0 ** -24
+    got = w.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(pw))
+    fine = ~torch.isnan(pw)
+    assert ((got - pw).abs()[fine] <= rel * pw.abs()[fine] + 1e-37).all()
+    if not grad:
+        return
+    dw = torch.randn(c.shape, generator=torch.Generator().manual_seed(7))
+    dx = L.route_backward(dw.cuda(), xt, c, score=kw["score"], renormalise=kw["renormalise"], scale=kw["scale"])
+    assert dx.dtype == xt.dtype and dx.shape == xt.shape
+    there = pc >= 0
+    picked = torch.where(there, s.gather(1, pc.clamp(min=0).long()), 0.0)
+    total = picked.sum(1, keepdim=True) if kw["renormalise"] else torch.ones_like(picked[:, :1])
+    total = torch.where(total > 0, total, 1.0)
+    d = torch.where(there, dw.double(), 0.0)
+    mean = (d * picked).sum(1, keepdim=True) / total if kw["renormalise"] else torch.zeros_like(total)
+    size_mean = (d.abs() * picked).sum(1, keepdim=True) / total if kw["renormalise"] else mean
+    on = torch.zeros_like(s).scatter_add_(1, pc.clamp(min=0).long(), torch.where(there, 1.0, 0.0).double())
+
+    def spread_out(v):
+        return torch.zeros_like(s).scatter_add_(1, pc.clamp(min=0).long(), torch.where(there, v, 0.0))
+
+    g, size_g = spread_out(kw["scale"] * (d - mean) / total), spread_out(kw["scale"] * (d.abs() + size_mean) / total)
+    if kw["score"] == "softmax":
+        want = s * (g - (g * s).sum(1, keepdim=True))
+        size = s * (size_g + (size_g * s).sum(1, keepdim=True))
+        if kw["renormalise"]:  # exactly 0 outside the choice: the sum above cancels there
+            want, size = want * (on > 0), size * (on > 0)
+    else:
+        want, size = g * s * (1 - s), size_g * s
+    err = (dx.double().cpu() - want).abs()
+    assert (err <= rel * size + HALF_ULP[dtype] * want.abs() + TINY[dtype]).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens,experts,k", [
+    (1, 1, 1), (1, 8, 2), (3, 7, 7), (33, 60, 6), (129, 64, 4), (5, 100, 8), (130, 128, 1), (17, 256, 8),
+    (64, 255, 16), (9, 300, 32), (4, 512, 10), (3, 1000, 32), (2, 1024, 5), (70, 16, 16)])
+def test_shapes(L, tokens, experts, k, score):
+    x = grid_logits(tokens, experts, tokens + experts)
+    for renormalise in (True, False):
+        check(L, x, k, score=score, renormalise=renormalise, scale=1.5)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("experts", [40, 60, 96, 250, 256, 264])
+def test_types_with_bias(L, dtype, experts):
+    for seed in range(2):
+        x, bias = grid_logits(37, experts, seed), grid_bias(experts, seed)
+        kw = dict(score="sigmoid", groups=1, top_groups=1)
+        check(L, x[settled(x, bias, kw)], 6, bias, dtype, scale=2.5, **kw)
+
+
+@pytest.mark.parametrize("experts,groups,top_groups,k", [
+    (256, 8, 4, 8), (64, 8, 1, 8), (60, 4, 2, 6), (160, 8, 3, 6), (64, 64, 9, 9), (96, 3, 3, 5), (1024, 64, 7, 32),
+    (14, 7, 2, 4), (512, 2, 1, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups(L, experts, groups, top_groups, k, score):
+    x, bias = grid_logits(41, experts, experts + groups), grid_bias(experts, groups)
+    kw = dict(score=score, groups=groups, top_groups=top_groups)
+    for b in (None, bias):
+        check(L, x[settled(x, b, kw)], k, b, renormalise=score == "sigmoid", **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts", [12, 64, 256])
+def test_ties_go_to_the_lowest_index(L, score, experts):
+    x = torch.zeros(5, experts, dtype=torch.float64)
+    x[1, experts // 2:] = 1.0
+    x[2] = -0.0
+    x[2, 1::2] = 0.0  # minus zero and zero are equal
+    x[3] = -4.0
+    x[4, -1] = 2.0
+    check(L, x, 5, score=score)
+    bias = torch.zeros(experts, dtype=torch.float64)
+    bias[experts // 3:] = -0.5  # negative scores tie as well
+    check(L, x - 3.0, 5, bias - 0.25, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_masked_experts(L, score, dtype):
+    x = grid_logits(8, 48, 3)
+    x[0] = -math.inf                 # nothing is left
+    x[1, 3:] = -math.inf             # fewer than k are left
+    x[2, ::2] = -math.inf
+    x[3, 5] = math.inf if score == "sigmoid" else 0.0
+    x[4] = torch.finfo(TYPES[dtype]).min  # the type's lowest value is a value: all equal
+    x[5, 1:] = torch.finfo(TYPES[dtype]).min
+    x[6, 0:40] = -math.inf
+    x[6, 40:] = -3.0
+    bias = torch.zeros(48, dtype=torch.float64)
+    bias[7] = -math.inf              # an expert taken out by its bias
+    for renormalise in (True, False):
+        check(L, x, 6, None, dtype, grad=False, score=score, renormalise=renormalise)
+        check(L, x, 6, bias, dtype, grad=False, score=score, renormalise=renormalise)
+    # gradients: rows whose scores are not all lost
+    check(L, x[[0, 1, 2, 6, 7]], 6, None, dtype, score=score, renormalise=False)
+    check(L, x[[0, 1, 2, 6, 7]], 6, None, dtype, score=score, renormalise=True)
+
+
+def test_masked_groups(L):
+    x = grid_logits(6, 32, 5)
+    x[:, 0:8] = -math.inf            # a group without experts
+    x[0] = -math.inf
+    x[1, 9:] = -math.inf             # one expert left, alone in its group
+    for tg in (1, 2, 4):
+        check(L, x, 4, None, grad=False, score="sigmoid", groups=4, top_groups=tg)
+
+
+def test_softmax_of_infinite_logits_is_its_limit(L):
+    x = grid_logits(2, 20, 9)
+    x[0, [3, 11]] = math.inf
+    w, c = L.route_forward(x.float().cuda(), 4, renormalise=False)
+    assert c[0].tolist() == [3, 11, 0, 1] and w[0].tolist() == [0.5, 0.5, 0.0, 0.0]
+
+
+def test_nan_logits_show_in_the_weights(L):
+    x = grid_logits(70, 33, 11)
+    x[0, 4] = math.nan
+    x[64] = math.nan
+    for score in ("softmax", "sigmoid"):
+        check(L, x, 3, grad=False, score=score)
+
+
+def test_score_that_underflows_gives_weight_zero(L):
+    x = torch.full((1, 8), -300.0, dtype=torch.float64)
+    w, c = L.route_forward(x.float().cuda(), 2, score="sigmoid")
+    assert c.tolist() == [[0, 1]] and w.tolist() == [[0.0, 0.0]]
+
+
+@pytest.mark.parametrize("dtype,experts", [("fp32", 64), ("bf16", 64), ("bf16", 100), ("fp32", 37)])
+def test_strided_and_misaligned_rows(L, dtype, experts):
+    x = grid_logits(50, experts, 21)
+    for pad, shift in ((8, 0), (3, 1), (16, 8), (1, 3)):
+        wide = torch.full((50, experts + pad + shift), math.nan, dtype=TYPES[dtype], device="cuda")
+        view = wide[:, shift:shift + experts]
+        view.copy_(x)
+        check(L, view, 5, None, dtype)
+        check(L, view, 5, None, dtype, renormalise=False)
+    check(L, x.to(TYPES[dtype]).cuda().t().contiguous().t(), 5, None, dtype)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [True, False])
+def test_gradient_against_differences(L, score, renormalise):
+    x = grid_logits(6, 24, 31)
+    w, c = L.route_forward(x.float().cuda(), 4, score=score, renormalise=renormalise, scale=1.25)
+    c = c.cpu()
+    dw = torch.randn(6, 4, dtype=torch.float64, generator=torch.Generator().manual_seed(3))
+    h = 1e-5  # differences in 64 bits: h^2 and 1e-16 / h are both below 1e-10
+    diff = torch.zeros_like(x)
+    for i in range(24):
+        up, down = x.clone(), x.clone()
+        up[:, i] += h
+        down[:, i] -= h
+        f = [(plain.route_weights(z, c, score, renormalise, 1.25) * dw).sum(1) for z in (up, down)]
+        diff[:, i] = (f[0] - f[1]) / (2 * h)
+    dx = L.route_backward(dw.float().cuda(), x.float().cuda(), c.cuda(), score=score, renormalise=renormalise,
+                          scale=1.25)
+    # dw is rounded to fp32 too: a few 2^-24 of the terms, each below max |dw| * scale
+    assert (dx.double().cpu() - diff).abs().max() <= 64 * 2.0 ** -24 * 1.25 * dw.abs().max()
+
+
+def test_autograd(L):
+    x = grid_logits(9, 32, 41).float().cuda().requires_grad_(True)
+    bias = grid_bias(32, 4).float().cuda()
+    w, c = L.route(x, 4, bias, score="sigmoid", scale=2.0)
+    assert not c.requires_grad
+    (w * torch.arange(1, 5, device="cuda")).sum().backward()
+    x2 = x.detach().double().cpu().requires_grad_(True)
+    (plain.route_weights(x2, c.cpu(), "sigmoid", True, 2.0) * torch.arange(1, 5)).sum().backward()
+    assert (x.grad.double().cpu() - x2.grad).abs().max() <= 64 * 2.0 ** -24 * 8
+
+
+def test_other_stream_graph_and_repeat(L):
+    x = grid_logits(300, 256, 51).bfloat16().cuda()
+    bias = grid_bias(256, 5).float().cuda()
+    kw = dict(score="sigmoid", groups=8, top_groups=4)
+    dw = torch.randn(300, 8, device="cuda")
+    w, c = L.route_forward(x, 8, bias, **kw)
+    dx = L.route_backward(dw, x, c, score="sigmoid")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        w2, c2 = L.route_forward(x, 8, bias, **kw)
+    side.synchronize()
+    assert torch.equal(w, w2) and torch.equal(c, c2)
+    graph = torch.cuda.CUDAGraph()
+    w3, c3, dx3 = torch.empty_like(w), torch.empty_like(c), torch.empty_like(dx)
+    with torch.cuda.graph(graph):
+        L.route_forward(x, 8, bias, out=(w3, c3), **kw)
+        L.route_backward(dw, x, c3, score="sigmoid", out=dx3)
+    for _ in range(3):
+        w3.zero_(), c3.zero_(), dx3.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(w, w3) and torch.equal(c, c3) and torch.equal(dx, dx3)
+
+
+def test_no_tokens(L):
+    w, c = L.route_forward(torch.empty(0, 16, device="cuda"), 3)
+    assert w.shape == (0, 3) and c.shape == (0, 3)
+    assert L.route_backward(w, torch.empty(0, 16, device="cuda"), c).shape == (0, 16)
+
+
+def test_choice_out_of_range_is_ignored_by_the_backward(L):
+    x = grid_logits(3, 16, 61).float().cuda()
+    w, c = L.route_forward(x, 2, renormalise=False)
+    bad = c.clone()
+    bad[1, 0], bad[2, 1] = 16, -7
+    dw = torch.ones_like(w)
+    dx = L.route_backward(dw, x, bad, renormalise=False)
+    assert torch.isfinite(dx).all() and torch.equal(dx[0], L.route_backward(dw, x, c, renormalise=False)[0])
+
+
+def test_refusals(L):
+    x = torch.randn(4, 16, device="cuda")
+    with pytest.raises(L.LapsumError):
+        L.route_forward(x.cpu(), 2)
+    with pytest.raises(L.LapsumError):
+        L.route_forward(x.double(), 2)
+    with pytest.raises(L.LapsumError):
+        L.route_forward(x, 2, score="relu")
+    with pytest.raises(L.LapsumError):
+        L.route_forward(x, 2, torch.zeros(15, device="cuda"))
+    for bad in (dict(k=0), dict(k=17), dict(k=2, groups=3), dict(k=2, groups=4, top_groups=5),
+                dict(k=2, groups=4, top_groups=0), dict(k=2, scale=math.inf)):
+        with pytest.raises(L.LapsumError):
+            L.route_forward(x, bad.pop("k"), **bad)
+    with pytest.raises(L.LapsumError):
+        L.route_forward(torch.randn(4, 1025, device="cuda"), 2)
+    with pytest.raises(L.LapsumError):
+        L.route_backward(torch.randn(4, 3, device="cuda"), x, torch.zeros(4, 2, dtype=torch.int32, device="cuda"))
