@@ -315,6 +315,7 @@ typedef enum lapsum_dtype { LAPSUM_F32 = 0, LAPSUM_BF16 = 1, LAPSUM_F16 = 2 } la
 #define LAPSUM_MAX_GROUPS 64
 #define LAPSUM_MAX_PAIRS ((int64_t)1 << 23) /* (token, choice) pairs of one dispatch */
 #define LAPSUM_MAX_CACHE ((int64_t)1 << 30) /* entries per key head of a cache */
+#define LAPSUM_MAX_ENTRY_STRIDE ((int64_t)1 << 23) /* elements between two entries of a key head */
 
 enum { LAPSUM_SCORE_SOFTMAX = 0, LAPSUM_SCORE_SIGMOID = 1 };
 
@@ -402,7 +403,8 @@ typedef struct lapsum_cache {
     int32_t width;        /* elements per entry, a multiple of 8, at most 256 */
     int64_t batch, heads; /* sequences, key heads */
     int64_t capacity;     /* entries per head, at most LAPSUM_MAX_CACHE */
-    int64_t k_stride_batch, k_stride_head, k_stride_entry; /* elements, multiples of 8 */
+    int64_t k_stride_batch, k_stride_head, k_stride_entry; /* elements, multiples of 8, not negative;
+                                                               entries LAPSUM_MAX_ENTRY_STRIDE at most */
     int64_t v_stride_batch, v_stride_head, v_stride_entry;
 } lapsum_cache;
 

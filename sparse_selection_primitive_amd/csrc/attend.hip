@@ -80,20 +80,55 @@ LDEV void load_queries(const AttendArgs &a, int64_t bh, int row, pack_t<T> (&q)[
   }
 }
 
-// this lane's part of 16 keys (first factor of Z'): entry first + lane % 16, held to the last one
-template <class T, int DP, bool EXACT>
-LDEV void load_keys(const AttendArgs &a, const T *keys, int first, int last, pack_t<T> (&k)[DP / 32]) {
-  const int lane = threadIdx.x % 64, c = lane / 16;
-  const int e = first + lane % 16;
-  const T *p = keys + (int64_t)(e < last ? e : last) * a.ke;
-#pragma unroll
-  for (int i = 0; i < DP / 32; ++i) {
-    const int d = i * 32 + c * 8;
-    const bool there = EXACT || d < a.width;
-    const uint4 w = *reinterpret_cast<const uint4 *>(p + (there ? d : 0));
-    k[i] = __builtin_bit_cast(pack_t<T>, there ? w : uint4{0, 0, 0, 0});
-  }
+// A window of memory that buffer loads are held to: what lies past its end
+// reads as zero.  Entries are reached through a window that starts at the block's first
+// one, so a load's address is the window (scalar registers), an offset of the lane that
+// stays the same from block to block, and a scalar offset.
+using window_t = __amdgpu_buffer_rsrc_t;
+LDEV window_t window_of(const void *first, int64_t bytes) {
+  const int64_t most = 0x7FFFFFF0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0, (int)(bytes < most ? bytes : most),
+                                           0x00020000);  // 32-bit data format
 }
+constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
+
+LDEV uint4 load_16(window_t w, uint32_t lane_offset, int offset) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane_offset, offset, 0));
+}
+LDEV uint2 load_8(window_t w, uint32_t lane_offset, int offset) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane_offset, offset, 0));
+}
+
+// the entries [first, end) of keys or values
+template <class T>
+LDEV window_t entries(const T *base, int64_t stride, int first, int end, int width) {
+  return window_of(base + (int64_t)first * stride, ((int64_t)(end - 1 - first) * stride + width) * (int64_t)sizeof(T));
+}
+
+// This lane's part of 16 keys (first factor of Z'): entry lane % 16 of the
+// window's `at`-th entry and on.
+template <class T, int DP, bool EXACT>
+struct Keys {
+  static constexpr int kSteps = DP / 32;
+  uint32_t off[EXACT ? 1 : kSteps];
+  int stride;  // bytes
+  LDEV explicit Keys(const AttendArgs &a) {
+    const int lane = threadIdx.x % 64;
+    stride = (int)a.ke * 2;
+    const uint32_t o = (uint32_t)((lane % 16) * stride + (lane / 16) * 16);
+    if constexpr (EXACT) {
+      off[0] = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) off[i] = i * 32 + (lane / 16) * 8 < a.width ? o : kNowhere;
+    }
+  }
+  LDEV void load(window_t w, int at, pack_t<T> (&k)[kSteps]) const {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      k[i] = __builtin_bit_cast(pack_t<T>, load_16(w, off[EXACT ? 0 : i] + i * 64, at * stride));
+  }
+};
 
 // the place-th entry of this lane's eight in a block
 LDEV int entry_of(int place) {
@@ -106,17 +141,26 @@ struct Values {
   static constexpr int W = DP / 16;  // elements per lane and entry
   typedef T vec __attribute__((ext_vector_type(DP / 16)));
   vec v[8];
-  template <bool EXACT>
-  LDEV void load(const AttendArgs &a, const T *values, int first, int last) {
-    const int d = (threadIdx.x % 16) * W;
-    const bool there = EXACT || d < a.width;
+  // off: this lane's offset in a window (value_offset)
+  LDEV void load(window_t w, uint32_t off, int stride) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = first + entry_of(j);
-      const T *p = values + (int64_t)(e < last ? e : last) * a.ve + (there ? d : 0);
-      v[j] = *reinterpret_cast<const vec *>(p);
-      if (!there) v[j] = (T)0.0f;
+      const int at = ((j / 4) * 16 + j % 4) * stride;
+      if constexpr (W == 4) {
+        v[j] = __builtin_bit_cast(vec, load_8(w, off, at));
+      } else if constexpr (W == 8) {
+        v[j] = __builtin_bit_cast(vec, load_16(w, off, at));
+      } else {
+        struct Two {
+          uint4 x, y;
+        } two = {load_16(w, off, at), load_16(w, off + 16, at)};
+        v[j] = __builtin_bit_cast(vec, two);
+      }
     }
+  }
+  static LDEV uint32_t value_offset(const AttendArgs &a) {
+    const int lane = threadIdx.x % 64, d = (lane % 16) * W;
+    return d < a.width ? (uint32_t)((lane / 16) * 4 * (int)a.ve * 2 + d * 2) : kNowhere;
   }
   LDEV pack_t<T> column(int n) const {
     pack_t<T> w;
@@ -126,27 +170,36 @@ struct Values {
   }
 };
 
-template <class T, int DP, int NT, bool EXACT>
-__global__ __launch_bounds__(64 * kAttendWaves) void attend_kernel(const AttendArgs a) {
+// The waves of a workgroup share its entries (BY_ROWS false: few rows, so the
+// entries' bytes are what counts; a wave takes every fourth block and the
+// waves are joined at the end) or its rows (BY_ROWS: every wave goes through
+// all the entries for rows of its own, and what one wave loads the others find in
+// the cache of their compute unit).
+template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE>
+__global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) void attend_kernel(const AttendArgs a) {
   constexpr int W = DP / 16;
   constexpr int kRows = 16 * NT;
+  constexpr int kPad = DP + 4;  // floats per row in LDS: 16 rows' 16-byte accesses fall on all banks
   struct Shared {
     float m[kAttendWaves][kRows], l[kAttendWaves][kRows];
-    float o[kRows][DP];
+    float o[BY_ROWS ? 1 : kAttendWaves][BY_ROWS ? 1 : kRows][BY_ROWS ? 4 : kPad];
   };
   __shared__ Shared sh;
   lds_poison(sh);
   const int64_t bh = grid_row();
   if (bh >= (int64_t)a.batch * a.heads) return;
-  const int split = blockIdx.x % a.splits, row0 = (blockIdx.x / a.splits) * kRows;
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64, c = lane / 16, r = lane % 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lane = threadIdx.x % 64, c = lane / 16, r = lane % 16;
+  const int split = blockIdx.x % a.splits;
+  const int row0 = (int)(blockIdx.x / a.splits) * kRows * (BY_ROWS ? kAttendWaves : 1) + (BY_ROWS ? wave * kRows : 0);
+  if (BY_ROWS && row0 >= a.rows) return;  // no barrier follows on that path
   const int length = length_of(a, bh);
   int begin, end;
   split_range(a, length, split, begin, end);
   float *ml = a.part_ml + ((bh * a.splits + split) * a.rows + row0) * 2;
   const int rows_here = min(a.rows - row0, kRows);
   if (begin >= end) {  // the same for the whole workgroup
-    for (int i = threadIdx.x; i < rows_here; i += blockDim.x) {
+    for (int i = BY_ROWS ? lane : threadIdx.x; i < rows_here; i += BY_ROWS ? 64 : blockDim.x) {
       ml[2 * i] = -INFINITY;
       ml[2 * i + 1] = 0.0f;
     }
@@ -155,7 +208,21 @@ __global__ __launch_bounds__(64 * kAttendWaves) void attend_kernel(const AttendA
   const int64_t b = bh / a.heads, h = bh % a.heads;
   const T *keys = static_cast<const T *>(a.k) + b * a.kb + h * a.kh;
   const T *values = static_cast<const T *>(a.v) + b * a.vb + h * a.vh;
+  constexpr int kStride = BY_ROWS ? kBlock : kStep;
+  const int first = begin + (BY_ROWS ? 0 : wave * kBlock);
 
+  // a block's keys are asked for as soon as the last block's are used up, its
+  // values likewise, so each is on its way while the other is worked on
+  const Keys<T, DP, EXACT> key(a);
+  const uint32_t value_off = Values<T, DP>::value_offset(a);
+  pack_t<T> k[2][DP / 32];
+  Values<T, DP> v;
+  if (first < end) {
+    const window_t w = entries(keys, a.ke, first, end, a.width);
+    key.load(w, 0, k[0]);
+    key.load(w, 16, k[1]);
+    v.load(entries(values, a.ve, first, end, a.width), value_off, (int)a.ve * 2);
+  }
   pack_t<T> q[NT][DP / 32];
   int limit[NT];  // the last entry this lane's row sees
 #pragma unroll
@@ -175,106 +242,156 @@ __global__ __launch_bounds__(64 * kAttendWaves) void attend_kernel(const AttendA
     for (int n = 0; n < W; ++n) o[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  for (int e0 = begin + wave * kBlock; e0 < end; e0 += kStep) {
-    pack_t<T> k[2][DP / 32];
-    Values<T, DP> v;
-    load_keys<T, DP, EXACT>(a, keys, e0, end - 1, k[0]);
-    load_keys<T, DP, EXACT>(a, keys, e0 + 16, end - 1, k[1]);
-    v.template load<EXACT>(a, values, e0, end - 1);
-    // some row does not see some entry of the block
-    const bool edge = e0 + kBlock > end || e0 + kBlock - 1 > length - a.news;
-    bool broken = false;
-    if (edge) {
-      bool odd = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (e0 + entry_of(j) >= end) v.v[j] = (T)0.0f;
-#pragma unroll
-        for (int n = 0; n < W; ++n) odd |= !(fabsf((float)v.v[j][n]) < INFINITY);
-      }
-      broken = a.news > 1 && __any(odd);
-    }
+  for (int e0 = first; e0 < end; e0 += kStride) {
+    const bool more = e0 + kStride < end;
+    f32x4 z[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      f32x4 z[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+      z[t][0] = z[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) {
-        z[0] = mfma(k[0][i], q[t][i], z[0]);
-        z[1] = mfma(k[1][i], q[t][i], z[1]);
+        z[t][0] = mfma(k[0][i], q[t][i], z[t][0]);
+        z[t][1] = mfma(k[1][i], q[t][i], z[t][1]);
       }
+    }
+    if (more) {
+      const window_t w = entries(keys, a.ke, e0 + kStride, end, a.width);
+      key.load(w, 0, k[0]);
+      key.load(w, 16, k[1]);
+    }
+    // some row does not see some entry of the block
+    const bool edge = e0 + kBlock > end || e0 + kBlock - 1 > length - a.news;
+    // the weights go into the product in two parts, so they keep 16 bits or more of their mantissa there
+    pack_t<T> hi[NT], lo[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          z[u][i] *= a.scale_log2;
+          z[t][u][i] *= a.scale_log2;
           if (edge) {
             const int e = e0 + 16 * u + 4 * c + i;
-            if (e > limit[t] || e >= end) z[u][i] = -INFINITY;
+            if (e > limit[t] || e >= end) z[t][u][i] = -INFINITY;
           }
         }
       }
-      if (a.logits != nullptr && row0 + 16 * t + r < a.rows) {
+      if (!BY_ROWS && a.logits != nullptr && row0 + 16 * t + r < a.rows) {
         float *to = a.logits + (bh * a.rows + row0 + 16 * t + r) * a.logit_stride + e0 + 4 * c;
-        *reinterpret_cast<f32x4 *>(to) = z[0];
-        *reinterpret_cast<f32x4 *>(to + 16) = z[1];
+        *reinterpret_cast<f32x4 *>(to) = z[t][0];
+        *reinterpret_cast<f32x4 *>(to + 16) = z[t][1];
       }
-      float top = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
-                        fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
-      top = groups_max(top);
-      const float next = fmaxf(m[t], top);
-      if (__any(next > m[t])) {
+      float top = fmaxf(fmaxf(fmaxf(z[t][0][0], z[t][0][1]), fmaxf(z[t][0][2], z[t][0][3])),
+                        fmaxf(fmaxf(z[t][1][0], z[t][1][1]), fmaxf(z[t][1][2], z[t][1][3])));
+      if (__any(top > m[t])) {
+        const float next = fmaxf(m[t], groups_max(top));
         const float f = exp2_of(m[t], next);
         l[t] *= f;
 #pragma unroll
         for (int n = 0; n < W; ++n) o[t][n] *= f;
         m[t] = next;
       }
-      // the weights go into the product in two parts, so they keep 16 bits or more of their mantissa there
-      pack_t<T> hi, lo;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = exp2_of(z[u][i], m[t]);
+          const float p = exp2_of(z[t][u][i], m[t]);
           l[t] += p;
-          hi[4 * u + i] = (T)p;
-          lo[4 * u + i] = (T)(p - (float)hi[4 * u + i]);
+          hi[t][4 * u + i] = (T)p;
+          lo[t][4 * u + i] = (T)(p - (float)hi[t][4 * u + i]);
         }
       }
-      if (!broken) {
+    }
+    bool broken = false;
+    if (!ONE && edge) {
+      bool odd = false;
 #pragma unroll
-        for (int n = 0; n < W; ++n) {
-          const pack_t<T> col = v.column(n);
-          o[t][n] = mfma(col, hi, o[t][n]);
-          o[t][n] = mfma(col, lo, o[t][n]);
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int n = 0; n < W; ++n) odd |= !(fabsf((float)v.v[j][n]) < INFINITY);
+      }
+      broken = __any(odd);
+    }
+    if (ONE || !broken) {
+#pragma unroll
+      for (int n = 0; n < W; ++n) {
+        const pack_t<T> col = v.column(n);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          o[t][n] = mfma(col, hi[t], o[t][n]);
+          o[t][n] = mfma(col, lo[t], o[t][n]);
         }
-      } else {
-        // NaN or infinity among values that some row does not see: one new
-        // token at a time, what it does not see set to zero
-        for (int i = 0; i < a.news; ++i) {
-          const int sees = length - a.news + i;
-          const bool mine = (row0 + 16 * t + r) / a.group == i;
+      }
+    } else {
+      // NaN or infinity among values that some row does not see: the products
+      // take them as zero, and what each row does see of them is counted by
+      // products of ones and added after
+      const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+      pack_t<T> seen[NT];
 #pragma unroll
-          for (int n = 0; n < W; ++n) {
-            pack_t<T> col = v.column(n);
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (e0 + entry_of(j) > sees) col[j] = (T)0.0f;
-            f32x4 part = mfma(col, hi, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-            part = mfma(col, lo, part);
+        for (int j = 0; j < 8; ++j) {
+          const int e = e0 + entry_of(j);
+          seen[t][j] = (T)(e <= limit[t] && e < end ? 1.0f : 0.0f);
+        }
+      }
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (mine) o[t][n][x] += part[x];
+      for (int n = 0; n < W; ++n) {
+        pack_t<T> col = v.column(n), up, down, nan;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = (float)col[j];
+          up[j] = (T)(x == INFINITY ? 1.0f : 0.0f);
+          down[j] = (T)(x == -INFINITY ? 1.0f : 0.0f);
+          nan[j] = (T)(x != x ? 1.0f : 0.0f);
+          if (!(fabsf(x) < INFINITY)) col[j] = (T)0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          o[t][n] = mfma(col, hi[t], o[t][n]);
+          o[t][n] = mfma(col, lo[t], o[t][n]);
+          const f32x4 ups = mfma(up, seen[t], none), downs = mfma(down, seen[t], none), nans = mfma(nan, seen[t], none);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (ups[x] > 0.0f) o[t][n][x] += INFINITY;
+            if (downs[x] > 0.0f) o[t][n][x] -= INFINITY;
+            if (nans[x] > 0.0f) o[t][n][x] = NAN;
           }
         }
       }
     }
+    if (more) v.load(entries(values, a.ve, e0 + kStride, end, a.width), value_off, (int)a.ve * 2);
   }
 
+#pragma unroll
+  for (int t = 0; t < NT; ++t) l[t] = groups_sum(l[t]);
+  float *part = a.part_o + ((bh * a.splits + split) * a.rows + row0) * a.width;
+  if constexpr (BY_ROWS) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = 16 * t + r;
+      if (row >= rows_here) continue;
+      if (c == 0) {
+        ml[2 * row] = m[t];
+        ml[2 * row + 1] = l[t];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int n = 0; n < W; n += 4) {
+          const int d = (4 * c + i) * W + n;
+          if (EXACT || d < a.width)
+            *reinterpret_cast<f32x4 *>(part + (int64_t)row * a.width + d) =
+                f32x4{o[t][n][i], o[t][n + 1][i], o[t][n + 2][i], o[t][n + 3][i]};
+        }
+      }
+    }
+    return;
+  }
   // join the waves: a common maximum, then their sums in the waves' order
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    l[t] = groups_sum(l[t]);
     if (c == 0) {
       sh.m[wave][16 * t + r] = m[t];
       sh.l[wave][16 * t + r] = l[t];
@@ -287,8 +404,6 @@ __global__ __launch_bounds__(64 * kAttendWaves) void attend_kernel(const AttendA
 #pragma unroll
     for (int w = 0; w < kAttendWaves; ++w) all = fmaxf(all, sh.m[w][16 * t + r]);
     const float f = exp2_of(m[t], all);
-#pragma unroll
-    for (int n = 0; n < W; ++n) o[t][n] *= f;
     if (wave == 0 && c == 0 && 16 * t + r < rows_here) {
       float sum = 0.0f;
 #pragma unroll
@@ -296,69 +411,129 @@ __global__ __launch_bounds__(64 * kAttendWaves) void attend_kernel(const AttendA
       ml[2 * (16 * t + r)] = all;
       ml[2 * (16 * t + r) + 1] = sum;
     }
-  }
-  for (int w = 0; w < kAttendWaves; ++w) {
-    if (wave == w) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int n = 0; n < W; ++n) {
-            float *at = &sh.o[16 * t + r][(4 * c + i) * W + n];
-            *at = w == 0 ? o[t][n][i] : *at + o[t][n][i];
-          }
-        }
-      }
+      for (int n = 0; n < W; n += 4)
+        *reinterpret_cast<f32x4 *>(&sh.o[wave][16 * t + r][(4 * c + i) * W + n]) =
+            f32x4{o[t][n][i] * f, o[t][n + 1][i] * f, o[t][n + 2][i] * f, o[t][n + 3][i] * f};
     }
-    __syncthreads();
   }
-  float *part = a.part_o + ((bh * a.splits + split) * a.rows + row0) * a.width;
-  for (int i = threadIdx.x; i < rows_here * a.width; i += blockDim.x) part[i] = sh.o[i / a.width][i % a.width];
-}
-
-// lse of a row over the splits (in units of log2), and its inverse sum at maximum `top`
-LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float &top, float &sum) {
-  top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_ml[((bh * a.splits + s) * a.rows + row) * 2]);
-  sum = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float *ml = a.part_ml + ((bh * a.splits + s) * a.rows + row) * 2;
-    sum += exp2_of(ml[0], top) * ml[1];
+  __syncthreads();
+  const int packs = a.width / 4;  // the width is a multiple of 8
+  for (int i = threadIdx.x; i < rows_here * packs; i += blockDim.x) {
+    const int row = i / packs, d = (i % packs) * 4;
+    f32x4 sum = *reinterpret_cast<const f32x4 *>(&sh.o[0][row][d]);
+#pragma unroll
+    for (int w = 1; w < kAttendWaves; ++w) sum += *reinterpret_cast<const f32x4 *>(&sh.o[w][row][d]);
+    *reinterpret_cast<f32x4 *>(part + (int64_t)row * a.width + d) = sum;
   }
 }
 
-// out: one workgroup per 16 rows and cache; lse into the logits' place when they are formed again
+// The splits' maxima and sums of a row as one, by a team of 16 lanes: its
+// lse in units of log2 (+inf for a row that sees nothing, so its weights are 0).
+LDEV float row_lse(const AttendArgs &a, int64_t bh, int row) {
+  const int j = threadIdx.x % 16;
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + bh * a.splits * a.rows + row;
+  float top = -INFINITY, sum = 0.0f;
+  for (int s = j; s < a.splits; s += 16) {
+    const float2 x = ml[(int64_t)s * a.rows];
+    const float next = fmaxf(top, x.x);
+    sum = sum * exp2_of(top, next) + exp2_of(x.x, next) * x.y;
+    top = next;
+  }
+  const float all = team_max<16>(top);
+  sum = team_sum<16>(sum * exp2_of(top, all));
+  return sum > 0.0f ? all + log2f(sum) : (sum == 0.0f ? INFINITY : sum);
+}
+
+// out of one row: its parts, each weighed by its maximum, summed over the splits
+template <class T>
+LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
+  struct Shared {
+    float weight[256];
+    float top[4], sum[4];
+    f32x4 o[256];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  const int tid = threadIdx.x, wave = tid / 64;
+  // splits <= 256: one per thread
+  const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + bh * a.splits * a.rows + row;
+  float2 x = {-INFINITY, 0.0f};
+  if (tid < a.splits) x = ml[(int64_t)tid * a.rows];
+  float top = team_max<64>(x.x);
+  if (tid % 64 == 0) sh.top[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3]));
+  const float f = exp2_of(x.x, top);
+  sh.weight[tid] = f;
+  const float part = team_sum<64>(f * x.y);
+  if (tid % 64 == 0) sh.sum[wave] = part;
+  __syncthreads();
+  const float sum = sh.sum[0] + sh.sum[1] + sh.sum[2] + sh.sum[3];
+  if (lse != nullptr && tid == 0)
+    lse[bh * a.rows + row] = sum > 0.0f ? top + log2f(sum) : (sum == 0.0f ? INFINITY : sum);
+  // a thread takes 4 elements of every n-th split
+  const int packs = a.width / 4, teams = 256 / packs, team = tid / packs, d = (tid % packs) * 4;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (team < teams) {
+    const float *po = a.part_o + (bh * a.splits * a.rows + row) * a.width + d;
+    const int64_t step = (int64_t)a.rows * a.width;
+#pragma unroll 4
+    for (int s = team; s < a.splits; s += teams) {
+      const float w = sh.weight[s];
+      if (w != 0.0f) o += w * *reinterpret_cast<const f32x4 *>(po + s * step);  // an empty split has no part
+    }
+  }
+  sh.o[tid] = o;
+  __syncthreads();
+  if (team != 0) return;
+  for (int t = 1; t < teams; ++t) o += sh.o[t * packs + tid];
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  typedef T vec4 __attribute__((ext_vector_type(4)));
+  T *out = const_cast<T *>(query_row<T>(a, bh, row) - static_cast<const T *>(a.q) + static_cast<T *>(a.out));
+  *reinterpret_cast<vec4 *>(out + d) = vec4{(T)(o[0] * inv), (T)(o[1] * inv), (T)(o[2] * inv), (T)(o[3] * inv)};
+}
+
+constexpr int kAccountEntries = 1024;  // entries per workgroup of the kept logits' sums
+
+// The first a.rows workgroups of a cache join its rows; the others add up the
+// accounts of 1024 entries each from the kept logits:
+// account_out = account + sum over rows of 2^(z - lse).
 template <class T>
 __global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a, float *lse) {
   const int64_t bh = grid_row();
   if (bh >= (int64_t)a.batch * a.heads) return;
-  const int row = blockIdx.x;
-  float top, sum;
-  join_row(a, bh, row, top, sum);
-  if (lse != nullptr && threadIdx.x == 0) lse[bh * a.rows + row] = sum > 0.0f ? top + log2f(sum) : (sum == 0.0f ? INFINITY : sum);
-  T *out = const_cast<T *>(query_row<T>(a, bh, row) - static_cast<const T *>(a.q) + static_cast<T *>(a.out));
-  for (int d = threadIdx.x; d < a.width; d += blockDim.x) {
-    float o = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t at = (bh * a.splits + s) * a.rows + row;
-      const float m = a.part_ml[at * 2];
-      if (m != -INFINITY) o += exp2_of(m, top) * a.part_o[at * a.width + d];
-    }
-    out[d] = (T)(sum == 0.0f ? 0.0f : o / sum);
+  if ((int)blockIdx.x < a.rows) {
+    join_row<T>(a, bh, (int)blockIdx.x, lse);
+    return;
   }
-}
-
-// account_out = account + sum over rows of 2^(z - lse), z kept
-__global__ __launch_bounds__(256) void account_kept_kernel(const AttendArgs a, const float *lse) {
-  const int64_t bh = grid_row();
-  if (bh >= (int64_t)a.batch * a.heads) return;
-  const int e = blockIdx.x * 256 + threadIdx.x;
-  if (e >= length_of(a, bh)) return;
-  float w = 0.0f;
-  for (int row = 0; row < a.rows; ++row)
-    w += __builtin_amdgcn_exp2f(a.logits[(bh * a.rows + row) * a.logit_stride + e] - lse[bh * a.rows + row]);
-  a.account_out[bh * a.capacity + e] = a.account[bh * a.capacity + e] + w;
+  const int length = length_of(a, bh);
+  const int base = ((int)blockIdx.x - a.rows) * kAccountEntries;
+  if (base >= length) return;
+  struct Shared {
+    float lse[kKeepRows];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  const int row = threadIdx.x / 16;  // kKeepRows teams of 16 lanes
+  const float x = row < a.rows ? row_lse(a, bh, row) : INFINITY;
+  if (threadIdx.x % 16 == 0) sh.lse[row] = x;
+  __syncthreads();
+  const int e = base + 4 * (int)threadIdx.x;
+  if (e >= length) return;
+  f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float *z = a.logits + bh * a.rows * a.logit_stride + e;
+#pragma unroll 4
+  for (int i = 0; i < a.rows; ++i) {
+    const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * a.logit_stride);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) w[n] += __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    if (e + n < length) a.account_out[bh * a.capacity + e + n] = a.account[bh * a.capacity + e + n] + w[n];
 }
 
 // the same, z formed again: a wave takes 64 entries and goes through all rows
@@ -369,15 +544,17 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
   if (bh >= (int64_t)a.batch * a.heads) return;
   const int lane = threadIdx.x % 64, c = lane / 16, r = lane % 16;
   const int length = length_of(a, bh);
-  const int e0 = (blockIdx.x * 4 + threadIdx.x / 64) * 16 * KT;
+  const int e0 = (int)(blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64)) * 16 * KT;
   if (e0 >= length) return;
   const int64_t b = bh / a.heads, h = bh % a.heads;
   const T *keys = static_cast<const T *>(a.k) + b * a.kb + h * a.kh;
+  const Keys<T, DP, EXACT> key(a);
+  const window_t win = entries(keys, a.ke, e0, length, a.width);
   pack_t<T> k[KT][DP / 32];
   f32x4 w[KT];
 #pragma unroll
   for (int u = 0; u < KT; ++u) {
-    load_keys<T, DP, EXACT>(a, keys, e0 + 16 * u, length - 1, k[u]);
+    key.load(win, 16 * u, k[u]);
     w[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   for (int row0 = 0; row0 < a.rows; row0 += 16) {
@@ -409,34 +586,42 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
   }
 }
 
-template <class T, int DP, int NT, bool EXACT>
+template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE>
 hipError_t attend(const AttendArgs &a, hipStream_t s) {
   const int64_t caches = (int64_t)a.batch * a.heads;
-  const int row_blocks = (a.rows + 16 * NT - 1) / (16 * NT);
-  attend_kernel<T, DP, NT, EXACT>
+  const int per = 16 * NT * (BY_ROWS ? kAttendWaves : 1), row_blocks = (a.rows + per - 1) / per;
+  attend_kernel<T, DP, NT, EXACT, BY_ROWS, ONE>
       <<<rows_grid((unsigned)(a.splits * row_blocks), caches), dim3(64 * kAttendWaves), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // the rows' lse follows the parts' maxima and sums
-  float *lse = a.account_out == nullptr ? nullptr : a.part_ml + caches * a.splits * a.rows * 2;
-  attend_join_kernel<T><<<rows_grid((unsigned)a.rows, caches), dim3(256), 0, s>>>(a, lse);
+  const bool kept = a.logits != nullptr, formed = a.account_out != nullptr && !kept;
+  // the rows' lse, where the logits are formed again, follow the parts' maxima and sums
+  float *lse = formed ? a.part_ml + caches * a.splits * a.rows * 2 : nullptr;
+  const int64_t sums = kept ? (a.capacity + kAccountEntries - 1) / kAccountEntries : 0;
+  attend_join_kernel<T><<<rows_grid((unsigned)(a.rows + sums), caches), dim3(256), 0, s>>>(a, lse);
   e = hipGetLastError();
-  if (e != hipSuccess || lse == nullptr) return e;
-  if (a.logits != nullptr) {
-    account_kept_kernel<<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);
-  } else {
-    account_formed_kernel<T, DP, EXACT>
-        <<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);
-  }
+  if (e != hipSuccess || !formed) return e;
+  account_formed_kernel<T, DP, EXACT>
+      <<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);
   return hipGetLastError();
+}
+// 16 rows are one tile of the matrix instruction, 32 two that share the
+// entries (ONE: a single new token, whose row sees every entry); beyond, the waves take rows of their own.  32 rows of 256 elements would not
+// fit a wave's registers.
+template <class T, int DP, bool EXACT>
+hipError_t attend_rows(const AttendArgs &a, hipStream_t s) {
+  if (a.rows <= 16) {
+    return a.news == 1 ? attend<T, DP, 1, EXACT, false, true>(a, s) : attend<T, DP, 1, EXACT, false, false>(a, s);
+  }
+  if constexpr (DP <= 128) {
+    if (a.rows <= 32) return attend<T, DP, 2, EXACT, false, false>(a, s);
+    if (a.rows > 64) return attend<T, DP, 2, EXACT, true, false>(a, s);
+  }
+  return attend<T, DP, 1, EXACT, true, false>(a, s);
 }
 template <class T, int DP>
 hipError_t attend_width(const AttendArgs &a, hipStream_t s) {
-  const bool exact = a.width == DP;
-  if constexpr (DP <= 128) {  // 32 rows of 256 elements would not fit the registers
-    if (a.rows > 16) return exact ? attend<T, DP, 2, true>(a, s) : attend<T, DP, 2, false>(a, s);
-  }
-  return exact ? attend<T, DP, 1, true>(a, s) : attend<T, DP, 1, false>(a, s);
+  return a.width == DP ? attend_rows<T, DP, true>(a, s) : attend_rows<T, DP, false>(a, s);
 }
 template <class T>
 hipError_t attend_type(const AttendArgs &a, hipStream_t s) {
@@ -449,7 +634,9 @@ hipError_t attend_type(const AttendArgs &a, hipStream_t s) {
 
 AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t rows, int width, bool accounts) {
   AttendPlan p{};
-  const int64_t caches = batch * heads, rows_per = rows <= 16 || width > 128 ? 16 : 32;
+  const int64_t caches = batch * heads;
+  // rows per workgroup, as attend_rows() chooses them
+  const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)) : 64);
   const int64_t row_blocks = (rows + rows_per - 1) / rows_per;
   int64_t splits = (1024 + caches * row_blocks - 1) / (caches * row_blocks);
   const int64_t most = (capacity + kStep - 1) / kStep;

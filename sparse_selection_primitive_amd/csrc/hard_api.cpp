@@ -102,6 +102,9 @@ lapsum_status check_cache(const lapsum_cache *c) {
                              c->v_stride_batch, c->v_stride_head, c->v_stride_entry};
   for (int64_t s : strides)
     if (s < 0 || s % 8 != 0) return LAPSUM_ERR_LAYOUT;
+  // 64 entries lie within the 2^31 bytes that a buffer load's offset reaches
+  if (c->k_stride_entry > LAPSUM_MAX_ENTRY_STRIDE || c->v_stride_entry > LAPSUM_MAX_ENTRY_STRIDE)
+    return LAPSUM_ERR_LAYOUT;
   return LAPSUM_OK;
 }
 lapsum_status check_cache_pointers(const lapsum_cache *c) {

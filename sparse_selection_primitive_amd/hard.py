@@ -64,9 +64,14 @@ def declare(lib):
 
 
 # ----------------------------------------------------------------- checks
-def _dtype(x, name, only=None):
+@functools.lru_cache(maxsize=None)
+def _codes():
     torch = _torch()
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(x.dtype)
+    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _dtype(x, name, only=None):
+    code = _codes().get(x.dtype)
     if code is None or (only is not None and code not in only):
         kinds = "bfloat16 or float16" if only else "float32, bfloat16 or float16"
         raise LapsumError(f"{name} must be {kinds}")
@@ -86,7 +91,7 @@ def _gpu(x, name, dim=None, dev=None):
 def _array(x, name, dtype, shape, dev):
     """A contiguous device tensor of exactly this type and shape."""
     _gpu(x, name, dev=dev)
-    if x.dtype != dtype or tuple(x.shape) != tuple(shape):
+    if x.dtype != dtype or x.shape != shape:
         raise LapsumError(f"{name} must be {dtype} {list(shape)}")
     return x.contiguous()
 
@@ -96,35 +101,39 @@ def _out(x, name, dtype, shape, dev):
     if x is None:
         return _torch().empty(shape, dtype=dtype, device=dev)
     _gpu(x, name, dev=dev)
-    if x.dtype != dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous():
+    if x.dtype != dtype or x.shape != shape or not x.is_contiguous():
         raise LapsumError(f"{name} must be contiguous {dtype} {list(shape)}")
     return x
 
 
 def _rows(x, name):
-    """[tokens, n] with contiguous rows (any distance between them): (x, stride)."""
-    _gpu(x, name, 2)
-    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
-        x = x.contiguous()
-    return x, (x.stride(0) if x.shape[0] > 1 else x.shape[1])
+    """[tokens, n] with contiguous rows (any distance between them): (x, tokens, n, stride)."""
+    tokens, n = x.shape
+    stride, inner = x.stride()
+    if (inner != 1 and n > 1) or (stride < n and tokens > 1):
+        x, stride = x.contiguous(), n
+    return x, tokens, n, (stride if tokens > 1 else n)
 
 
-class _on:
-    """Makes a device current for the length of a call (nothing to do when it is)."""
+@functools.lru_cache(maxsize=None)
+def _stream_reader():
+    """device index -> the current stream's handle.  torch's raw reader takes 0.1 us, its stream object 1.9 us."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw if raw is not None else (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, dev):
-        torch = _torch()
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self.dev = dev
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _torch().cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(dev, name, *args):
+    """A library call on a device's current stream (every entry point takes the stream last)."""
+    f = getattr(load_library(), name)
+    index = dev.index
+    if index == _torch().cuda.current_device():
+        rc = f(*args, _stream_reader()(index))
+    else:
+        with _torch().cuda.device(dev):
+            rc = f(*args, _stream_reader()(index))
+    if rc:
+        _check(rc, name)
 
 
 # ---------------------------------------------------------------- routing
@@ -146,10 +155,9 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
     by their sum if renormalise, times scale.  A slot without an available
     expert holds -1 and weight 0.  out: (weights, chosen) to write into."""
     torch = _torch()
-    lib = load_library()
     code = _dtype(_gpu(logits, "logits", 2), "logits")
-    x, stride = _rows(logits, "logits")
-    (tokens, experts), dev = x.shape, x.device
+    x, tokens, experts, stride = _rows(logits, "logits")
+    dev = x.device
     opt = _route_options(int(k), score, int(groups), top_groups, renormalise, float(scale))
     if bias is not None:
         bias = _array(bias, "bias", torch.float32, (experts,), dev)
@@ -157,10 +165,8 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
     chosen = _out(None if out is None else out[1], "chosen", torch.int32, (tokens, opt.k), dev)
     if tokens == 0:
         return weights, chosen
-    with _on(dev) as stream:
-        _check(lib.lapsum_route_forward(x.data_ptr(), code, tokens, experts, stride,
-                                        None if bias is None else bias.data_ptr(), opt, weights.data_ptr(),
-                                        chosen.data_ptr(), stream), "lapsum_route_forward")
+    _call(dev, "lapsum_route_forward", x.data_ptr(), code, tokens, experts, stride,
+          None if bias is None else bias.data_ptr(), opt, weights.data_ptr(), chosen.data_ptr())
     return weights, chosen
 
 
@@ -168,20 +174,17 @@ def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=Tru
     """dlogits [tokens, experts], of the logits' type: the gradient of the weights, the choice held fixed
     (score, renormalise and scale as in the forward)."""
     torch = _torch()
-    lib = load_library()
     code = _dtype(_gpu(logits, "logits", 2), "logits")
-    x, stride = _rows(logits, "logits")
-    (tokens, experts), dev = x.shape, x.device
+    x, tokens, experts, stride = _rows(logits, "logits")
+    dev = x.device
     chosen = _array(_gpu(chosen, "chosen", 2), "chosen", torch.int32, (tokens, chosen.shape[1]), dev)
     dweights = _array(dweights, "dweights", torch.float32, chosen.shape, dev)
     opt = _route_options(chosen.shape[1], score, 1, 1, renormalise, float(scale))
     dlogits = _out(out, "dlogits", logits.dtype, (tokens, experts), dev)
     if tokens == 0:
         return dlogits
-    with _on(dev) as stream:
-        _check(lib.lapsum_route_backward(dweights.data_ptr(), x.data_ptr(), code, tokens, experts, stride,
-                                         chosen.data_ptr(), opt, dlogits.data_ptr(), stream),
-               "lapsum_route_backward")
+    _call(dev, "lapsum_route_backward", dweights.data_ptr(), x.data_ptr(), code, tokens, experts, stride,
+          chosen.data_ptr(), opt, dlogits.data_ptr())
     return dlogits
 
 
@@ -218,22 +221,19 @@ def dispatch_plan(chosen, experts):
     offsets int32 [experts + 1] (expert e's rows are offsets[e]:offsets[e + 1]), slot int32 [tokens, k] (a pair's row, -1
     for entries that name no expert) and order int32 [tokens * k] (the pair t * k + j of a row, -1 behind the last)."""
     torch = _torch()
-    lib = load_library()
     _gpu(chosen, "chosen", 2)
     (tokens, k), dev, experts = chosen.shape, chosen.device, int(experts)
     chosen = _array(chosen, "chosen", torch.int32, (tokens, k), dev)
     if tokens * k == 0:
         return (torch.zeros(experts + 1, dtype=torch.int32, device=dev), torch.empty_like(chosen),
                 torch.empty(0, dtype=torch.int32, device=dev))
-    # one allocation for the three small arrays
-    both = torch.empty(2 * tokens * k + experts + 1, dtype=torch.int32, device=dev)
-    slot, order, offsets = both[:tokens * k].view(tokens, k), both[tokens * k:2 * tokens * k], both[2 * tokens * k:]
-    with _on(dev) as stream:
-        ws, wptr, wlen = _workspace(_plan_bytes(tokens, k, experts), dev)
-        rc = lib.lapsum_dispatch_plan(chosen.data_ptr(), tokens, k, experts, offsets.data_ptr(), slot.data_ptr(),
-                                      order.data_ptr(), wptr, wlen, stream)
-        del ws
-        _check(rc, "lapsum_dispatch_plan")
+    slot = torch.empty_like(chosen)
+    order = torch.empty(tokens * k, dtype=torch.int32, device=dev)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    ws, wptr, wlen = _workspace(_plan_bytes(tokens, k, experts), dev)
+    _call(dev, "lapsum_dispatch_plan", chosen.data_ptr(), tokens, k, experts, offsets.data_ptr(), slot.data_ptr(),
+          order.data_ptr(), wptr, wlen)
+    del ws  # back to the pool, ordered after this call on its stream
     return offsets, slot, order
 
 
@@ -248,25 +248,21 @@ def _offsets_of(offsets, dev):
 
 def dispatch_forward(x, slot, offsets, *, out=None):
     """xs [tokens * k, width]: token rows in expert order, xs[slot[t, j]] = x[t] (rows behind the last pair zero)."""
-    lib = load_library()
     code = _dtype(_gpu(x, "x", 2), "x")
-    x, stride = _rows(x, "x")
-    (tokens, width), dev = x.shape, x.device
+    x, tokens, width, stride = _rows(x, "x")
+    dev = x.device
     slot, offsets = _slot_of(slot, dev, tokens), _offsets_of(offsets, dev)
     k = slot.shape[1]
     xs = _out(out, "xs", x.dtype, (tokens * k, width), dev)
     if xs.numel() == 0:
         return xs
-    with _on(dev) as stream:
-        _check(lib.lapsum_dispatch_forward(x.data_ptr(), code, tokens, k, width, stride, slot.data_ptr(),
-                                           offsets.data_ptr(), offsets.numel() - 1, xs.data_ptr(), stream),
-               "lapsum_dispatch_forward")
+    _call(dev, "lapsum_dispatch_forward", x.data_ptr(), code, tokens, k, width, stride, slot.data_ptr(),
+          offsets.data_ptr(), offsets.numel() - 1, xs.data_ptr())
     return xs
 
 
 def dispatch_backward(dxs, slot, *, out=None):
     """dx [tokens, width]: the sum of each token's rows of dxs."""
-    lib = load_library()
     code = _dtype(_gpu(dxs, "dxs", 2), "dxs")
     dev = dxs.device
     slot = _slot_of(slot, dev)
@@ -275,16 +271,13 @@ def dispatch_backward(dxs, slot, *, out=None):
     dx = _out(out, "dx", dxs.dtype, (tokens, width), dev)
     if dxs.numel() == 0:
         return dx.zero_()
-    with _on(dev) as stream:
-        _check(lib.lapsum_dispatch_backward(dxs.data_ptr(), code, tokens, k, width, slot.data_ptr(), dx.data_ptr(),
-                                            stream), "lapsum_dispatch_backward")
+    _call(dev, "lapsum_dispatch_backward", dxs.data_ptr(), code, tokens, k, width, slot.data_ptr(), dx.data_ptr())
     return dx
 
 
 def combine_forward(ys, slot, weights, *, out=None):
     """y [tokens, width]: y[t] = sum_j weights[t, j] ys[slot[t, j]]."""
     torch = _torch()
-    lib = load_library()
     code = _dtype(_gpu(ys, "ys", 2), "ys")
     dev = ys.device
     slot = _slot_of(slot, dev)
@@ -294,19 +287,17 @@ def combine_forward(ys, slot, weights, *, out=None):
     y = _out(out, "y", ys.dtype, (tokens, width), dev)
     if ys.numel() == 0:
         return y.zero_()
-    with _on(dev) as stream:
-        _check(lib.lapsum_combine_forward(ys.data_ptr(), code, tokens, k, width, slot.data_ptr(), weights.data_ptr(),
-                                          y.data_ptr(), stream), "lapsum_combine_forward")
+    _call(dev, "lapsum_combine_forward", ys.data_ptr(), code, tokens, k, width, slot.data_ptr(), weights.data_ptr(),
+          y.data_ptr())
     return y
 
 
 def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
     """dys [tokens * k, width] and dweights fp32 [tokens, k]: dys[slot] = w dy[t], dweights = <dy[t], ys[slot]>."""
     torch = _torch()
-    lib = load_library()
     code = _dtype(_gpu(dy, "dy", 2), "dy")
-    dy, stride = _rows(dy, "dy")
-    (tokens, width), dev = dy.shape, dy.device
+    dy, tokens, width, stride = _rows(dy, "dy")
+    dev = dy.device
     slot, offsets = _slot_of(slot, dev, tokens), _offsets_of(offsets, dev)
     k = slot.shape[1]
     ys = _array(ys, "ys", dy.dtype, (tokens * k, width), dev)
@@ -315,11 +306,9 @@ def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
     dweights = _out(None if out is None else out[1], "dweights", torch.float32, (tokens, k), dev)
     if ys.numel() == 0:
         return dys, dweights.zero_()
-    with _on(dev) as stream:
-        _check(lib.lapsum_combine_backward(dy.data_ptr(), stride, ys.data_ptr(), code, tokens, k, width,
-                                           slot.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-                                           offsets.numel() - 1, dys.data_ptr(), dweights.data_ptr(), stream),
-               "lapsum_combine_backward")
+    _call(dev, "lapsum_combine_backward", dy.data_ptr(), stride, ys.data_ptr(), code, tokens, k, width,
+          slot.data_ptr(), weights.data_ptr(), offsets.data_ptr(), offsets.numel() - 1, dys.data_ptr(),
+          dweights.data_ptr())
     return dys, dweights
 
 
@@ -391,7 +380,6 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     the entries up to lengths[b] - news + i).  account fp32 [batch, heads, capacity]: each entry's weight, summed over
     the new tokens and the query heads of its key head, is added to it, in place or into account_out.  scale: 1/sqrt(width) by default."""
     torch = _torch()
-    lib = load_library()
     cache = _cache_of(k, v)
     dev = k.device
     _gpu(q, "q", 4, dev)
@@ -411,16 +399,12 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
         raise LapsumError("account_out needs an account")
     if q.numel() == 0:
         return out
-    with _on(dev) as stream:
-        nbytes = _attend_bytes(cache.dtype, tuple(k.shape), news, q_heads, int(account is not None))
-        ws, wptr, wlen = _workspace(nbytes, dev)
-        rc = lib.lapsum_cache_attend(q.data_ptr(), cache, lengths.data_ptr(), news, q_heads,
-                                     width ** -0.5 if scale is None else float(scale),
-                                     None if account is None else account.data_ptr(),
-                                     None if account is None else account_out.data_ptr(), out.data_ptr(), wptr, wlen,
-                                     stream)
-        del ws
-        _check(rc, "lapsum_cache_attend")
+    nbytes = _attend_bytes(cache.dtype, tuple(k.shape), news, q_heads, int(account is not None))
+    ws, wptr, wlen = _workspace(nbytes, dev)
+    _call(dev, "lapsum_cache_attend", q.data_ptr(), cache, lengths.data_ptr(), news, q_heads,
+          width ** -0.5 if scale is None else float(scale), None if account is None else account.data_ptr(),
+          None if account is None else account_out.data_ptr(), out.data_ptr(), wptr, wlen)
+    del ws
     return out
 
 
@@ -441,7 +425,6 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
     Returns kept int32 [batch, heads, keep] (the slot each entry came from, -1 behind the last) and the new lengths
     (a new tensor)."""
     torch = _torch()
-    lib = load_library()
     cache = _cache_of(k, v)
     dev, batch, keep = k.device, k.shape[0], int(keep)
     shape = tuple(k.shape[:3])
@@ -456,14 +439,11 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
     lengths = _array(lengths, "lengths", torch.int32, (batch,), dev)
     if next_position is not None:
         next_position = _array(next_position, "next_position", torch.int32, (batch,), dev)
-    with _on(dev) as stream:
-        kept = torch.empty(shape[:2] + (max(keep, 0),), dtype=torch.int32, device=dev)
-        lengths_out = torch.empty_like(lengths)
-        ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, tuple(k.shape), keep), dev)
-        rc = lib.lapsum_cache_evict(cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,
-                                    None if next_position is None else next_position.data_ptr(), int(sinks),
-                                    int(recent), account_out.data_ptr(), positions_out.data_ptr(), kept.data_ptr(),
-                                    lengths_out.data_ptr(), wptr, wlen, stream)
-        del ws
-        _check(rc, "lapsum_cache_evict")
+    kept = torch.empty(shape[:2] + (max(keep, 0),), dtype=torch.int32, device=dev)
+    lengths_out = torch.empty_like(lengths)
+    ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, tuple(k.shape), keep), dev)
+    _call(dev, "lapsum_cache_evict", cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,
+          None if next_position is None else next_position.data_ptr(), int(sinks), int(recent),
+          account_out.data_ptr(), positions_out.data_ptr(), kept.data_ptr(), lengths_out.data_ptr(), wptr, wlen)
+    del ws
     return kept, lengths_out
