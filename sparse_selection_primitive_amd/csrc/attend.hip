@@ -26,10 +26,12 @@ namespace lapsum {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = 32;       // entries a wave takes at a time
 constexpr int kAttendWaves = 4;  // waves of a workgroup, taking its blocks in turn
 constexpr int kStep = kBlock * kAttendWaves;
+constexpr int kMaxSplits = 256;
 constexpr int kKeepRows = 16;    // up to this many rows the logits are kept for the accounts
 
 LDEV f32x4 mfma(pack_t<bf16> a, pack_t<bf16> b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -87,22 +89,32 @@ LDEV void load_queries(const AttendArgs &a, int64_t bh, int row, pack_t<T> (&q)[
 using window_t = __amdgpu_buffer_rsrc_t;
 LDEV window_t window_of(const void *first, int64_t bytes) {
   const int64_t most = 0x7FFFFFF0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0, (int)(bytes < most ? bytes : most),
-                                           0x00020000);  // 32-bit data format
+  bytes = bytes < 0 ? 0 : (bytes < most ? bytes : most);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0, (int)bytes, 0x00020000);  // 32-bit format
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
 
+// Values are read as streamed (not kept in the cache): 200001 entries in 154
+// us instead of 174.  Keys are not: a load touches 16 rows' half lines, and without the
+// cache the other halves are fetched again.
+constexpr int kCached = 0, kStreamed = 2;
+template <int AUX>
 LDEV uint4 load_16(window_t w, uint32_t lane_offset, int offset) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane_offset, offset, 0));
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane_offset, offset, AUX));
 }
 LDEV uint2 load_8(window_t w, uint32_t lane_offset, int offset) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane_offset, offset, 0));
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane_offset, offset, kStreamed));
 }
 
-// the entries [first, end) of keys or values
+LDEV void store_16(window_t w, uint32_t lane_offset, int offset, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), w, (int)lane_offset, offset, 0);
+}
+
+// the entries [first, end) of keys or values; none where first >= end
 template <class T>
 LDEV window_t entries(const T *base, int64_t stride, int first, int end, int width) {
-  return window_of(base + (int64_t)first * stride, ((int64_t)(end - 1 - first) * stride + width) * (int64_t)sizeof(T));
+  const int64_t bytes = ((int64_t)(end - 1 - first) * stride + width) * (int64_t)sizeof(T);
+  return window_of(base + (int64_t)first * stride, first < end ? bytes : 0);
 }
 
 // This lane's part of 16 keys (first factor of Z'): entry lane % 16 of the
@@ -126,7 +138,7 @@ struct Keys {
   LDEV void load(window_t w, int at, pack_t<T> (&k)[kSteps]) const {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      k[i] = __builtin_bit_cast(pack_t<T>, load_16(w, off[EXACT ? 0 : i] + i * 64, at * stride));
+      k[i] = __builtin_bit_cast(pack_t<T>, load_16<kCached>(w, off[EXACT ? 0 : i] + i * 64, at * stride));
   }
 };
 
@@ -145,15 +157,15 @@ struct Values {
   LDEV void load(window_t w, uint32_t off, int stride) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int at = ((j / 4) * 16 + j % 4) * stride;
+      const int at = __builtin_amdgcn_readfirstlane(((j / 4) * 16 + j % 4) * stride);  // a scalar offset
       if constexpr (W == 4) {
         v[j] = __builtin_bit_cast(vec, load_8(w, off, at));
       } else if constexpr (W == 8) {
-        v[j] = __builtin_bit_cast(vec, load_16(w, off, at));
+        v[j] = __builtin_bit_cast(vec, load_16<kStreamed>(w, off, at));
       } else {
         struct Two {
           uint4 x, y;
-        } two = {load_16(w, off, at), load_16(w, off + 16, at)};
+        } two = {load_16<kStreamed>(w, off, at), load_16<kStreamed>(w, off + 16, at)};
         v[j] = __builtin_bit_cast(vec, two);
       }
     }
@@ -175,7 +187,7 @@ struct Values {
 // waves are joined at the end) or its rows (BY_ROWS: every wave goes through
 // all the entries for rows of its own, and what one wave loads the others find in
 // the cache of their compute unit).
-template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE>
+template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE, bool KEEP>
 __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) void attend_kernel(const AttendArgs a) {
   constexpr int W = DP / 16;
   constexpr int kRows = 16 * NT;
@@ -212,17 +224,13 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
   const int first = begin + (BY_ROWS ? 0 : wave * kBlock);
 
   // a block's keys are asked for as soon as the last block's are used up, its
-  // values likewise, so each is on its way while the other is worked on
+  // values likewise, so each is on its way while the other is worked on (past the
+  // last block from an empty window: a branch here would make the compiler
+  // wait for the keys where only the values are needed)
   const Keys<T, DP, EXACT> key(a);
   const uint32_t value_off = Values<T, DP>::value_offset(a);
   pack_t<T> k[2][DP / 32];
   Values<T, DP> v;
-  if (first < end) {
-    const window_t w = entries(keys, a.ke, first, end, a.width);
-    key.load(w, 0, k[0]);
-    key.load(w, 16, k[1]);
-    v.load(entries(values, a.ve, first, end, a.width), value_off, (int)a.ve * 2);
-  }
   pack_t<T> q[NT][DP / 32];
   int limit[NT];  // the last entry this lane's row sees
 #pragma unroll
@@ -231,6 +239,16 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
     load_queries<T, DP>(a, bh, row, q[t]);
     limit[t] = length - a.news + row / a.group;
   }
+  // the order of the loads is the loop's: keys before values
+  __builtin_amdgcn_sched_barrier(0);
+  {
+    const window_t w = entries(keys, a.ke, first, end, a.width);
+    key.load(w, 0, k[0]);
+    key.load(w, 16, k[1]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  v.load(entries(values, a.ve, first, end, a.width), value_off, (int)a.ve * 2);
+  __builtin_amdgcn_sched_barrier(0);
 
   float m[NT], l[NT];
   f32x4 o[NT][W];
@@ -243,7 +261,6 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
   }
 
   for (int e0 = first; e0 < end; e0 += kStride) {
-    const bool more = e0 + kStride < end;
     f32x4 z[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -254,11 +271,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
         z[t][1] = mfma(k[1][i], q[t][i], z[t][1]);
       }
     }
-    if (more) {
-      const window_t w = entries(keys, a.ke, e0 + kStride, end, a.width);
-      key.load(w, 0, k[0]);
-      key.load(w, 16, k[1]);
-    }
+    const window_t next_keys = entries(keys, a.ke, e0 + kStride, end, a.width);
+    key.load(next_keys, 0, k[0]);
+    key.load(next_keys, 16, k[1]);
     // some row does not see some entry of the block
     const bool edge = e0 + kBlock > end || e0 + kBlock - 1 > length - a.news;
     // the weights go into the product in two parts, so they keep 16 bits or more of their mantissa there
@@ -270,16 +285,23 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           z[t][u][i] *= a.scale_log2;
-          if (edge) {
-            const int e = e0 + 16 * u + 4 * c + i;
-            if (e > limit[t] || e >= end) z[t][u][i] = -INFINITY;
-          }
         }
       }
-      if (!BY_ROWS && a.logits != nullptr && row0 + 16 * t + r < a.rows) {
-        float *to = a.logits + (bh * a.rows + row0 + 16 * t + r) * a.logit_stride + e0 + 4 * c;
-        *reinterpret_cast<f32x4 *>(to) = z[t][0];
-        *reinterpret_cast<f32x4 *>(to + 16) = z[t][1];
+      if (edge) {
+        const int most = min(limit[t], end - 1) - e0 - 4 * c;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * u + i > most) z[t][u][i] = -INFINITY;
+        }
+      }
+      if constexpr (KEEP) {  // rows past the last one go nowhere; no branch, so the waits for the loads stay exact
+        const window_t to = window_of(a.logits + (bh * a.blocks + e0 / kBlock) * a.rows * kBlock,
+                                      (int64_t)a.rows * kBlock * (int64_t)sizeof(float));
+        const int at = ((row0 + 16 * t + r) * kBlock + 4 * c) * (int)sizeof(float);
+        store_16(to, (uint32_t)at, 0, z[t][0]);
+        store_16(to, (uint32_t)at, 64, z[t][1]);
       }
       float top = fmaxf(fmaxf(fmaxf(z[t][0][0], z[t][0][1]), fmaxf(z[t][0][2], z[t][0][3])),
                         fmaxf(fmaxf(z[t][1][0], z[t][1][1]), fmaxf(z[t][1][2], z[t][1][3])));
@@ -361,7 +383,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
         }
       }
     }
-    if (more) v.load(entries(values, a.ve, e0 + kStride, end, a.width), value_off, (int)a.ve * 2);
+    v.load(entries(values, a.ve, e0 + kStride, end, a.width), value_off, (int)a.ve * 2);
   }
 
 #pragma unroll
@@ -448,39 +470,42 @@ LDEV float row_lse(const AttendArgs &a, int64_t bh, int row) {
 }
 
 // out of one row: its parts, each weighed by its maximum, summed over the splits
-template <class T>
+template <class T, int TH>
 LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   struct Shared {
-    float weight[256];
-    float top[4], sum[4];
-    f32x4 o[256];
+    float weight[TH];
+    float top[TH / 64], sum[TH / 64];
+    f32x4 o[TH];
   };
   __shared__ Shared sh;
   lds_poison(sh);
   const int tid = threadIdx.x, wave = tid / 64;
-  // splits <= 256: one per thread
+  static_assert(kMaxSplits <= TH, "one split per thread");
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + bh * a.splits * a.rows + row;
   float2 x = {-INFINITY, 0.0f};
   if (tid < a.splits) x = ml[(int64_t)tid * a.rows];
   float top = team_max<64>(x.x);
   if (tid % 64 == 0) sh.top[wave] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3]));
+#pragma unroll
+  for (int w = 0; w < TH / 64; ++w) top = fmaxf(top, sh.top[w]);
   const float f = exp2_of(x.x, top);
   sh.weight[tid] = f;
   const float part = team_sum<64>(f * x.y);
   if (tid % 64 == 0) sh.sum[wave] = part;
   __syncthreads();
-  const float sum = sh.sum[0] + sh.sum[1] + sh.sum[2] + sh.sum[3];
+  float sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < TH / 64; ++w) sum += sh.sum[w];
   if (lse != nullptr && tid == 0)
     lse[bh * a.rows + row] = sum > 0.0f ? top + log2f(sum) : (sum == 0.0f ? INFINITY : sum);
   // a thread takes 4 elements of every n-th split
-  const int packs = a.width / 4, teams = 256 / packs, team = tid / packs, d = (tid % packs) * 4;
+  const int packs = a.width / 4, teams = TH / packs, team = tid / packs, d = (tid % packs) * 4;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   if (team < teams) {
     const float *po = a.part_o + (bh * a.splits * a.rows + row) * a.width + d;
     const int64_t step = (int64_t)a.rows * a.width;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = team; s < a.splits; s += teams) {
       const float w = sh.weight[s];
       if (w != 0.0f) o += w * *reinterpret_cast<const f32x4 *>(po + s * step);  // an empty split has no part
@@ -496,38 +521,38 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   *reinterpret_cast<vec4 *>(out + d) = vec4{(T)(o[0] * inv), (T)(o[1] * inv), (T)(o[2] * inv), (T)(o[3] * inv)};
 }
 
-constexpr int kAccountEntries = 1024;  // entries per workgroup of the kept logits' sums
-
 // The first a.rows workgroups of a cache join its rows; the others add up the
-// accounts of 1024 entries each from the kept logits:
+// accounts of 4 entries a thread from the kept logits:
 // account_out = account + sum over rows of 2^(z - lse).
-template <class T>
-__global__ __launch_bounds__(256) void attend_join_kernel(const AttendArgs a, float *lse) {
+template <class T, int TH>
+__global__ __launch_bounds__(TH) void attend_join_kernel(const AttendArgs a, float *lse) {
   const int64_t bh = grid_row();
   if (bh >= (int64_t)a.batch * a.heads) return;
   if ((int)blockIdx.x < a.rows) {
-    join_row<T>(a, bh, (int)blockIdx.x, lse);
+    join_row<T, TH>(a, bh, (int)blockIdx.x, lse);
     return;
   }
   const int length = length_of(a, bh);
-  const int base = ((int)blockIdx.x - a.rows) * kAccountEntries;
+  const int base = ((int)blockIdx.x - a.rows) * (4 * TH);
   if (base >= length) return;
   struct Shared {
     float lse[kKeepRows];
   };
   __shared__ Shared sh;
   lds_poison(sh);
-  const int row = threadIdx.x / 16;  // kKeepRows teams of 16 lanes
-  const float x = row < a.rows ? row_lse(a, bh, row) : INFINITY;
-  if (threadIdx.x % 16 == 0) sh.lse[row] = x;
+  const int row = threadIdx.x / 16;  // a team of 16 lanes each
+  if (row < a.rows) {
+    const float x = row_lse(a, bh, row);
+    if (threadIdx.x % 16 == 0) sh.lse[row] = x;
+  }
   __syncthreads();
   const int e = base + 4 * (int)threadIdx.x;
   if (e >= length) return;
   f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
-  const float *z = a.logits + bh * a.rows * a.logit_stride + e;
+  const float *z = a.logits + (bh * a.blocks + e / kBlock) * a.rows * kBlock + e % kBlock;
 #pragma unroll 4
   for (int i = 0; i < a.rows; ++i) {
-    const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * a.logit_stride);
+    const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
 #pragma unroll
     for (int n = 0; n < 4; ++n) w[n] += __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
   }
@@ -586,20 +611,26 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
   }
 }
 
-template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE>
+template <class T, int TH>
+hipError_t join(const AttendArgs &a, float *lse, hipStream_t s) {
+  const int64_t sums = a.logits != nullptr ? (a.capacity + 4 * TH - 1) / (4 * TH) : 0;
+  attend_join_kernel<T, TH>
+      <<<rows_grid((unsigned)(a.rows + sums), (int64_t)a.batch * a.heads), dim3(TH), 0, s>>>(a, lse);
+  return hipGetLastError();
+}
+
+template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE, bool KEEP>
 hipError_t attend(const AttendArgs &a, hipStream_t s) {
   const int64_t caches = (int64_t)a.batch * a.heads;
   const int per = 16 * NT * (BY_ROWS ? kAttendWaves : 1), row_blocks = (a.rows + per - 1) / per;
-  attend_kernel<T, DP, NT, EXACT, BY_ROWS, ONE>
+  attend_kernel<T, DP, NT, EXACT, BY_ROWS, ONE, KEEP>
       <<<rows_grid((unsigned)(a.splits * row_blocks), caches), dim3(64 * kAttendWaves), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool kept = a.logits != nullptr, formed = a.account_out != nullptr && !kept;
   // the rows' lse, where the logits are formed again, follow the parts' maxima and sums
   float *lse = formed ? a.part_ml + caches * a.splits * a.rows * 2 : nullptr;
-  const int64_t sums = kept ? (a.capacity + kAccountEntries - 1) / kAccountEntries : 0;
-  attend_join_kernel<T><<<rows_grid((unsigned)(a.rows + sums), caches), dim3(256), 0, s>>>(a, lse);
-  e = hipGetLastError();
+  e = a.splits > 16 ? join<T, 512>(a, lse, s) : join<T, 256>(a, lse, s);
   if (e != hipSuccess || !formed) return e;
   account_formed_kernel<T, DP, EXACT>
       <<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);
@@ -610,14 +641,17 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
 // fit a wave's registers.
 template <class T, int DP, bool EXACT>
 hipError_t attend_rows(const AttendArgs &a, hipStream_t s) {
+  const bool keep = a.logits != nullptr;  // at most 16 rows
   if (a.rows <= 16) {
-    return a.news == 1 ? attend<T, DP, 1, EXACT, false, true>(a, s) : attend<T, DP, 1, EXACT, false, false>(a, s);
+    if (a.news == 1)
+      return keep ? attend<T, DP, 1, EXACT, false, true, true>(a, s) : attend<T, DP, 1, EXACT, false, true, false>(a, s);
+    return keep ? attend<T, DP, 1, EXACT, false, false, true>(a, s) : attend<T, DP, 1, EXACT, false, false, false>(a, s);
   }
   if constexpr (DP <= 128) {
-    if (a.rows <= 32) return attend<T, DP, 2, EXACT, false, false>(a, s);
-    if (a.rows > 64) return attend<T, DP, 2, EXACT, true, false>(a, s);
+    if (a.rows <= 32) return attend<T, DP, 2, EXACT, false, false, false>(a, s);
+    if (a.rows > 64) return attend<T, DP, 2, EXACT, true, false, false>(a, s);
   }
-  return attend<T, DP, 1, EXACT, true, false>(a, s);
+  return attend<T, DP, 1, EXACT, true, false, false>(a, s);
 }
 template <class T, int DP>
 hipError_t attend_width(const AttendArgs &a, hipStream_t s) {
@@ -632,23 +666,30 @@ hipError_t attend_type(const AttendArgs &a, hipStream_t s) {
 
 }  // namespace
 
-AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t rows, int width, bool accounts) {
+AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t rows, bool one, int width,
+                       bool accounts) {
   AttendPlan p{};
   const int64_t caches = batch * heads;
   // rows per workgroup, as attend_rows() chooses them
   const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)) : 64);
-  const int64_t row_blocks = (rows + rows_per - 1) / rows_per;
-  int64_t splits = (1024 + caches * row_blocks - 1) / (caches * row_blocks);
+  const int64_t groups = caches * ((rows + rows_per - 1) / rows_per);
+  // Workgroups over all.  768 fit the chip at once (three a compute unit), and
+  // one round of them is best where their shares are equal: one sequence of 200001 entries takes
+  // 132 us, in three rounds 145.  Sequences of several lengths need a finer grain: 64 of
+  // 512 to 8192 entries take 188 us in three rounds, 196 in one.  With more than 32 rows one
+  // workgroup fills a compute unit.
+  const int64_t wanted = rows > 32 ? 512 : (batch > 1 && one ? 2304 : 768);
+  int64_t splits = (wanted + groups - 1) / groups;
   const int64_t most = (capacity + kStep - 1) / kStep;
   if (splits > most) splits = most;
-  if (splits > 128) splits = 128;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   if (splits < 1) splits = 1;
   p.splits = (int)splits;
   p.keep_logits = accounts && rows <= kKeepRows;
-  p.logit_stride = (capacity + kBlock - 1) / kBlock * kBlock;
+  p.blocks = (capacity + kBlock - 1) / kBlock;
   p.part_o = (size_t)(caches * splits * rows) * width * sizeof(float);
   p.part_ml = (size_t)(caches * splits * rows) * 2 * sizeof(float) + (size_t)(caches * rows) * sizeof(float);
-  p.logits = p.keep_logits ? (size_t)(caches * rows) * p.logit_stride * sizeof(float) : 0;
+  p.logits = p.keep_logits ? (size_t)(caches * rows) * p.blocks * kBlock * sizeof(float) : 0;
   return p;
 }
 

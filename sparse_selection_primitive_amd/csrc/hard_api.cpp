@@ -228,7 +228,7 @@ size_t lapsum_cache_attend_workspace_bytes(const lapsum_cache *cache, int64_t ne
                                            int32_t accounts) {
   if (check_attend(cache, news, q_heads) != LAPSUM_OK) return 0;
   return attend_bytes(attend_plan(cache->batch, cache->heads, cache->capacity, news * (q_heads / cache->heads),
-                                  cache->width, accounts != 0));
+                                  news == 1, cache->width, accounts != 0));
 }
 
 lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, const int32_t *lengths, int64_t news,
@@ -242,8 +242,8 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
   if (st != LAPSUM_OK) return st;
   if (!aligned(q, 16) || !aligned(out, 16)) return LAPSUM_ERR_LAYOUT;
   const int64_t group = q_heads / cache->heads, rows = news * group;
-  const AttendPlan p = attend_plan(cache->batch, cache->heads, cache->capacity, rows, cache->width,
-                                   account != nullptr);
+  const AttendPlan p = attend_plan(cache->batch, cache->heads, cache->capacity, rows, news == 1,
+                                   cache->width, account != nullptr);
   st = check_workspace(workspace, workspace_bytes, attend_bytes(p));
   if (st != LAPSUM_OK) return st;
   char *ws = static_cast<char *>(workspace);
@@ -273,7 +273,7 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float *>(ws + aligned_up(p.part_o));
   a.logits = p.keep_logits ? reinterpret_cast<float *>(ws + aligned_up(p.part_o) + aligned_up(p.part_ml)) : nullptr;
-  a.logit_stride = p.logit_stride;
+  a.blocks = p.blocks;
   (void)hipGetLastError();
   return done(launch_attend(a, cache->dtype, reinterpret_cast<hipStream_t>(stream)));
 }

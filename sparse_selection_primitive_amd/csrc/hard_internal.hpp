@@ -67,16 +67,17 @@ struct AttendArgs {
   void *out;
   float *part_o;                   // [batch * heads][splits][rows][width]
   float *part_ml;                  // [batch * heads][splits][rows][2]
-  float *logits;                   // [batch * heads][rows][logit_stride], or NULL: formed again
-  int64_t logit_stride;
+  float *logits;                   // [batch * heads][blocks][rows][32], or NULL: formed again
+  int64_t blocks;                  // of 32 entries
 };
 struct AttendPlan {
   int splits;
   bool keep_logits;
-  int64_t logit_stride;
+  int64_t blocks;
   size_t part_o, part_ml, logits;  // bytes
 };
-AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t rows, int width, bool accounts);
+AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t rows, bool one, int width,
+                       bool accounts);
 hipError_t launch_attend(const AttendArgs &a, int dtype, hipStream_t s);
 
 // evict.hip
