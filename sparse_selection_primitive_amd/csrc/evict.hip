@@ -7,6 +7,15 @@
 // sorted.  The survivors in front of slot `keep` stay where they are and those
 // behind it fill the holes in front, so the bytes moved are those of the
 // entries behind the budget that survive, not those of the budget.
+//
+// Slots in order, let before(i) be the number of survivors before slot i and F the
+// number of those in front of slot keep.  A hole at slot i is the
+// (i - before(i))-th, a survivor behind the budget the (before(i) - F)-th, so
+// one scan of the survivors ranks both.
+//
+// Rows of up to 16384 entries: one workgroup holds the row's keys in its
+// registers, so the accounts are read once.  Longer rows: tiles of 4096
+// entries on as many workgroups, one launch a digit, joined by counts.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -15,11 +24,13 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / 64;
-constexpr int kMoveSlots = 256;  // slots per workgroup of the move
+constexpr int kRowMax = 16384;  // entries of a row that one workgroup holds
+constexpr int kFewMoves = 64;   // up to this many entries the selecting workgroup moves itself
+constexpr int kMoveSlots = 256;
 
-LDEV int64_t evict_length(const EvictArgs &a, int64_t row) {
+LDEV int evict_length(const EvictArgs &a, int64_t row) {
   const int64_t n = a.lengths[row / a.heads];
-  return n < 0 ? 0 : (n > a.capacity ? a.capacity : n);
+  return (int)(n < 0 ? 0 : (n > a.capacity ? a.capacity : n));
 }
 
 struct RowKeys {
@@ -46,131 +57,260 @@ LDEV RowKeys row_keys(const EvictArgs &a, int64_t row) {
   return k;
 }
 
-// exclusive count of `flag` over the workgroup's threads; `all` the total
-LDEV int count_before(bool flag, int *waves, int &all) {
-  const unsigned long long m = __ballot(flag);
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  if (lane == 0) waves[wave] = __popcll(m);
-  __syncthreads();
-  int before = __popcll(m & ((1ull << lane) - 1ull));
-  all = 0;
-  for (int w = 0; w < kSelectWaves; ++w) {
-    if (w < wave) before += waves[w];
-    all += waves[w];
+// One entry's keys and values from slot `src` to slot `to`, 16 bytes a lane
+// (`lane` of a.entry_bytes / 16).
+struct Mover {
+  char *k, *v;
+  int64_t ke, ve;  // bytes
+  LDEV Mover(const EvictArgs &a, int64_t row) {
+    const int64_t b = row / a.heads, h = row % a.heads;
+    k = static_cast<char *>(a.k) + (b * a.kb + h * a.kh) * 2;
+    v = static_cast<char *>(a.v) + (b * a.vb + h * a.vh) * 2;
+    ke = a.ke * 2;
+    ve = a.ve * 2;
   }
-  __syncthreads();
-  return before;
+  LDEV void move(int64_t src, int64_t to, int lane) const {
+    const int64_t at = (int64_t)lane * 16;
+    const uint4 x = *reinterpret_cast<const uint4 *>(k + src * ke + at);
+    const uint4 y = *reinterpret_cast<const uint4 *>(v + src * ve + at);
+    *reinterpret_cast<uint4 *>(k + to * ke + at) = x;
+    *reinterpret_cast<uint4 *>(v + to * ve + at) = y;
+  }
+};
+
+// From a histogram of 2^BITS bins (LDS), the bin in which the want-th entry
+// from the top lies, by one wave: bin and the number wanted inside it.
+template <int BITS>
+LDEV void find_bin(const uint32_t *hist, uint32_t want, uint32_t *bin, uint32_t *inside) {
+  constexpr int PER = (1 << BITS) / 64;
+  const int lane = threadIdx.x % 64;
+  uint32_t sum = 0;
+#pragma unroll
+  for (int x = 0; x < PER; ++x) sum += hist[(1 << BITS) - 1 - (lane * PER + x)];
+  uint32_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const uint32_t u = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += u;
+  }
+  uint32_t above = inc - sum;
+  if (above < want && want <= inc) {
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+      const uint32_t b = (1 << BITS) - 1 - (lane * PER + x), n = hist[b];
+      if (above < want && want <= above + n) {
+        *bin = b;
+        *inside = want - above;
+      }
+      above += n;
+    }
+  }
 }
 
-// kept[0 .. keep): one workgroup per cache row.  holes: scratch [rows][keep].
-__global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(const EvictArgs a, int32_t *holes) {
+// ----------------------------------------------------- rows in registers
+// V entries a thread: entry v * 1024 + thread.
+template <int V>
+__global__ __launch_bounds__(kSelectThreads) void evict_row_kernel(const EvictArgs a, const bool move_here) {
   struct Shared {
     uint32_t hist[256];
-    int waves[kSelectWaves];
-    uint32_t prefix;
-    uint32_t want;  // how many entries of the keys that begin with `prefix` stay
+    int count[V * kSelectWaves];    // per round and wave, then the counts before
+    unsigned long long worst[kSelectWaves];
+    uint32_t prefix, want;
+    int total;
+    int32_t movers[V * kSelectThreads / 2];
+    int32_t holes[kFewMoves];
   };
   __shared__ Shared sh;
   lds_poison(sh);
   const int64_t row = grid_row();
   if (row >= a.batch * a.heads) return;
-  const int tid = threadIdx.x;
-  const int64_t n = evict_length(a, row), keep = a.keep;
-  int32_t *kept = a.kept + row * keep;
-  for (int64_t i = tid; i < keep; i += kSelectThreads) kept[i] = i < n ? (int32_t)i : -1;
-  if (n <= keep) return;
-  holes += row * keep;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int n = evict_length(a, row), keep = (int)a.keep, after = n < keep ? n : keep;
+  int32_t *kept = a.kept + row * a.keep;
   const RowKeys keys = row_keys(a, row);
+  const int64_t base = row * a.capacity;
+  const bool apart = a.account_out != a.account || a.positions_out != a.positions;
+  if (tid == 0 && row % a.heads == 0) a.lengths_out[row / a.heads] = after;
 
-  uint32_t prefix = 0, want = (uint32_t)keep;
+  if (n <= keep) {
+    for (int i = tid; i < keep; i += kSelectThreads) {
+      kept[i] = i < n ? i : -1;
+      if (i < n && apart) {
+        a.account_out[base + i] = a.account[base + i];
+        a.positions_out[base + i] = a.positions[base + i];
+      }
+    }
+    return;
+  }
+  uint32_t k[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = v * kSelectThreads + tid;
+    k[v] = i < n ? keys.key(i) : 0u;
+  }
+
+  if (n == keep + 1) {
+    // one entry leaves: the smallest key, of equal ones the highest slot
+    unsigned long long worst = ~0ull;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint32_t i = (uint32_t)(v * kSelectThreads + tid);
+      if ((int)i < n) {
+        const unsigned long long x = ((unsigned long long)k[v] << 32) | (0xFFFFFFFFu - i);
+        worst = x < worst ? x : worst;
+      }
+    }
+    worst = wave_reduce(worst, [](unsigned long long x, unsigned long long y) { return x < y ? x : y; });
+    if (lane == 0) sh.worst[wave] = worst;
+    __syncthreads();
+    worst = sh.worst[0];
+#pragma unroll
+    for (int w = 1; w < kSelectWaves; ++w) worst = sh.worst[w] < worst ? sh.worst[w] : worst;
+    const int hole = (int)(0xFFFFFFFFu - (uint32_t)worst);  // == keep: the last entry itself leaves
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = v * kSelectThreads + tid;
+      if (i >= keep) continue;
+      const int from = i == hole ? keep : i;
+      kept[i] = from;
+      if (apart || from != i) {
+        a.account_out[base + i] = a.account[base + from];
+        a.positions_out[base + i] = a.positions[base + from];
+      }
+    }
+    if (hole < keep && tid < a.entry_bytes / 16) Mover(a, row).move(keep, hole, tid);
+    return;
+  }
+
+  uint32_t prefix = 0, want = (uint32_t)keep, equal = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
     if (tid < 256) sh.hist[tid] = 0;
     __syncthreads();
     const uint32_t high = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int64_t i = tid; i < n; i += kSelectThreads) {
-      const uint32_t k = keys.key(i);
-      if ((k & high) == prefix) atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (v * kSelectThreads + tid < n && (k[v] & high) == prefix) atomicAdd(&sh.hist[(k[v] >> shift) & 255u], 1u);
     }
     __syncthreads();
-    if (tid < 64) {  // bins from the top: lane l holds bins 255 - 4l .. 252 - 4l
-      uint32_t v[4], sum = 0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) sum += v[x] = sh.hist[255 - 4 * tid - x];
-      uint32_t inc = sum;
-#pragma unroll
-      for (int o = 1; o < 64; o *= 2) {
-        const uint32_t u = __shfl_up(inc, o, 64);
-        if (tid >= o) inc += u;
-      }
-      uint32_t above = inc - sum;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (above < want && want <= above + v[x]) {
-          sh.prefix = prefix | ((uint32_t)(255 - 4 * tid - x) << shift);
-          sh.want = want - above;
-        }
-        above += v[x];
-      }
-    }
+    if (wave == 0) find_bin<8>(sh.hist, want, &sh.prefix, &sh.want);
     __syncthreads();
-    prefix = sh.prefix;
+    equal = sh.hist[sh.prefix];
+    prefix |= sh.prefix << shift;
     want = sh.want;
     __syncthreads();
   }
 
-  // slots in ascending order: of the entries with exactly the key `prefix` the first `want` stay
-  int64_t same = 0, moved = 0;
-  for (int64_t base = 0; base < n; base += kSelectThreads) {
-    const int64_t i = base + tid;
-    const uint32_t k = i < n ? keys.key(i) : 0u;
-    int all;
-    const bool equal = i < n && k == prefix;
-    const int64_t rank = same + count_before(equal, sh.waves, all);
-    same += all;
-    const bool stays = i < n && (k > prefix || (equal && rank < (int64_t)want));
-    const bool hole = i < keep && !stays, mover = i >= keep && stays;
-    // a tile can hold both: the holes lie in front, and their number is not needed with the movers'
-    const int h = count_before(hole, sh.waves, all);
-    const int holes_here = all;
-    if (hole) holes[moved + h] = (int32_t)i;
-    if (base < keep) moved += holes_here;
-    if (base + kSelectThreads >= keep) {
-      if (base < keep) {  // the last tile with holes: from here on `moved` counts movers
-        __syncthreads();
-        moved = 0;
+  // counts before each round and wave; the scan's total in sh.total
+  const auto scan = [&]() {
+    __syncthreads();
+    if (wave == 0) {
+      constexpr int PER = (V * kSelectWaves + 63) / 64;
+      int own[PER], sum = 0;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int at = lane * PER + x;
+        own[x] = at < V * kSelectWaves ? sh.count[at] : 0;
+        sum += own[x];
       }
-      const int m = count_before(mover, sh.waves, all);
-      if (mover) kept[holes[moved + m]] = (int32_t)i;
-      moved += all;
+      int inc = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o *= 2) {
+        const int u = __shfl_up(inc, o, 64);
+        if (lane >= o) inc += u;
+      }
+      int before = inc - sum;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int at = lane * PER + x;
+        if (at < V * kSelectWaves) sh.count[at] = before;
+        before += own[x];
+      }
     }
+    __syncthreads();
+  };
+  const unsigned long long below = (1ull << lane) - 1ull;
+
+  // stays: bit v of a mask
+  uint32_t stays = 0;
+  if (equal != want) {  // some of the entries with exactly the last key leave: rank them by slot
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const unsigned long long m = __ballot(v * kSelectThreads + tid < n && k[v] == prefix);
+      if (lane == 0) sh.count[v * kSelectWaves + wave] = __popcll(m);
+    }
+    scan();
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = v * kSelectThreads + tid;
+    bool s = i < n && k[v] >= prefix;
+    if (equal != want) {
+      const bool same = i < n && k[v] == prefix;
+      const unsigned long long m = __ballot(same);
+      const uint32_t rank = (uint32_t)(sh.count[v * kSelectWaves + wave] + __popcll(m & below));
+      if (same && rank >= want) s = false;
+    }
+    stays |= s ? 1u << v : 0u;
+  }
+  __syncthreads();
+  if (tid == 0) sh.total = 0;
+  int behind = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool s = ((stays >> v) & 1u) != 0;
+    const unsigned long long m = __ballot(s);
+    if (lane == 0) sh.count[v * kSelectWaves + wave] = __popcll(m);
+    behind += __popcll(__ballot(s && v * kSelectThreads + tid >= keep));
+  }
+  __syncthreads();
+  if (lane == 0 && behind != 0) atomicAdd(&sh.total, behind);
+  scan();
+  const int front = keep - sh.total;  // survivors in front of slot keep
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = v * kSelectThreads + tid;
+    const bool s = ((stays >> v) & 1u) != 0;
+    const int before = sh.count[v * kSelectWaves + wave] + __popcll(__ballot(s) & below);
+    if (s && i >= keep) sh.movers[before - front] = i;  // fewer than n - keep and keep, so at most half of the row
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = v * kSelectThreads + tid;
+    const bool s = ((stays >> v) & 1u) != 0;
+    const int before = sh.count[v * kSelectWaves + wave] + __popcll(__ballot(s) & below);
+    if (i >= keep) continue;
+    const int from = s ? i : sh.movers[i - before];
+    kept[i] = from;
+    if (apart || from != i) {
+      a.account_out[base + i] = a.account[base + from];
+      a.positions_out[base + i] = a.positions[base + from];
+    }
+    if (!s && move_here) sh.holes[i - before] = i;
+  }
+  if (!move_here) return;  // the same for the whole launch
+  __syncthreads();
+  const Mover mover(a, row);
+  const int packs = a.entry_bytes / 16, teams = 64 / packs, team = lane / packs;
+  if (team < teams) {
+    for (int m = wave * teams + team; m < sh.total; m += kSelectWaves * teams)
+      mover.move(sh.movers[m], sh.holes[m], lane % packs);
   }
 }
 
-// The survivors' accounts and positions, and the keys and values of those that move.
+// The keys and values of the entries that move, from `kept`: a wave takes 64 slots.
 __global__ __launch_bounds__(256) void evict_move_kernel(const EvictArgs a) {
   const int64_t row = grid_row();
   if (row >= a.batch * a.heads) return;
-  const int64_t n = evict_length(a, row);
-  const int64_t after = n < a.keep ? n : a.keep;
-  const int64_t base = (int64_t)blockIdx.x * kMoveSlots;
-  const int64_t i = base + threadIdx.x;
-  const int64_t b = row / a.heads, h = row % a.heads;
-  if (base == 0 && h == 0 && threadIdx.x == 0) a.lengths_out[b] = (int32_t)after;
-  if (base >= after) return;
-  int from = -1;
-  if (i < after) {
-    from = a.kept[row * a.keep + i];
-    a.account_out[row * a.capacity + i] = a.account[row * a.capacity + from];
-    a.positions_out[row * a.capacity + i] = a.positions[row * a.capacity + from];
-    if (from == (int)i) from = -1;
-  }
-  // each wave moves its own 64 slots' entries: 16 bytes a lane and entry
+  const int n = evict_length(a, row), after = n < a.keep ? n : (int)a.keep;
+  const int64_t i = (int64_t)blockIdx.x * kMoveSlots + threadIdx.x;
+  if (n <= a.keep) return;
+  const int from = i < after ? a.kept[row * a.keep + i] : -1;
   const int lane = threadIdx.x % 64;
   const int packs = a.entry_bytes / 16, team = lane / packs, teams = 64 / packs;
-  char *k = static_cast<char *>(a.k) + (b * a.kb + h * a.kh) * 2;
-  char *v = static_cast<char *>(a.v) + (b * a.vb + h * a.vh) * 2;
-  const int64_t first = base + (threadIdx.x / 64) * 64;
-  unsigned long long todo = __ballot(from >= 0);
+  const Mover mover(a, row);
+  const int64_t first = i - lane;
+  unsigned long long todo = __ballot(from >= 0 && from != (int)i);
   while (todo != 0) {
     // the next `teams` entries, one per team
     int mine = -1;
@@ -180,29 +320,386 @@ __global__ __launch_bounds__(256) void evict_move_kernel(const EvictArgs a) {
       if (t == team) mine = bit;
     }
     const int src = __shfl(from, mine < 0 ? 0 : mine, 64);
-    if (mine >= 0) {
-      const int64_t at = (int64_t)(lane % packs) * 16, to = first + mine;
-      const uint4 x = *reinterpret_cast<const uint4 *>(k + (int64_t)src * a.ke * 2 + at);
-      const uint4 y = *reinterpret_cast<const uint4 *>(v + (int64_t)src * a.ve * 2 + at);
-      *reinterpret_cast<uint4 *>(k + to * a.ke * 2 + at) = x;
-      *reinterpret_cast<uint4 *>(v + to * a.ve * 2 + at) = y;
+    if (mine >= 0) mover.move(src, first + mine, lane % packs);
+  }
+}
+
+// ------------------------------------------------------------ long rows
+// Tiles of a row: those of the slots in front of `keep`, then those behind.
+constexpr int kTileThreads = 256;
+constexpr int kTileRounds = 16;
+constexpr int kTileMin = kTileThreads * kTileRounds;
+constexpr int kMaxTiles = 256;  // of either part; one thread each where they are summed up
+
+struct Tiles {
+  int size, front, count;  // entries per tile; tiles in front of keep; tiles
+};
+Tiles tiles_of(int64_t capacity, int64_t keep) {
+  const int64_t longest = keep > capacity - keep ? keep : capacity - keep;
+  int64_t size = (longest + kMaxTiles / 2 - 1) / (kMaxTiles / 2);
+  size = (size + kTileMin - 1) / kTileMin * kTileMin;
+  Tiles t;
+  t.size = (int)size;
+  t.front = (int)((keep + size - 1) / size);
+  t.count = t.front + (int)((capacity - keep + size - 1) / size);
+  return t;
+}
+
+struct LongRow {  // a row's state in the workspace
+  uint32_t prefix[3], want[3];  // after each digit: the key's digits so far, and how many of those stay
+  int32_t moves;
+  int32_t pad;
+};
+struct LongArgs {
+  EvictArgs e;
+  Tiles t;
+  LongRow *state;      // [rows]
+  uint32_t *hist;      // [rows][3][2048]
+  int2 *counts;        // [rows][tiles]: entries above the key, entries that hold it
+  int32_t *holes, *movers;  // [rows][limit]
+  int64_t limit;       // most entries that can move
+};
+constexpr int kDigits = 3;
+constexpr int kBins = 2048;
+LDEV int digit_shift(int d) { return d == 0 ? 21 : (d == 1 ? 10 : 0); }
+LDEV uint32_t digit_mask(int d) { return d == 2 ? 1023u : 2047u; }
+
+LDEV void tile_range(const LongArgs &a, int n, int tile, int &begin, int &end) {
+  const int keep = (int)a.e.keep;
+  const int64_t first = tile < a.t.front ? (int64_t)tile * a.t.size : keep + (int64_t)(tile - a.t.front) * a.t.size;
+  const int64_t stop = tile < a.t.front ? keep : n;
+  begin = (int)first;
+  end = (int)(first + a.t.size < stop ? first + a.t.size : stop);
+}
+
+// What is wanted of digit d - 1's bin, by the whole workgroup (>= 64 threads); hist: 2048 words of LDS.
+LDEV void settle_digit(const LongArgs &a, int64_t row, int d, uint32_t *hist, uint32_t *found, uint32_t &prefix,
+                       uint32_t &want) {
+  prefix = 0;
+  want = (uint32_t)a.e.keep;
+  if (d == 0) return;
+  if (d > 1) {
+    prefix = a.state[row].prefix[d - 2];
+    want = a.state[row].want[d - 2];
+  }
+  const uint32_t *from = a.hist + (row * kDigits + d - 1) * kBins;
+  for (int i = threadIdx.x; i < kBins; i += blockDim.x) hist[i] = from[i];
+  __syncthreads();
+  if (threadIdx.x < 64) find_bin<11>(hist, want, &found[0], &found[1]);
+  __syncthreads();
+  prefix |= found[0] << digit_shift(d - 1);
+  want = found[1];
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.state[row].prefix[d - 1] = prefix;
+    a.state[row].want[d - 1] = want;
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(256) void evict_clear_kernel(uint32_t *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+// Digit d of the keys that begin with the digits found so far.
+__global__ __launch_bounds__(kTileThreads) void evict_digit_kernel(const LongArgs a, const int d) {
+  struct Shared {
+    uint32_t hist[kBins];
+    uint32_t found[2];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  const int64_t row = grid_row();
+  if (row >= a.e.batch * a.e.heads) return;
+  const int n = evict_length(a.e, row);
+  if (n <= a.e.keep) return;
+  uint32_t prefix, want;
+  settle_digit(a, row, d, sh.hist, sh.found, prefix, want);
+  for (int i = threadIdx.x; i < kBins; i += kTileThreads) sh.hist[i] = 0;
+  __syncthreads();
+  const RowKeys keys = row_keys(a.e, row);
+  int begin, end;
+  tile_range(a, n, blockIdx.x, begin, end);
+  const int shift = digit_shift(d);
+  const uint32_t mask = digit_mask(d), high = d == 0 ? 0u : ~((mask << shift) | ((1u << shift) - 1u));
+#pragma unroll 4
+  for (int i = begin + (int)threadIdx.x; i < end; i += kTileThreads) {
+    const uint32_t k = keys.key(i);
+    if ((k & high) == prefix) atomicAdd(&sh.hist[(k >> shift) & mask], 1u);
+  }
+  __syncthreads();
+  uint32_t *to = a.hist + (row * kDigits + d) * kBins;
+  for (int i = threadIdx.x; i < kBins; i += kTileThreads)
+    if (sh.hist[i] != 0) atomicAdd(&to[i], sh.hist[i]);
+}
+
+LDEV int block_sum(int v, int *waves) {
+  v = wave_reduce(v, [](int x, int y) { return x + y; });
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) waves[threadIdx.x / 64] = v;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 64; ++w) sum += waves[w];
+  return sum;
+}
+// exclusive sum of v over the threads; `all` the total
+LDEV int block_before(int v, int *waves, int &all) {
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int u = __shfl_up(inc, o, 64);
+    if ((int)(threadIdx.x % 64) >= o) inc += u;
+  }
+  __syncthreads();
+  if (threadIdx.x % 64 == 63) waves[threadIdx.x / 64] = inc;
+  __syncthreads();
+  int before = inc - v;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 64; ++w) {
+    if (w < (int)(threadIdx.x / 64)) before += waves[w];
+    all += waves[w];
+  }
+  return before;
+}
+
+// Entries above the last key, and entries that hold it, of each tile.
+__global__ __launch_bounds__(kTileThreads) void evict_count_kernel(const LongArgs a) {
+  struct Shared {
+    uint32_t hist[kBins];
+    uint32_t found[2];
+    int waves[kTileThreads / 64];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  const int64_t row = grid_row();
+  if (row >= a.e.batch * a.e.heads) return;
+  const int n = evict_length(a.e, row);
+  if (n <= a.e.keep) return;
+  uint32_t key, want;
+  settle_digit(a, row, kDigits, sh.hist, sh.found, key, want);
+  const RowKeys keys = row_keys(a.e, row);
+  int begin, end, above = 0, same = 0;
+  tile_range(a, n, blockIdx.x, begin, end);
+#pragma unroll 4
+  for (int i = begin + (int)threadIdx.x; i < end; i += kTileThreads) {
+    const uint32_t k = keys.key(i);
+    above += k > key ? 1 : 0;
+    same += k == key ? 1 : 0;
+  }
+  above = block_sum(above, sh.waves);
+  same = block_sum(same, sh.waves);
+  if (threadIdx.x == 0) a.counts[row * a.t.count + blockIdx.x] = int2{above, same};
+}
+
+// Ranks of the holes and of the survivors that fill them; the accounts and
+// positions of the entries that stay where they are.
+__global__ __launch_bounds__(kTileThreads) void evict_place_kernel(const LongArgs a) {
+  struct Shared {
+    int waves[kTileThreads / 64];
+    int pre[kMaxTiles];
+  };
+  __shared__ Shared sh;
+  lds_poison(sh);
+  const int64_t row = grid_row();
+  if (row >= a.e.batch * a.e.heads) return;
+  const int tid = threadIdx.x, tile = blockIdx.x;
+  const int n = evict_length(a.e, row), keep = (int)a.e.keep, after = n < keep ? n : keep;
+  int32_t *kept = a.e.kept + row * a.e.keep;
+  const int64_t base = row * a.e.capacity;
+  const bool apart = a.e.account_out != a.e.account || a.e.positions_out != a.e.positions;
+  if (tile == 0 && tid == 0) {
+    if (row % a.e.heads == 0) a.e.lengths_out[row / a.e.heads] = after;
+    if (n <= keep) a.state[row].moves = 0;
+  }
+  if (n <= keep) {
+    if (tile >= a.t.front) return;
+    const int64_t first = (int64_t)tile * a.t.size, stop = first + a.t.size < keep ? first + a.t.size : keep;
+    for (int64_t i = first + tid; i < stop; i += kTileThreads) {
+      kept[i] = i < n ? (int32_t)i : -1;
+      if (i < n && apart) {
+        a.e.account_out[base + i] = a.e.account[base + i];
+        a.e.positions_out[base + i] = a.e.positions[base + i];
+      }
+    }
+    return;
+  }
+  const uint32_t key = a.state[row].prefix[kDigits - 1];
+  const int want = (int)a.state[row].want[kDigits - 1];
+  // tiles' survivors: entries above the key, and of those that hold it the first `want` of the row
+  int all;
+  const int2 mine = tid < a.t.count ? a.counts[row * a.t.count + tid] : int2{0, 0};
+  const int same_before = block_before(mine.y, sh.waves, all);
+  int left = want - same_before;
+  left = left < 0 ? 0 : (left < mine.y ? left : mine.y);
+  const int stay = mine.x + left;
+  const int stay_before = block_before(stay, sh.waves, all);
+  const int front = block_sum(tid < a.t.front ? stay : 0, sh.waves);
+  __syncthreads();
+  if (tid == tile) {
+    sh.pre[0] = same_before;
+    sh.pre[1] = stay_before;
+  }
+  __syncthreads();
+  int same_at = sh.pre[0], stay_at = sh.pre[1];
+  if (tile == 0 && tid == 0) a.state[row].moves = keep - front;
+
+  const RowKeys keys = row_keys(a.e, row);
+  int begin, end;
+  tile_range(a, n, tile, begin, end);
+  const int lane = tid % 64, wave = tid / 64;
+  const unsigned long long below = (1ull << lane) - 1ull;
+  for (int at = begin; at < end; at += kTileThreads) {
+    const int i = at + tid;
+    const uint32_t k = i < end ? keys.key(i) : 0u;
+    const bool same = i < end && k == key;
+    // both counts of a wave in one word
+    const unsigned long long ms = __ballot(same), mg = __ballot(i < end && k > key);
+    __syncthreads();
+    if (lane == 0) sh.waves[wave] = __popcll(ms) | (__popcll(mg) << 16);
+    __syncthreads();
+    int same_b = same_at + __popcll(ms & below), above_b = __popcll(mg & below), same_all = 0, above_all = 0;
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 64; ++w) {
+      const int x = sh.waves[w];
+      if (w < wave) {
+        same_b += x & 0xFFFF;
+        above_b += x >> 16;
+      }
+      same_all += x & 0xFFFF;
+      above_all += x >> 16;
+    }
+    // survivors before this slot: those above the key, and the holders of the key among the first `want`
+    const int holders = (same_b < want ? same_b : want) - (same_at < want ? same_at : want);
+    const int before = stay_at + above_b + holders;
+    const bool s = i < end && (k > key || (same && same_b < want));
+    if (i < end) {
+      if (tile < a.t.front) {
+        if (s) {
+          kept[i] = i;
+          if (apart) {
+            a.e.account_out[base + i] = a.e.account[base + i];
+            a.e.positions_out[base + i] = a.e.positions[base + i];
+          }
+        } else {
+          a.holes[row * a.limit + i - before] = i;
+        }
+      } else if (s) {
+        a.movers[row * a.limit + before - front] = i;
+      }
+    }
+    const int same_next = same_at + same_all;
+    stay_at += above_all + (same_next < want ? same_next : want) - (same_at < want ? same_at : want);
+    same_at = same_next;
+  }
+}
+
+// The entries that move, a team of lanes each.
+__global__ __launch_bounds__(256) void evict_fill_kernel(const LongArgs a) {
+  const int64_t row = grid_row();
+  if (row >= a.e.batch * a.e.heads) return;
+  const int moves = a.state[row].moves;
+  const int lane = threadIdx.x % 64;
+  const int packs = a.e.entry_bytes / 16, teams = 64 / packs, team = lane / packs;
+  if (team >= teams) return;
+  const Mover mover(a.e, row);
+  const int64_t base = row * a.e.capacity;
+  const int step = (int)gridDim.x * 4 * teams;
+  for (int m = ((int)blockIdx.x * 4 + (int)threadIdx.x / 64) * teams + team; m < moves; m += step) {
+    const int to = a.holes[row * a.limit + m], src = a.movers[row * a.limit + m];
+    mover.move(src, to, lane % packs);
+    if (lane % packs == 0) {
+      a.e.kept[row * a.e.keep + to] = src;
+      a.e.account_out[base + to] = a.e.account[base + src];
+      a.e.positions_out[base + to] = a.e.positions[base + src];
     }
   }
+}
+
+struct LongLayout {
+  size_t state, hist, counts, holes, movers, bytes;
+  int64_t limit;
+};
+LongLayout long_layout(int64_t rows, int64_t capacity, int64_t keep) {
+  const Tiles t = tiles_of(capacity, keep);
+  LongLayout l;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  l.limit = keep < capacity - keep ? keep : capacity - keep;
+  if (l.limit < 1) l.limit = 1;
+  l.state = take((size_t)rows * sizeof(LongRow));
+  l.hist = take((size_t)rows * kDigits * kBins * sizeof(uint32_t));
+  l.counts = take((size_t)rows * t.count * sizeof(int2));
+  l.holes = take((size_t)(rows * l.limit) * sizeof(int32_t));
+  l.movers = take((size_t)(rows * l.limit) * sizeof(int32_t));
+  l.bytes = at;
+  return l;
+}
+
+hipError_t evict_long(const EvictArgs &e, hipStream_t s) {
+  const int64_t rows = e.batch * e.heads;
+  const LongLayout l = long_layout(rows, e.capacity, e.keep);
+  char *ws = static_cast<char *>(e.workspace);
+  LongArgs a;
+  a.e = e;
+  a.t = tiles_of(e.capacity, e.keep);
+  a.state = reinterpret_cast<LongRow *>(ws + l.state);
+  a.hist = reinterpret_cast<uint32_t *>(ws + l.hist);
+  a.counts = reinterpret_cast<int2 *>(ws + l.counts);
+  a.holes = reinterpret_cast<int32_t *>(ws + l.holes);
+  a.movers = reinterpret_cast<int32_t *>(ws + l.movers);
+  a.limit = l.limit;
+  const int64_t words = rows * kDigits * kBins, blocks = (words + 1023) / 1024;
+  evict_clear_kernel<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s>>>(a.hist, words);
+  hipError_t err = hipGetLastError();
+  const dim3 grid = rows_grid((unsigned)a.t.count, rows), threads(kTileThreads);
+  for (int d = 0; d < kDigits && err == hipSuccess; ++d) {
+    evict_digit_kernel<<<grid, threads, 0, s>>>(a, d);
+    err = hipGetLastError();
+  }
+  if (err != hipSuccess) return err;
+  evict_count_kernel<<<grid, threads, 0, s>>>(a);
+  err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  evict_place_kernel<<<grid, threads, 0, s>>>(a);
+  err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  // about 8 entries a team, on 4096 workgroups at most over all rows
+  const int64_t per = 4 * (64 / (e.entry_bytes / 16)) * 8;
+  int64_t fill = (a.limit + per - 1) / per, most = 4096 / rows;
+  if (most < 1) most = 1;
+  if (fill > most) fill = most;
+  evict_fill_kernel<<<rows_grid((unsigned)fill, rows), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int V>
+hipError_t evict_rows(const EvictArgs &a, hipStream_t s) {
+  const int64_t rows = a.batch * a.heads, limit = a.keep < a.capacity - a.keep ? a.keep : a.capacity - a.keep;
+  const bool here = limit <= kFewMoves;
+  evict_row_kernel<V><<<rows_grid(1, rows), dim3(kSelectThreads), 0, s>>>(a, here);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || here) return e;
+  evict_move_kernel<<<rows_grid((unsigned)((a.keep + kMoveSlots - 1) / kMoveSlots), rows), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 size_t evict_workspace(int64_t batch, int64_t heads, int64_t capacity, int64_t keep) {
-  return (size_t)(batch * heads) * (size_t)keep * sizeof(int32_t);
+  return capacity > kRowMax ? long_layout(batch * heads, capacity, keep).bytes : 0;
 }
 
 hipError_t launch_evict(const EvictArgs &a, hipStream_t s) {
-  const int64_t rows = a.batch * a.heads;
-  evict_select_kernel<<<rows_grid(1, rows), dim3(kSelectThreads), 0, s>>>(a, static_cast<int32_t *>(a.workspace));
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  evict_move_kernel<<<rows_grid((unsigned)((a.keep + kMoveSlots - 1) / kMoveSlots), rows), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+  if (a.capacity > kRowMax) return evict_long(a, s);
+  if (a.capacity <= 2 * kSelectThreads) return evict_rows<2>(a, s);
+  if (a.capacity <= 5 * kSelectThreads) return evict_rows<5>(a, s);
+  if (a.capacity <= 8 * kSelectThreads) return evict_rows<8>(a, s);
+  return evict_rows<16>(a, s);
 }
 
 }  // namespace lapsum

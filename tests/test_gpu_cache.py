@@ -310,9 +310,15 @@ def test_evict_accounts(L, kind, capacity, keep):
 def test_evict_long_row(L):
     """131072 entries to a quarter, and one over the budget, against a sort."""
     g = torch.Generator().manual_seed(6)
-    for lengths, keep in (([130001, 131072], 32768), ([131072, 131000], 131071)):
+    for lengths, keep, kind in (([130001, 131072], 32768, ""), ([131072, 131000], 131071, ""),
+                                ([131072, 70000], 65536, "few"), ([100000, 20], 4096, "equal"),
+                                ([131072, 131072], 9, "few"), ([131072, 4097], 4096, "")):
         s = 131072
         a = torch.exp(2 * torch.randn(2, 1, s, generator=g)).cuda()
+        if kind == "few":
+            a = a.ceil().clamp(max=5.0)
+        elif kind == "equal":
+            a[:] = 1.0
         p = torch.arange(s, dtype=torch.int32).expand(2, 1, s).contiguous().cuda()
         k, v = (x.cuda() for x in cache(2, 1, s, 16, "bf16", seed=9))
         k0, v0 = k.clone(), v.clone()
@@ -325,7 +331,7 @@ def test_evict_long_row(L):
             got = kept[b, 0, :m].long()
             assert torch.equal(torch.sort(got).values, torch.sort(top).values)
             stay = got[got < m]
-            assert torch.equal(stay, torch.nonzero(got < m)[:, 0])
+            assert torch.equal(stay, torch.nonzero(got < m)[:, 0]) and (kept[b, 0, m:] == -1).all()
             moved = got[got >= m]
             assert torch.equal(moved, torch.sort(moved).values)
             assert torch.equal(k[b, 0, :m], k0[b, 0][got]) and torch.equal(v[b, 0, :m], v0[b, 0][got])

@@ -132,9 +132,11 @@ def test_evict_checks(lib):
     for bad in (dict(ke=56), dict(ve=0), dict(kh=0), dict(vb=0), dict(k=P + 8)):
         assert call(cache(**bad)) == LAYOUT, bad
     assert call(cache(dtype=hard.F32)) == OPTION and call(None) == NULL
-    need = lib.lapsum_cache_evict_workspace_bytes(c, 10)
-    assert need > 0 and lib.lapsum_cache_evict_workspace_bytes(c, 101) == 0
-    assert call(c, nbytes=need - 1) == WORKSPACE and call(c, ws=None) == NULL
+    assert lib.lapsum_cache_evict_workspace_bytes(c, 10) == 0  # short rows need none
+    long = cache(capacity=100000, kh=6400000, kb=12800000, vh=6400000, vb=12800000)
+    need = lib.lapsum_cache_evict_workspace_bytes(long, 10)
+    assert need > 0 and lib.lapsum_cache_evict_workspace_bytes(long, 100001) == 0
+    assert call(long, nbytes=need - 1) == WORKSPACE and call(long, ws=None) == NULL
 
 
 def test_no_cpu_path():
