@@ -326,8 +326,8 @@ __global__ __launch_bounds__(256) void evict_move_kernel(const EvictArgs a) {
 
 // ------------------------------------------------------------ long rows
 // Tiles of a row: those of the slots in front of `keep`, then those behind.
-constexpr int kTileThreads = 256;
-constexpr int kTileRounds = 16;
+constexpr int kTileThreads = 1024;
+constexpr int kTileRounds = 4;
 constexpr int kTileMin = kTileThreads * kTileRounds;
 constexpr int kMaxTiles = 256;  // of either part; one thread each where they are summed up
 
