@@ -22,9 +22,13 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import LapsumError, _check, _torch, _workspace, load_library
+from . import LapsumError, _check, _workspace, load_library
 
 F32, BF16, F16 = 0, 1, 2
+# bound by the first call: the package can be imported without torch
+torch = None
+_TYPES, _FUNCTIONS = {}, {}
+_raw_stream = None
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
 
@@ -63,15 +67,20 @@ def declare(lib):
         f.restype, f.argtypes = res, args
 
 
+def _bind():
+    global torch, _raw_stream
+    import torch as t
+    load_library()
+    _TYPES.update({t.float32: F32, t.bfloat16: BF16, t.float16: F16})
+    # torch's raw reader of the current stream takes 0.1 us, its stream object 1.9 us
+    raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = raw if raw is not None else (lambda index: t.cuda.current_stream(index).cuda_stream)
+    torch = t
+
+
 # ----------------------------------------------------------------- checks
-@functools.lru_cache(maxsize=None)
-def _codes():
-    torch = _torch()
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-
-
 def _dtype(x, name, only=None):
-    code = _codes().get(x.dtype)
+    code = _TYPES.get(x.dtype)
     if code is None or (only is not None and code not in only):
         kinds = "bfloat16 or float16" if only else "float32, bfloat16 or float16"
         raise LapsumError(f"{name} must be {kinds}")
@@ -79,7 +88,10 @@ def _dtype(x, name, only=None):
 
 
 def _gpu(x, name, dim=None, dev=None):
-    if not isinstance(x, _torch().Tensor) or not x.is_cuda:
+    """A GPU tensor (of `dim` dimensions, on `dev`).  The first check of every entry point."""
+    if torch is None:
+        _bind()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise LapsumError(f"{name} must be a GPU tensor (no CPU path exists)")
     if dim is not None and x.dim() != dim:
         raise LapsumError(f"{name} must have {dim} dimensions")
@@ -90,17 +102,19 @@ def _gpu(x, name, dim=None, dev=None):
 
 def _array(x, name, dtype, shape, dev):
     """A contiguous device tensor of exactly this type and shape."""
-    _gpu(x, name, dev=dev)
+    if not isinstance(x, torch.Tensor) or x.device != dev:
+        _gpu(x, name, None, dev)
     if x.dtype != dtype or x.shape != shape:
         raise LapsumError(f"{name} must be {dtype} {list(shape)}")
-    return x.contiguous()
+    return x if x.is_contiguous() else x.contiguous()
 
 
 def _out(x, name, dtype, shape, dev):
     """An output: the caller's tensor (used as it is, so it must be contiguous), or a new one."""
     if x is None:
-        return _torch().empty(shape, dtype=dtype, device=dev)
-    _gpu(x, name, dev=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(x, torch.Tensor) or x.device != dev:
+        _gpu(x, name, None, dev)
     if x.dtype != dtype or x.shape != shape or not x.is_contiguous():
         raise LapsumError(f"{name} must be contiguous {dtype} {list(shape)}")
     return x
@@ -115,23 +129,17 @@ def _rows(x, name):
     return x, tokens, n, (stride if tokens > 1 else n)
 
 
-@functools.lru_cache(maxsize=None)
-def _stream_reader():
-    """device index -> the current stream's handle.  torch's raw reader takes 0.1 us, its stream object 1.9 us."""
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw if raw is not None else (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
 def _call(dev, name, *args):
     """A library call on a device's current stream (every entry point takes the stream last)."""
-    f = getattr(load_library(), name)
+    f = _FUNCTIONS.get(name)
+    if f is None:
+        f = _FUNCTIONS[name] = getattr(load_library(), name)
     index = dev.index
-    if index == _torch().cuda.current_device():
-        rc = f(*args, _stream_reader()(index))
+    if index == torch.cuda.current_device():
+        rc = f(*args, _raw_stream(index))
     else:
-        with _torch().cuda.device(dev):
-            rc = f(*args, _stream_reader()(index))
+        with torch.cuda.device(dev):
+            rc = f(*args, _raw_stream(index))
     if rc:
         _check(rc, name)
 
@@ -154,7 +162,6 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
     by default); the weights are the chosen scores (without the bias), divided
     by their sum if renormalise, times scale.  A slot without an available
     expert holds -1 and weight 0.  out: (weights, chosen) to write into."""
-    torch = _torch()
     code = _dtype(_gpu(logits, "logits", 2), "logits")
     x, tokens, experts, stride = _rows(logits, "logits")
     dev = x.device
@@ -173,7 +180,6 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
 def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=True, scale=1.0, out=None):
     """dlogits [tokens, experts], of the logits' type: the gradient of the weights, the choice held fixed
     (score, renormalise and scale as in the forward)."""
-    torch = _torch()
     code = _dtype(_gpu(logits, "logits", 2), "logits")
     x, tokens, experts, stride = _rows(logits, "logits")
     dev = x.device
@@ -191,7 +197,6 @@ def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=Tru
 def route(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, renormalise=True, scale=1.0):
     """Differentiable route_forward: the weights' gradient reaches the logits.  The choice is not differentiable, so
     the bias, which takes part in nothing else, gets no gradient."""
-    torch = _torch()
 
     class _Route(torch.autograd.Function):
         @staticmethod
@@ -220,7 +225,6 @@ def dispatch_plan(chosen, experts):
     """The expert order of the (token, choice) pairs of chosen [tokens, k]:
     offsets int32 [experts + 1] (expert e's rows are offsets[e]:offsets[e + 1]), slot int32 [tokens, k] (a pair's row, -1
     for entries that name no expert) and order int32 [tokens * k] (the pair t * k + j of a row, -1 behind the last)."""
-    torch = _torch()
     _gpu(chosen, "chosen", 2)
     (tokens, k), dev, experts = chosen.shape, chosen.device, int(experts)
     chosen = _array(chosen, "chosen", torch.int32, (tokens, k), dev)
@@ -239,11 +243,11 @@ def dispatch_plan(chosen, experts):
 
 def _slot_of(slot, dev, tokens=None):
     _gpu(slot, "slot", 2)
-    return _array(slot, "slot", _torch().int32, (slot.shape[0] if tokens is None else tokens, slot.shape[1]), dev)
+    return _array(slot, "slot", torch.int32, (slot.shape[0] if tokens is None else tokens, slot.shape[1]), dev)
 
 
 def _offsets_of(offsets, dev):
-    return _array(_gpu(offsets, "offsets", 1), "offsets", _torch().int32, offsets.shape, dev)
+    return _array(_gpu(offsets, "offsets", 1), "offsets", torch.int32, offsets.shape, dev)
 
 
 def dispatch_forward(x, slot, offsets, *, out=None):
@@ -277,7 +281,6 @@ def dispatch_backward(dxs, slot, *, out=None):
 
 def combine_forward(ys, slot, weights, *, out=None):
     """y [tokens, width]: y[t] = sum_j weights[t, j] ys[slot[t, j]]."""
-    torch = _torch()
     code = _dtype(_gpu(ys, "ys", 2), "ys")
     dev = ys.device
     slot = _slot_of(slot, dev)
@@ -294,7 +297,6 @@ def combine_forward(ys, slot, weights, *, out=None):
 
 def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
     """dys [tokens * k, width] and dweights fp32 [tokens, k]: dys[slot] = w dy[t], dweights = <dy[t], ys[slot]>."""
-    torch = _torch()
     code = _dtype(_gpu(dy, "dy", 2), "dy")
     dy, tokens, width, stride = _rows(dy, "dy")
     dev = dy.device
@@ -314,7 +316,6 @@ def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
 
 def dispatch(x, slot, offsets):
     """Differentiable dispatch_forward."""
-    torch = _torch()
 
     class _Dispatch(torch.autograd.Function):
         @staticmethod
@@ -330,7 +331,6 @@ def dispatch(x, slot, offsets):
 
 def combine(ys, weights, slot, offsets):
     """Differentiable combine_forward: gradients reach the experts' outputs and the weights."""
-    torch = _torch()
 
     class _Combine(torch.autograd.Function):
         @staticmethod
@@ -350,8 +350,10 @@ def combine(ys, weights, slot, offsets):
 @functools.lru_cache(maxsize=1024)
 def _cache_shape(code, k_shape, k_strides, v_strides):
     """The layout of a cache (everything but its pointers)."""
+    if k_strides[3] != 1 or v_strides[3] != 1:
+        raise LapsumError("the entries of k and v must be contiguous (last stride 1)")
     batch, heads, capacity, width = k_shape
-    return Cache(None, None, code, width, batch, heads, capacity, *k_strides, *v_strides)
+    return Cache(None, None, code, width, batch, heads, capacity, *k_strides[:3], *v_strides[:3])
 
 
 def _cache_of(k, v):
@@ -359,10 +361,7 @@ def _cache_of(k, v):
     _gpu(v, "v", 4, k.device)
     if v.dtype != k.dtype or v.shape != k.shape:
         raise LapsumError("k and v must have the same type and shape")
-    if k.stride(3) != 1 or v.stride(3) != 1:
-        raise LapsumError("the entries of k and v must be contiguous (last stride 1)")
-    shape = _cache_shape(code, tuple(k.shape), tuple(k.stride()[:3]), tuple(v.stride()[:3]))
-    cache = Cache.from_buffer_copy(shape)
+    cache = Cache.from_buffer_copy(_cache_shape(code, k.shape, k.stride(), v.stride()))
     cache.k, cache.v = k.data_ptr(), v.data_ptr()
     return cache
 
@@ -379,7 +378,6 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     [batch, heads, capacity, width] whose first lengths[b] entries are filled, the new tokens' own last (token i sees
     the entries up to lengths[b] - news + i).  account fp32 [batch, heads, capacity]: each entry's weight, summed over
     the new tokens and the query heads of its key head, is added to it, in place or into account_out.  scale: 1/sqrt(width) by default."""
-    torch = _torch()
     cache = _cache_of(k, v)
     dev = k.device
     _gpu(q, "q", 4, dev)
@@ -399,7 +397,7 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
         raise LapsumError("account_out needs an account")
     if q.numel() == 0:
         return out
-    nbytes = _attend_bytes(cache.dtype, tuple(k.shape), news, q_heads, int(account is not None))
+    nbytes = _attend_bytes(cache.dtype, k.shape, news, q_heads, int(account is not None))
     ws, wptr, wlen = _workspace(nbytes, dev)
     _call(dev, "lapsum_cache_attend", q.data_ptr(), cache, lengths.data_ptr(), news, q_heads,
           width ** -0.5 if scale is None else float(scale), None if account is None else account.data_ptr(),
@@ -424,10 +422,9 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
 
     Returns kept int32 [batch, heads, keep] (the slot each entry came from, -1 behind the last) and the new lengths
     (a new tensor)."""
-    torch = _torch()
     cache = _cache_of(k, v)
     dev, batch, keep = k.device, k.shape[0], int(keep)
-    shape = tuple(k.shape[:3])
+    shape = k.shape[:3]
     # arrays that are written in place have to be usable as they are
     account = _out(account, "account", torch.float32, shape, dev) if account_out is None else _array(
         account, "account", torch.float32, shape, dev)
@@ -439,9 +436,9 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
     lengths = _array(lengths, "lengths", torch.int32, (batch,), dev)
     if next_position is not None:
         next_position = _array(next_position, "next_position", torch.int32, (batch,), dev)
-    kept = torch.empty(shape[:2] + (max(keep, 0),), dtype=torch.int32, device=dev)
+    kept = torch.empty((*shape[:2], max(keep, 0)), dtype=torch.int32, device=dev)
     lengths_out = torch.empty_like(lengths)
-    ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, tuple(k.shape), keep), dev)
+    ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, k.shape, keep), dev)
     _call(dev, "lapsum_cache_evict", cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,
           None if next_position is None else next_position.data_ptr(), int(sinks), int(recent),
           account_out.data_ptr(), positions_out.data_ptr(), kept.data_ptr(), lengths_out.data_ptr(), wptr, wlen)
