@@ -339,7 +339,8 @@ typedef struct lapsum_route_options {
  *   logits  device [tokens, experts] of `dtype`, rows `row_stride` elements apart
  *   bias    device [experts] fp32, or NULL
  *   weights device [tokens, k] fp32;   chosen device [tokens, k] int32
- * An expert whose logit or c is -inf or NaN is not available.  A slot that no
+ * An expert whose logit or c is -inf or NaN, or whose c is the lowest fp32
+ * value, is not available.  A slot that no
  * available expert fills gets chosen = -1 and weight 0, so a row of -inf
  * gives -1 and 0 throughout.  The softmax with logits of +inf is its limit
  * (they share the mass equally).  A NaN logit makes the row's weights NaN

@@ -12,9 +12,9 @@
 // fp32 value leaves the 29 lowest bits of the fp64 mantissa free) and the
 // expert in the lowest ten, set so that of equal c the lower expert is the
 // larger number.  Then one max gives score and place at once, all numbers of a row
-// differ, and compare-exchange is a max and a min.  Each lane sorts its
-// own V numbers once; a round takes the maximum of the lanes' heads by a DPP
-// butterfly, and the lane that held it moves up.
+// differ, and compare-exchange is a max and a min.  Each lane orders the
+// largest of its own numbers once; a round takes the maximum of the lanes' heads by a
+// DPP butterfly, and the lane that held it moves up.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -22,39 +22,62 @@ namespace lapsum {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr float kLargest = 3.40282347e38f;
 
-// the fp64 number of (c, expert); experts that are not available are -inf
+// The fp64 number of (c, expert).  Minus infinity becomes the lowest fp32
+// value, which no available expert has.
 LDEV double number_of(float c, int expert) {
-  if (!(c > -INFINITY)) return -INFINITY;
-  c = fminf(c + 0.0f, 3.40282347e38f);  // -0 counts as 0; an infinite c as the largest finite one
+  c = __builtin_amdgcn_fmed3f(c + 0.0f, -kLargest, kLargest);  // -0 counts as 0
   unsigned long long u = (unsigned long long)__double_as_longlong((double)c);
   u |= (unsigned long long)(c < 0.0f ? expert : LAPSUM_MAX_EXPERTS - 1 - expert);
   return __longlong_as_double((long long)u);
 }
+LDEV bool available(double d) { return d > -(double)kLargest; }
 LDEV int expert_of(double d) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(d);
   const int low = (int)(u & (LAPSUM_MAX_EXPERTS - 1));
   return (u >> 63) != 0 ? low : LAPSUM_MAX_EXPERTS - 1 - low;
 }
 
-// Descending merge-exchange network (Batcher 1968) on V registers.
-template <int V>
-LDEV void sort_descending(double (&a)[V]) {
+LDEV void exchange(double &x, double &y) {
+  const double a = fmax(x, y), b = fmin(x, y);
+  x = a;
+  y = b;
+}
+// Descending merge-exchange network (Batcher 1968) on N registers from a[at].
+template <int N, int V>
+LDEV void sort_descending(double (&a)[V], int at) {
 #pragma unroll
-  for (int p = 1; p < V; p *= 2) {
+  for (int p = 1; p < N; p *= 2) {
 #pragma unroll
     for (int q = p; q >= 1; q /= 2) {
 #pragma unroll
-      for (int j = q % p; j + q < V; j += 2 * q) {
+      for (int j = q % p; j + q < N; j += 2 * q) {
 #pragma unroll
         for (int i = 0; i < q; ++i) {
-          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-            const double x = a[i + j], y = a[i + j + q];
-            a[i + j] = fmax(x, y);
-            a[i + j + q] = fmin(x, y);
-          }
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) exchange(a[at + i + j], a[at + i + j + q]);
         }
       }
+    }
+  }
+}
+// The K largest of V numbers, descending, to the front (K = V, or V / 2).
+template <int K, int V>
+LDEV void sort_largest(double (&a)[V]) {
+  if constexpr (K == V) {
+    sort_descending<V>(a, 0);
+  } else {
+    static_assert(2 * K == V, "two halves");
+    sort_descending<K>(a, 0);
+    sort_descending<K>(a, K);
+    // of two descending halves, the larger of a[i] and a[V - 1 - i] are the K largest, in bitonic order
+#pragma unroll
+    for (int i = 0; i < K; ++i) a[i] = fmax(a[i], a[V - 1 - i]);
+#pragma unroll
+    for (int q = K / 2; q >= 1; q /= 2) {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if ((i & q) == 0) exchange(a[i], a[i + q]);
     }
   }
 }
@@ -97,151 +120,238 @@ LDEV void load_row(const T *row, int experts, bool packs, int j, float (&x)[V]) 
   }
 }
 
+// e^(x - m), m the row's maximum; 1 where both are the same infinity.
+LDEV float share_of(float x, float m) { return exp_full(x == m ? 0.0f : x - m); }
+
 LDEV float sigmoid(float x) {
   const float e = exp_full(-fabsf(x));
-  return (x > 0.0f ? 1.0f : e) / (1.0f + e);
+  return (x > 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// The two largest of what has been seen, b1 >= b2.
+LDEV void best_two(float &b1, float &b2, float y) {
+  b2 = __builtin_amdgcn_fmed3f(b1, b2, y);
+  b1 = fmaxf(b1, y);
+}
+template <int M>
+LDEV void best_two_across(float &b1, float &b2) {
+  const float x1 = pair_lane<M>(b1), x2 = pair_lane<M>(b2);
+  b2 = fmaxf(fminf(b1, x1), fmaxf(b2, x2));
+  b1 = fmaxf(b1, x1);
+}
+
+// Numbers A + 1 .. B of a lane one place up if it won the round.  Written out
+// by recursion: a loop would have its selects turned into indexed reads before it is unrolled.
+template <int A, int B, int V>
+LDEV void move_up(double (&num)[V], bool won) {
+  if constexpr (A < B) {
+    const double next = num[A + 1], own = num[A];
+    num[A] = won ? next : own;
+    move_up<A + 1, B>(num, won);
+  }
+}
+// Up to eight rounds; choice i goes to lane i of the team.  After round I a lane has
+// at most K - 1 - I numbers left that can still be chosen.
+template <int L, int K, int I, int V>
+LDEV void choose(double (&num)[V], int k, int j, double &mine) {
+  if constexpr (I < 8) {
+    if (I >= k) return;  // k is the same for the whole launch
+    const double best = team_max<L>(num[0]);
+    if (I == j) mine = best;
+    constexpr int last = K - 1 - I > 0 ? K - 1 - I : 0;
+    const bool won = num[0] == best;
+    move_up<0, last>(num, won);
+    if constexpr (I >= K - 1) num[0] = won ? -INFINITY : num[0];  // a lane of fewer than eight numbers
+    choose<L, K, I + 1>(num, k, j, mine);
+  }
 }
 
 // packs: the rows can be read in 16-byte packs (host-checked alignment, and
-// a whole number of packs per row)
-template <class T, int L, int V>
-__global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteArgs a, const bool packs) {
+// a whole number of packs per row).  spread: the lanes that share a group, a
+// power of two, where groups are whole packs of neighbouring lanes; else 0.
+// KM: most choices (8 or 32).
+template <class T, int L, int V, int KM>
+__global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteArgs a, const bool packs,
+                                                                    const int spread) {
   constexpr int R = 64 / L;              // rows per wave
-  constexpr int C = (LAPSUM_MAX_CHOICES + L - 1) / L;  // choices a lane records, at most
+  constexpr int C = (KM + L - 1) / L;    // choices a lane records, at most
+  constexpr int K = KM < V ? KM : V;     // numbers of a lane that can be chosen
+  constexpr int P = Pack<T>::N < V ? Pack<T>::N : V;
   constexpr int kN = places(L * V);
   struct Shared {
     float s[kWaves][R][kN];
     float group[kWaves][R][LAPSUM_MAX_GROUPS];
-    int open[kWaves][R][LAPSUM_MAX_GROUPS];
   };
   __shared__ Shared sh;
   lds_poison(sh);
   const int wave = threadIdx.x / 64, team = (threadIdx.x % 64) / L, j = threadIdx.x % L;
   const int64_t token = ((int64_t)blockIdx.x * kWaves + wave) * R + team;
   const bool live = token < a.tokens;
-  float *sc = sh.s[wave][team];
+  const T *row = static_cast<const T *>(a.logits) + (live ? token : 0) * a.stride;
 
   float x[V];
-  if (live) {
-    load_row<T, L, V>(static_cast<const T *>(a.logits) + token * a.stride, a.experts, packs, j, x);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = -INFINITY;
-  }
+  load_row<T, L, V>(row, live ? a.experts : 0, packs, j, x);
   bool nan = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (x[v] != x[v]) {
-      nan = true;
-      x[v] = -INFINITY;
-    }
+    nan |= x[v] != x[v];
+    x[v] = x[v] != x[v] ? -INFINITY : x[v];
   }
   nan = team_max<L>(nan ? 1.0f : 0.0f) > 0.0f;
 
-  float s[V];
+  // c: the scores the choice goes by
+  float c[V];
+  float m = 0.0f, r = 0.0f;  // softmax: maximum and the inverse sum
   if (a.score == LAPSUM_SCORE_SOFTMAX) {
-    float m = x[0];
+    m = x[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
     m = team_max<L>(m);
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      s[v] = x[v] == -INFINITY ? 0.0f : (x[v] == m ? 1.0f : exp_full(x[v] - m));
-      sum += s[v];
+      c[v] = share_of(x[v], m);
+      sum += c[v];
     }
     sum = team_sum<L>(sum);
-    const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+    r = m > -INFINITY ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] *= r;
+    for (int v = 0; v < V; ++v) c[v] *= r;
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = x[v] == -INFINITY ? 0.0f : sigmoid(x[v]);
+    for (int v = 0; v < V; ++v) c[v] = sigmoid(x[v]);
   }
-
-  // c: the scores the choice goes by
-  float c[V];
+  if (a.bias != nullptr && packs) {  // whole packs inside the row
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = expert_at<T, L, V>(j, v);
-    c[v] = s[v];
-    if (a.bias != nullptr && e < a.experts) c[v] += a.bias[e];
-    if (x[v] == -INFINITY || c[v] != c[v]) c[v] = -INFINITY;
-  }
-  if (a.groups > 1) {
+    for (int i = 0; i < V / P; ++i) {
+      const int e = expert_at<T, L, V>(j, i * P);
+      const float *bias = a.bias + (e < a.experts ? e : 0);
 #pragma unroll
-    for (int v = 0; v < V; ++v) sc[place(expert_at<T, L, V>(j, v))] = c[v];
-    wave_sync();
-    for (int g = j; g < a.groups; g += L) {
-      float b1 = -INFINITY, b2 = -INFINITY;
-      for (int i = 0; i < a.group_size; ++i) {
-        const float y = sc[place(g * a.group_size + i)];
-        b2 = fmaxf(b2, fminf(b1, y));
-        b1 = fmaxf(b1, y);
-      }
-      sh.group[wave][team][g] = a.group_size > 1 ? b1 + b2 : b1;
+      for (int v = 0; v < P; ++v) c[i * P + v] += bias[v];
     }
-    wave_sync();
-    for (int g = j; g < a.groups; g += L) {
-      const float mine = sh.group[wave][team][g];
-      int before = 0;
-      for (int h = 0; h < a.groups; ++h) {
-        const float y = sh.group[wave][team][h];
-        before += (y > mine || (y == mine && h < g)) ? 1 : 0;
-      }
-      sh.open[wave][team][g] = before < a.top_groups ? 1 : 0;
-    }
-    wave_sync();
+  } else if (a.bias != nullptr) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = expert_at<T, L, V>(j, v);
-      if (e < a.experts) {
-        if (sh.open[wave][team][(uint32_t)e * a.group_magic >> 21] == 0) c[v] = -INFINITY;
+      c[v] += a.bias[e < a.experts ? e : 0];
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (x[v] == -INFINITY || c[v] != c[v]) c[v] = -INFINITY;
+
+  if (a.groups > 1) {
+    float *group = sh.group[wave][team];
+    if (spread > 0) {
+      // a pack lies in one group, and the group's packs in neighbouring lanes
+#pragma unroll
+      for (int i = 0; i < V / P; ++i) {
+        float b1 = c[i * P], b2 = -INFINITY;
+#pragma unroll
+        for (int v = 1; v < P; ++v) best_two(b1, b2, c[i * P + v]);
+        if constexpr (L > 1) { if (spread > 1) best_two_across<1>(b1, b2); }
+        if constexpr (L > 2) { if (spread > 2) best_two_across<2>(b1, b2); }
+        if constexpr (L > 4) { if (spread > 4) best_two_across<4>(b1, b2); }
+        if constexpr (L > 8) { if (spread > 8) best_two_across<8>(b1, b2); }
+        if constexpr (L > 16) { if (spread > 16) best_two_across<16>(b1, b2); }
+        if constexpr (L > 32) { if (spread > 32) best_two_across<32>(b1, b2); }
+        const int e = expert_at<T, L, V>(j, i * P);
+        if (e < a.experts && (j & (spread - 1)) == 0)
+          group[(uint32_t)e * a.group_magic >> 21] = a.group_size > 1 ? b1 + b2 : b1;
+      }
+    } else {
+      float *sc = sh.s[wave][team];
+#pragma unroll
+      for (int v = 0; v < V; ++v) sc[place(expert_at<T, L, V>(j, v))] = c[v];
+      wave_sync();
+      for (int g = j; g < a.groups; g += L) {
+        float b1 = -INFINITY, b2 = -INFINITY;
+        for (int i = 0; i < a.group_size; ++i) best_two(b1, b2, sc[place(g * a.group_size + i)]);
+        group[g] = a.group_size > 1 ? b1 + b2 : b1;
       }
     }
     wave_sync();
-  }
+    // the groups in the order of their scores: a group's place is the number of groups before it
+    unsigned long long open = 0;
+    for (int g = 0; g < a.groups; g += L) {
+      const int mine = g + j;
+      const float y = mine < a.groups ? group[mine] : 0.0f;
+      int before = 0;
+      for (int h = 0; h < a.groups; ++h) {
+        const float z = group[h];
+        before += (z > y || (z == y && h < mine)) ? 1 : 0;
+      }
+      const unsigned long long in = __ballot(mine < a.groups && before < a.top_groups);
+      constexpr unsigned long long kTeam = L == 64 ? ~0ull : (1ull << (L % 64)) - 1ull;
+      open |= ((in >> (team * L)) & kTeam) << g;
+    }
+    if (spread > 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) sc[place(expert_at<T, L, V>(j, v))] = s[v];
-  wave_sync();
+      for (int i = 0; i < V / P; ++i) {
+        const int e = expert_at<T, L, V>(j, i * P);
+        const bool shut = ((open >> ((uint32_t)e * a.group_magic >> 21)) & 1ull) == 0;
+#pragma unroll
+        for (int v = 0; v < P; ++v)
+          if (shut) c[i * P + v] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = expert_at<T, L, V>(j, v);
+        if (((open >> ((uint32_t)e * a.group_magic >> 21)) & 1ull) == 0) c[v] = -INFINITY;
+      }
+    }
+  }
 
   double num[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) num[v] = number_of(c[v], expert_at<T, L, V>(j, v));
-  sort_descending<V>(num);
+  sort_largest<K>(num);
 
-  double mine[C];  // choice r * L + j of this row
+  double mine[C];  // choice i * L + j of this row
 #pragma unroll
-  for (int r = 0; r < C; ++r) mine[r] = -INFINITY;
+  for (int i = 0; i < C; ++i) mine[i] = -INFINITY;
+  if constexpr (KM == 8) {
+    choose<L, K, 0>(num, a.k, j, mine[0]);
+  } else {
 #pragma unroll
-  for (int r = 0; r < C; ++r) {
-    const int n = min(a.k - r * L, L);
-    for (int i = 0; i < n; ++i) {
-      const double best = team_max<L>(num[0]);
-      if (i == j) mine[r] = best;
-      if (num[0] == best) {  // one lane of the team (several only when nothing is left)
+    for (int r2 = 0; r2 < C; ++r2) {
+      const int n = min(a.k - r2 * L, L);
+      for (int i = 0; i < n; ++i) {
+        const double best = team_max<L>(num[0]);
+        if (i == j) mine[r2] = best;
+        if (num[0] == best) {
 #pragma unroll
-        for (int v = 0; v + 1 < V; ++v) num[v] = num[v + 1];
-        num[V - 1] = -INFINITY;
+          for (int v = 0; v + 1 < V; ++v) num[v] = num[v + 1];
+          num[V - 1] = -INFINITY;
+        }
       }
     }
   }
 
+  // the chosen scores: the c themselves, or formed again from the logits where a bias is in them
   float w[C], sum = 0.0f;
 #pragma unroll
-  for (int r = 0; r < C; ++r) {
-    w[r] = mine[r] > -INFINITY ? sc[place(expert_of(mine[r]))] : 0.0f;
-    sum += w[r];
+  for (int i = 0; i < C; ++i) {
+    const bool there = available(mine[i]);
+    if (a.bias == nullptr) {
+      const unsigned long long u = (unsigned long long)__double_as_longlong(mine[i]) & ~1023ull;
+      w[i] = there ? (float)__longlong_as_double((long long)u) : 0.0f;
+    } else {
+      const float y = there ? (float)row[expert_of(mine[i])] : -INFINITY;
+      w[i] = a.score == LAPSUM_SCORE_SOFTMAX ? share_of(y, m) * r : sigmoid(y);
+    }
+    sum += w[i];
   }
   sum = a.renormalise != 0 ? team_sum<L>(sum) : 1.0f;
   const float f = sum > 0.0f ? a.scale / sum : 0.0f;
   if (!live) return;
 #pragma unroll
-  for (int r = 0; r < C; ++r) {
-    const int i = r * L + j;
-    if (i < a.k) {
-      a.weights[token * a.k + i] = nan ? NAN : w[r] * f;
-      a.chosen[token * a.k + i] = mine[r] > -INFINITY ? expert_of(mine[r]) : -1;
+  for (int i = 0; i < C; ++i) {
+    const int at = i * L + j;
+    if (at < a.k) {
+      a.weights[token * a.k + at] = nan ? NAN : w[i] * f;
+      a.chosen[token * a.k + at] = available(mine[i]) ? expert_of(mine[i]) : -1;
     }
   }
 }
@@ -294,15 +404,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const Route
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      z[v] = z[v] == -INFINITY ? 0.0f : (z[v] == m ? 1.0f : exp_full(z[v] - m));
+      z[v] = share_of(z[v], m);
       sum += z[v];
     }
     sum = team_sum<L>(sum);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = m == -INFINITY ? 0.0f : 1.0f / sum;
     float dot = 0.0f;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
-      s[r] = x[r] == -INFINITY ? 0.0f : (x[r] == m ? inv : exp_full(x[r] - m) * inv);
+      s[r] = share_of(x[r], m) * inv;
       g[r] *= a.scale;
       dot += g[r] * s[r];
       if (e[r] >= 0) d[e[r]] = g[r];
@@ -325,9 +435,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const Route
     float sum = 0.0f, mean = 0.0f;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
+      s[r] = soft ? share_of(x[r], m) : sigmoid(x[r]);
       if (x[r] == -INFINITY) s[r] = 0.0f;
-      else if (soft) s[r] = x[r] == m ? 1.0f : exp_full(x[r] - m);
-      else s[r] = sigmoid(x[r]);
       sum += s[r];
       mean += g[r] * s[r];
     }
@@ -372,11 +481,14 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const Route
 
 template <class T, int L, int V>
 hipError_t forward(const RouteArgs &a, hipStream_t s) {
-  constexpr int P = Pack<T>::N;
-  const bool packs = a.experts % P == 0 && a.stride % P == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+  constexpr int N = Pack<T>::N, P = N < V ? N : V;
+  const bool packs = a.experts % N == 0 && a.stride % N == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+  int spread = a.group_size % P == 0 ? a.group_size / P : 0;
+  if (spread > L || (spread & (spread - 1)) != 0) spread = 0;
   constexpr int rows = kWaves * (64 / L);
-  route_forward_kernel<T, L, V>
-      <<<dim3((unsigned)((a.tokens + rows - 1) / rows)), dim3(64 * kWaves), 0, s>>>(a, packs);
+  const dim3 grid((unsigned)((a.tokens + rows - 1) / rows)), threads(64 * kWaves);
+  if (a.k <= 8) route_forward_kernel<T, L, V, 8><<<grid, threads, 0, s>>>(a, packs, spread);
+  else route_forward_kernel<T, L, V, 32><<<grid, threads, 0, s>>>(a, packs, spread);
   return hipGetLastError();
 }
 template <class T, int L, int V>
