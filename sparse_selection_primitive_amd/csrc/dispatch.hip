@@ -167,33 +167,42 @@ int bits_for(int experts) {
 // ----------------------------------------------------------------- rows
 // Threads per token by the row's length in 16-byte packs; a workgroup of 256
 // threads takes 256 / G tokens.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+LDEV uint4 stream_load(const uint4 *p);
+LDEV void stream_store(uint4 *p, uint4 v);
+
+// What a thread moves at a time: a pack of 16 bytes, or one element where
+// rows are not 16-byte aligned.  Kept as it is in memory.
 template <class T, bool PACKS>
-struct Unit {  // what a thread moves at a time: a pack, or one element where rows are not 16-byte aligned
-  static constexpr int N = PACKS ? Pack<T>::N : 1;
-  float f[N];
-  LDEV void load(const T *p) {
-    if constexpr (PACKS) {
-      const pack_t<T> w = load_pack(p);
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = (float)w[i];
-    } else {
-      f[0] = (float)*p;
-    }
+struct Unit {
+  static constexpr int N = Pack<T>::N;
+  pack_t<T> v;
+  LDEV float at(int n) const { return (float)v[n]; }
+  static LDEV Unit load(const T *p) { return Unit{load_pack(p)}; }
+  static LDEV Unit stream(const T *p) {
+    return Unit{__builtin_bit_cast(pack_t<T>, stream_load(reinterpret_cast<const uint4 *>(p)))};
   }
-  LDEV void store(T *p) const {
-    if constexpr (PACKS) {
-      pack_t<T> w;
+  LDEV void store(T *p) const { stream_store(reinterpret_cast<uint4 *>(p), __builtin_bit_cast(uint4, v)); }
+  LDEV void cached(T *p) const { store_pack(p, v); }
+  static LDEV Unit zero() { return Unit{__builtin_bit_cast(pack_t<T>, uint4{0, 0, 0, 0})}; }
+  static LDEV Unit of(const float (&f)[N]) {
+    Unit u;
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = (T)f[i];
-      store_pack(p, w);
-    } else {
-      *p = (T)f[0];
-    }
+    for (int n = 0; n < N; ++n) u.v[n] = (T)f[n];
+    return u;
   }
-  LDEV void zero() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = 0.0f;
-  }
+};
+template <class T>
+struct Unit<T, false> {
+  static constexpr int N = 1;
+  T v;
+  LDEV float at(int) const { return (float)v; }
+  static LDEV Unit load(const T *p) { return Unit{*p}; }
+  static LDEV Unit stream(const T *p) { return Unit{*p}; }
+  LDEV void store(T *p) const { *p = v; }
+  LDEV void cached(T *p) const { *p = v; }
+  static LDEV Unit zero() { return Unit{(T)0.0f}; }
+  static LDEV Unit of(const float (&f)[1]) { return Unit{(T)f[0]}; }
 };
 
 LDEV int slot_at(const RowsArgs &a, int64_t pair) {
@@ -201,25 +210,56 @@ LDEV int slot_at(const RowsArgs &a, int64_t pair) {
   return (uint64_t)(int64_t)s < (uint64_t)a.pairs ? s : -1;
 }
 
+// Rows of the experts' side are read or written once and are far more than the
+// caches hold: streamed past them.
+LDEV uint4 stream_load(const uint4 *p) {
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+  return __builtin_bit_cast(uint4, v);
+}
+LDEV void stream_store(uint4 *p, uint4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4 *>(p));
+}
+
+constexpr int kAhead = 8;  // rows of a token whose loads are under way together
+
+// The token of this thread: the same for its whole wave, so slots and weights
+// are scalar loads.
+template <int G>
+LDEV int64_t token_of() {
+  return (int64_t)blockIdx.x * (256 / G) + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+}
+
+// The slots (and weights) of up to kAhead pairs from `pair`; absent ones -1 (and 0).
+LDEV void slots_of(const RowsArgs &a, int64_t pair, int left, int (&s)[kAhead], float (&w)[kAhead]) {
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    s[i] = i < left ? slot_at(a, pair + i) : -1;
+    w[i] = i < left && a.weights != nullptr ? a.weights[pair + i] : 1.0f;
+  }
+}
+
 // xs[slot[t][j]] = x[t]; the rows behind the last pair are zeroed by the
 // tokens whose pairs have those indices.
 template <class T, bool PACKS, int G>
 __global__ __launch_bounds__(256) void dispatch_rows_kernel(const RowsArgs a) {
   using U = Unit<T, PACKS>;
-  const int64_t token = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int64_t token = token_of<G>();
   if (token >= a.tokens) return;
   const int64_t placed = *a.placed;
   const T *src = static_cast<const T *>(a.src) + token * a.stride;
   T *dst = static_cast<T *>(a.dst);
   for (int64_t c = (int64_t)(threadIdx.x % G) * U::N; c < a.width; c += (int64_t)G * U::N) {
-    U u, z;
-    u.load(src + c);
-    z.zero();
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t pair = token * a.k + j;
-      const int s = slot_at(a, pair);
-      if (s >= 0) u.store(dst + (int64_t)s * a.width + c);
-      if (pair >= placed) z.store(dst + pair * a.width + c);
+    const U u = U::load(src + c);
+    for (int j0 = 0; j0 < a.k; j0 += kAhead) {
+      const int64_t pair = token * a.k + j0;
+      int s[kAhead];
+      float w[kAhead];
+      slots_of(a, pair, a.k - j0, s, w);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s[i] >= 0) u.store(dst + (int64_t)s[i] * a.width + c);
+        if (i < a.k - j0 && pair + i >= placed) U::zero().store(dst + (pair + i) * a.width + c);
+      }
     }
   }
 }
@@ -228,85 +268,92 @@ __global__ __launch_bounds__(256) void dispatch_rows_kernel(const RowsArgs a) {
 template <class T, bool PACKS, int G>
 __global__ __launch_bounds__(256) void sum_rows_kernel(const RowsArgs a) {
   using U = Unit<T, PACKS>;
-  const int64_t token = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int64_t token = token_of<G>();
   if (token >= a.tokens) return;
   const T *src = static_cast<const T *>(a.src);
   T *dst = static_cast<T *>(a.dst) + token * a.width;
   for (int64_t c = (int64_t)(threadIdx.x % G) * U::N; c < a.width; c += (int64_t)G * U::N) {
-    U sum;
-    sum.zero();
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t pair = token * a.k + j;
-      const int s = slot_at(a, pair);
-      if (s < 0) continue;
-      U u;
-      u.load(src + (int64_t)s * a.width + c);
-      const float w = a.weights != nullptr ? a.weights[pair] : 1.0f;
+    float sum[U::N];
 #pragma unroll
-      for (int i = 0; i < U::N; ++i) sum.f[i] = __builtin_fmaf(w, u.f[i], sum.f[i]);
+    for (int i = 0; i < U::N; ++i) sum[i] = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += kAhead) {
+      int s[kAhead];
+      float w[kAhead];
+      slots_of(a, token * a.k + j0, a.k - j0, s, w);
+      U u[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (s[i] >= 0) u[i] = U::stream(src + (int64_t)s[i] * a.width + c);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s[i] < 0) continue;
+#pragma unroll
+        for (int n = 0; n < U::N; ++n) sum[n] = __builtin_fmaf(w[i], u[i].at(n), sum[n]);
+      }
     }
-    sum.store(dst + c);
+    U::of(sum).cached(dst + c);
   }
 }
 
 // dys[slot] = w dy[t], dweights = <dy[t], ys[slot]>: one pass over both.  The
-// products' sum goes over the team's lanes in a fixed order.
+// products' sum goes over a wave's lanes, then over the waves, in a fixed order.
 template <class T, bool PACKS, int G>
 __global__ __launch_bounds__(256) void combine_backward_kernel(const RowsArgs a) {
   using U = Unit<T, PACKS>;
-  constexpr int kWavesPer = G > 64 ? G / 64 : 1;
   struct Shared {
     float part[LAPSUM_MAX_CHOICES][4];
   };
   __shared__ Shared sh;
   lds_poison(sh);
-  const int64_t token = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int64_t token = token_of<G>();
   const bool live = token < a.tokens;
   const int64_t placed = *a.placed;
   const T *dy = static_cast<const T *>(a.dy) + (live ? token : 0) * a.stride;
   const T *ys = static_cast<const T *>(a.src);
   T *dys = static_cast<T *>(a.dst);
   const int lane = threadIdx.x % G;
-  for (int j = 0; j < a.k; ++j) {
-    float dot = 0.0f;
-    if (live) {
-      const int64_t pair = token * a.k + j;
-      const int s = slot_at(a, pair);
-      const float w = a.weights[pair];
-      for (int64_t c = (int64_t)lane * U::N; c < a.width; c += (int64_t)G * U::N) {
-        if (s >= 0) {
-          U g, u;
-          g.load(dy + c);
-          u.load(ys + (int64_t)s * a.width + c);
+  for (int j0 = 0; j0 < a.k && live; j0 += kAhead) {
+    const int64_t pair = token * a.k + j0;
+    int s[kAhead];
+    float w[kAhead], dot[kAhead];
+    slots_of(a, pair, a.k - j0, s, w);
 #pragma unroll
-          for (int i = 0; i < U::N; ++i) {
-            dot = __builtin_fmaf(g.f[i], u.f[i], dot);
-            g.f[i] *= w;
+    for (int i = 0; i < kAhead; ++i) dot[i] = 0.0f;
+    for (int64_t c = (int64_t)lane * U::N; c < a.width; c += (int64_t)G * U::N) {
+      const U g = U::load(dy + c);
+      U u[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (s[i] >= 0) u[i] = U::stream(ys + (int64_t)s[i] * a.width + c);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s[i] >= 0) {
+          float d[U::N];
+#pragma unroll
+          for (int n = 0; n < U::N; ++n) {
+            dot[i] = __builtin_fmaf(g.at(n), u[i].at(n), dot[i]);
+            d[n] = w[i] * g.at(n);
           }
-          g.store(dys + (int64_t)s * a.width + c);
+          U::of(d).store(dys + (int64_t)s[i] * a.width + c);
         }
-        if (pair >= placed) {
-          U z;
-          z.zero();
-          z.store(dys + pair * a.width + c);
-        }
+        if (i < a.k - j0 && pair + i >= placed) U::zero().store(dys + (pair + i) * a.width + c);
       }
     }
-    dot = team_sum<(G < 64 ? G : 64)>(dot);
-    if constexpr (G <= 64) {
-      if (live && lane == 0) a.dweights[token * a.k + j] = dot;
-    } else {
-      if (threadIdx.x % 64 == 0) sh.part[j][threadIdx.x / 64] = dot;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i >= a.k - j0) continue;
+      dot[i] = wave_reduce(dot[i], [](float x, float y) { return x + y; });
+      if (threadIdx.x % 64 == 0) {
+        if constexpr (G == 64) a.dweights[pair + i] = dot[i];
+        else sh.part[j0 + i][threadIdx.x / 64] = dot[i];
+      }
     }
   }
   if constexpr (G > 64) {
     __syncthreads();
-    if (live && lane < a.k) {
-      float dot = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWavesPer; ++w) dot += sh.part[lane][(threadIdx.x / G) * kWavesPer + w];
-      a.dweights[token * a.k + lane] = dot;
-    }
+    if (live && lane < a.k)
+      a.dweights[token * a.k + lane] =
+          (sh.part[lane][0] + sh.part[lane][1]) + (sh.part[lane][2] + sh.part[lane][3]);
   }
 }
 
