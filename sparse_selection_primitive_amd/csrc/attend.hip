@@ -170,6 +170,24 @@ struct Values {
       }
     }
   }
+  // sets infinities and NaN to zero (by their exponents, on the packed words); whether there were any
+  LDEV bool drop() {
+    constexpr uint32_t kExponent = (float)(T)65536.0f == 65536.0f ? 0x7F80u : 0x7C00u;  // bf16, fp16
+    typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      words x = __builtin_bit_cast(words, v[j]);
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const bool low = (x[i] & kExponent) == kExponent, high = ((x[i] >> 16) & kExponent) == kExponent;
+        any |= low || high;
+        x[i] &= (low ? 0xFFFF0000u : 0xFFFFFFFFu) & (high ? 0x0000FFFFu : 0xFFFFFFFFu);
+      }
+      v[j] = __builtin_bit_cast(vec, x);
+    }
+    return any;
+  }
   static LDEV uint32_t value_offset(const AttendArgs &a) {
     const int lane = threadIdx.x % 64, d = (lane % 16) * W;
     return d < a.width ? (uint32_t)((lane / 16) * 4 * (int)a.ve * 2 + d * 2) : kNowhere;
@@ -188,12 +206,13 @@ struct Values {
 // all the entries for rows of its own, and what one wave loads the others find in
 // the cache of their compute unit).
 template <class T, int DP, int NT, bool EXACT, bool BY_ROWS, bool ONE, bool KEEP>
-__global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) void attend_kernel(const AttendArgs a) {
+__global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 ? 2 : 1) void attend_kernel(const AttendArgs a) {
   constexpr int W = DP / 16;
   constexpr int kRows = 16 * NT;
   constexpr int kPad = DP + 4;  // floats per row in LDS: 16 rows' 16-byte accesses fall on all banks
   struct Shared {
     float m[kAttendWaves][kRows], l[kAttendWaves][kRows];
+    int dropped[kAttendWaves];
     float o[BY_ROWS ? 1 : kAttendWaves][BY_ROWS ? 1 : kRows][BY_ROWS ? 4 : kPad];
   };
   __shared__ Shared sh;
@@ -215,6 +234,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
       ml[2 * i] = -INFINITY;
       ml[2 * i + 1] = 0.0f;
     }
+    if (!ONE && threadIdx.x == 0) a.dropped[bh * a.splits + split] = 0;
     return;
   }
   const int64_t b = bh / a.heads, h = bh % a.heads;
@@ -260,6 +280,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
     for (int n = 0; n < W; ++n) o[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
+  bool dropped = false;
   for (int e0 = first; e0 < end; e0 += kStride) {
     f32x4 z[NT][2];
 #pragma unroll
@@ -324,68 +345,26 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
         }
       }
     }
-    bool broken = false;
-    if (!ONE && edge) {
-      bool odd = false;
+    // NaN or infinity among values that some row does not see must not meet
+    // that row's zero weights: they are left out here and added by the join
+    if (!ONE && edge) dropped |= v.drop();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int n = 0; n < W; ++n) odd |= !(fabsf((float)v.v[j][n]) < INFINITY);
-      }
-      broken = __any(odd);
-    }
-    if (ONE || !broken) {
-#pragma unroll
-      for (int n = 0; n < W; ++n) {
-        const pack_t<T> col = v.column(n);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][n] = mfma(col, hi[t], o[t][n]);
-          o[t][n] = mfma(col, lo[t], o[t][n]);
-        }
-      }
-    } else {
-      // NaN or infinity among values that some row does not see: the products
-      // take them as zero, and what each row does see of them is counted by
-      // products of ones and added after
-      const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
-      pack_t<T> seen[NT];
+    for (int n = 0; n < W; ++n) {
+      const pack_t<T> col = v.column(n);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + entry_of(j);
-          seen[t][j] = (T)(e <= limit[t] && e < end ? 1.0f : 0.0f);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < W; ++n) {
-        pack_t<T> col = v.column(n), up, down, nan;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = (float)col[j];
-          up[j] = (T)(x == INFINITY ? 1.0f : 0.0f);
-          down[j] = (T)(x == -INFINITY ? 1.0f : 0.0f);
-          nan[j] = (T)(x != x ? 1.0f : 0.0f);
-          if (!(fabsf(x) < INFINITY)) col[j] = (T)0.0f;
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][n] = mfma(col, hi[t], o[t][n]);
-          o[t][n] = mfma(col, lo[t], o[t][n]);
-          const f32x4 ups = mfma(up, seen[t], none), downs = mfma(down, seen[t], none), nans = mfma(nan, seen[t], none);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (ups[x] > 0.0f) o[t][n][x] += INFINITY;
-            if (downs[x] > 0.0f) o[t][n][x] -= INFINITY;
-            if (nans[x] > 0.0f) o[t][n][x] = NAN;
-          }
-        }
+        o[t][n] = mfma(col, hi[t], o[t][n]);
+        o[t][n] = mfma(col, lo[t], o[t][n]);
       }
     }
     v.load(entries(values, a.ve, e0 + kStride, end, a.width), value_off, (int)a.ve * 2);
   }
 
+  int *const flag = a.dropped + bh * a.splits + split;
+  if constexpr (!ONE && BY_ROWS) {  // every wave has seen the same values
+    const bool any = __any(dropped);
+    if (lane == 0) *flag = any ? 1 : 0;
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t) l[t] = groups_sum(l[t]);
   float *part = a.part_o + ((bh * a.splits + split) * a.rows + row0) * a.width;
@@ -412,6 +391,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
     return;
   }
   // join the waves: a common maximum, then their sums in the waves' order
+  if constexpr (!ONE) sh.dropped[wave] = __any(dropped) ? 1 : 0;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     if (c == 0) {
@@ -420,6 +400,7 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 && NT == 1 ? 2 : 1) vo
     }
   }
   __syncthreads();
+  if (!ONE && threadIdx.x == 0) *flag = sh.dropped[0] | sh.dropped[1] | sh.dropped[2] | sh.dropped[3];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float all = -INFINITY;
@@ -484,6 +465,7 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + bh * a.splits * a.rows + row;
   float2 x = {-INFINITY, 0.0f};
   if (tid < a.splits) x = ml[(int64_t)tid * a.rows];
+  const bool again = a.news > 1 && __syncthreads_or(tid < a.splits && a.dropped[bh * a.splits + tid] != 0) != 0;
   float top = team_max<64>(x.x);
   if (tid % 64 == 0) sh.top[wave] = top;
   __syncthreads();
@@ -516,9 +498,24 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   if (team != 0) return;
   for (int t = 1; t < teams; ++t) o += sh.o[t * packs + tid];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  o *= inv;
+  if (again) {
+    // infinities and NaN that the products left out, of the entries this row
+    // sees (one that they did not leave out is in the sum already, and stays)
+    const int length = length_of(a, bh), last = length - a.news + row / a.group;
+    const int64_t b = bh / a.heads, h = bh % a.heads;
+    const T *v = static_cast<const T *>(a.v) + b * a.vb + h * a.vh + d;
+    for (int e = max(0, length - a.news - kBlock); e <= last; ++e) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float x = (float)v[(int64_t)e * a.ve + n];
+        if (!(fabsf(x) < INFINITY)) o[n] += x;
+      }
+    }
+  }
   typedef T vec4 __attribute__((ext_vector_type(4)));
   T *out = const_cast<T *>(query_row<T>(a, bh, row) - static_cast<const T *>(a.q) + static_cast<T *>(a.out));
-  *reinterpret_cast<vec4 *>(out + d) = vec4{(T)(o[0] * inv), (T)(o[1] * inv), (T)(o[2] * inv), (T)(o[3] * inv)};
+  *reinterpret_cast<vec4 *>(out + d) = vec4{(T)o[0], (T)o[1], (T)o[2], (T)o[3]};
 }
 
 // The first a.rows workgroups of a cache join its rows; the others add up the
@@ -582,33 +579,51 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
     key.load(win, 16 * u, k[u]);
     w[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  static_assert(KT == 4, "16 entries a lane group, one a lane in the end");
+  const int mine = e0 + 16 * (r / 4) + 4 * c + r % 4;
+  const float before = mine < length ? a.account[bh * a.capacity + mine] : 0.0f;
+  // some row does not see some entry
+  const bool edge = e0 + 16 * KT - 1 > length - a.news;
+  pack_t<T> next[DP / 32];
+  load_queries<T, DP>(a, bh, r, next);
+  float next_off = r < a.rows ? lse[bh * a.rows + r] : INFINITY;
   for (int row0 = 0; row0 < a.rows; row0 += 16) {
     const int row = row0 + r;
     pack_t<T> q[DP / 32];
-    load_queries<T, DP>(a, bh, row, q);
-    const float off = row < a.rows ? lse[bh * a.rows + row] : INFINITY;
-    const int limit = length - a.news + row / a.group;
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) q[i] = next[i];
+    const float off = next_off;
+    // the next rows while these are worked on
+    load_queries<T, DP>(a, bh, row + 16, next);
+    next_off = row + 16 < a.rows ? lse[bh * a.rows + row + 16] : INFINITY;
+    const int most = row < a.rows ? length - a.news + row / a.group - e0 - 4 * c : -1;
+    const bool some = edge || row0 + 16 > a.rows;
 #pragma unroll
     for (int u = 0; u < KT; ++u) {
       f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) z = mfma(k[u][i], q[i], z);
+      if (some) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - off);
-        if (e0 + 16 * u + 4 * c + i <= limit && row < a.rows) w[u][i] += p;
+        for (int i = 0; i < 4; ++i)
+          w[u][i] += 16 * u + i > most ? 0.0f : __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - off);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[u][i] += __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - off);
       }
     }
   }
+  // lane r of a group takes the sum of its r-th entry
+  float sum = 0.0f;
 #pragma unroll
   for (int u = 0; u < KT; ++u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float sum = team_sum<16>(w[u][i]);
-      const int e = e0 + 16 * u + 4 * c + i;
-      if (r == 0 && e < length) a.account_out[bh * a.capacity + e] = a.account[bh * a.capacity + e] + sum;
+      const float x = team_sum<16>(w[u][i]);
+      sum = r == 4 * u + i ? x : sum;
     }
   }
+  if (mine < length) a.account_out[bh * a.capacity + mine] = before + sum;
 }
 
 template <class T, int TH>
@@ -673,12 +688,13 @@ AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t r
   // rows per workgroup, as attend_rows() chooses them
   const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)) : 64);
   const int64_t groups = caches * ((rows + rows_per - 1) / rows_per);
-  // Workgroups over all.  768 fit the chip at once (three a compute unit), and
-  // one round of them is best where their shares are equal: one sequence of 200001 entries takes
-  // 132 us, in three rounds 145.  Sequences of several lengths need a finer grain: 64 of
-  // 512 to 8192 entries take 188 us in three rounds, 196 in one.  With more than 32 rows one
-  // workgroup fills a compute unit.
-  const int64_t wanted = rows > 32 ? 512 : (batch > 1 && one ? 2304 : 768);
+  // Workgroups over all.  768 fit the chip at once (three a compute unit), and one
+  // round of them is best where their shares are equal: one sequence of 200001 entries takes 132 us,
+  // in three rounds 145.  Sequences of several lengths need a finer grain: 64 of 512 to 8192
+  // entries take 188 us in three rounds, 196 in one.  With more rows, or wider ones, a
+  // split's part of the outputs weighs more: 32 new tokens over 16384 entries take 56 us with
+  // one workgroup a compute unit, 73 with two and 87 with half of them idle.
+  const int64_t wanted = rows > 16 || width > 128 ? 256 : (batch > 1 && one ? 2304 : 768);
   int64_t splits = (wanted + groups - 1) / groups;
   const int64_t most = (capacity + kStep - 1) / kStep;
   if (splits > most) splits = most;
@@ -689,6 +705,7 @@ AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t r
   p.blocks = (capacity + kBlock - 1) / kBlock;
   p.part_o = (size_t)(caches * splits * rows) * width * sizeof(float);
   p.part_ml = (size_t)(caches * splits * rows) * 2 * sizeof(float) + (size_t)(caches * rows) * sizeof(float);
+  p.dropped = (size_t)(caches * splits) * sizeof(int);
   p.logits = p.keep_logits ? (size_t)(caches * rows) * p.blocks * kBlock * sizeof(float) : 0;
   return p;
 }

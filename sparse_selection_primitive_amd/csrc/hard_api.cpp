@@ -120,7 +120,9 @@ lapsum_status check_attend(const lapsum_cache *c, int64_t news, int64_t q_heads)
   return LAPSUM_OK;
 }
 
-size_t attend_bytes(const AttendPlan &p) { return aligned_up(p.part_o) + aligned_up(p.part_ml) + aligned_up(p.logits); }
+size_t attend_bytes(const AttendPlan &p) {
+  return aligned_up(p.part_o) + aligned_up(p.part_ml) + aligned_up(p.dropped) + aligned_up(p.logits);
+}
 
 }  // namespace
 
@@ -272,7 +274,9 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
   a.out = out;
   a.part_o = reinterpret_cast<float *>(ws);
   a.part_ml = reinterpret_cast<float *>(ws + aligned_up(p.part_o));
-  a.logits = p.keep_logits ? reinterpret_cast<float *>(ws + aligned_up(p.part_o) + aligned_up(p.part_ml)) : nullptr;
+  ws += aligned_up(p.part_o) + aligned_up(p.part_ml);
+  a.dropped = reinterpret_cast<int *>(ws);
+  a.logits = p.keep_logits ? reinterpret_cast<float *>(ws + aligned_up(p.dropped)) : nullptr;
   a.blocks = p.blocks;
   (void)hipGetLastError();
   return done(launch_attend(a, cache->dtype, reinterpret_cast<hipStream_t>(stream)));

@@ -69,12 +69,13 @@ struct AttendArgs {
   float *part_ml;                  // [batch * heads][splits][rows][2]
   float *logits;                   // [batch * heads][blocks][rows][32], or NULL: formed again
   int64_t blocks;                  // of 32 entries
+  int *dropped;                    // [batch * heads][splits] several new tokens: infinities or NaN left out
 };
 struct AttendPlan {
   int splits;
   bool keep_logits;
   int64_t blocks;
-  size_t part_o, part_ml, logits;  // bytes
+  size_t part_o, part_ml, dropped, logits;  // bytes
 };
 AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t rows, bool one, int width,
                        bool accounts);
