@@ -584,34 +584,52 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
   const float before = mine < length ? a.account[bh * a.capacity + mine] : 0.0f;
   // some row does not see some entry
   const bool edge = e0 + 16 * KT - 1 > length - a.news;
-  pack_t<T> next[DP / 32];
-  load_queries<T, DP>(a, bh, r, next);
-  float next_off = r < a.rows ? lse[bh * a.rows + r] : INFINITY;
-  for (int row0 = 0; row0 < a.rows; row0 += 16) {
-    const int row = row0 + r;
+  // this lane's row of 16 from `row0` (one past the last is read as the first, and left out below)
+  const T *queries = query_row<T>(a, bh, 0);
+  const int64_t news_stride = (int64_t)a.heads * a.group * a.width;
+  struct Rows {
     pack_t<T> q[DP / 32];
+    float off;
+    int most;  // the last of the lane group's entries that the row sees
+  };
+  const auto load = [&](int row0, Rows &x) {
+    const int row = row0 + r < a.rows ? row0 + r : 0;
+    const int i = a.group == 1 ? row : (int)__umulhi((uint32_t)row, a.group_magic);
+    const T *p = queries + i * news_stride + (row - i * a.group) * a.width;
 #pragma unroll
-    for (int i = 0; i < DP / 32; ++i) q[i] = next[i];
-    const float off = next_off;
-    // the next rows while these are worked on
-    load_queries<T, DP>(a, bh, row + 16, next);
-    next_off = row + 16 < a.rows ? lse[bh * a.rows + row + 16] : INFINITY;
-    const int most = row < a.rows ? length - a.news + row / a.group - e0 - 4 * c : -1;
+    for (int n = 0; n < DP / 32; ++n) {
+      const int d = n * 32 + c * 8;
+      const uint4 w = *reinterpret_cast<const uint4 *>(p + (EXACT || d < a.width ? d : 0));
+      x.q[n] = __builtin_bit_cast(pack_t<T>, w);  // past the width the keys are zero
+    }
+    x.off = lse[bh * a.rows + row];
+    x.most = row0 + r < a.rows ? length - a.news + i - e0 - 4 * c : -1;
+  };
+  const auto add = [&](int row0, const Rows &x) {
     const bool some = edge || row0 + 16 > a.rows;
 #pragma unroll
     for (int u = 0; u < KT; ++u) {
       f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < DP / 32; ++i) z = mfma(k[u][i], q[i], z);
+      for (int n = 0; n < DP / 32; ++n) z = mfma(k[u][n], x.q[n], z);
       if (some) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          w[u][i] += 16 * u + i > most ? 0.0f : __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - off);
+          w[u][i] += 16 * u + i > x.most ? 0.0f : __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - x.off);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[u][i] += __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - off);
+        for (int i = 0; i < 4; ++i) w[u][i] += __builtin_amdgcn_exp2f(z[i] * a.scale_log2 - x.off);
       }
     }
+  };
+  // two sets of rows in turn, one on its way while the other is worked on
+  Rows x, y;
+  load(0, x);
+  for (int row0 = 0; row0 < a.rows; row0 += 32) {
+    load(row0 + 16, y);
+    add(row0, x);
+    load(row0 + 32, x);
+    if (row0 + 16 < a.rows) add(row0 + 16, y);
   }
   // lane r of a group takes the sum of its r-th entry
   float sum = 0.0f;

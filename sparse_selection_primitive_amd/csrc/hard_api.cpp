@@ -264,6 +264,7 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
   a.news = (int)news;
   a.group = (int)group;
   a.rows = (int)rows;
+  a.group_magic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)group - 1) / (uint64_t)group);
   a.width = cache->width;
   a.capacity = cache->capacity;
   a.lengths = lengths;

@@ -57,6 +57,7 @@ struct AttendArgs {
   int64_t kb, kh, ke, vb, vh, ve;  // strides of batch, head, entry (elements)
   int batch, heads, news, group;   // group: query heads per key head
   int rows;                        // news * group
+  uint32_t group_magic;            // ceil(2^32 / group) for group > 1: row / group is its product's upper word
   int width;
   int64_t capacity;
   const int32_t *lengths;
