@@ -26,11 +26,13 @@ namespace lapsum {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = 32;       // entries a wave takes at a time
 constexpr int kAttendWaves = 4;  // waves of a workgroup, taking its blocks in turn
 constexpr int kStep = kBlock * kAttendWaves;
+constexpr float kSlack = 8.0f;   // powers of two that a row's weights may exceed 1 by
 constexpr int kMaxSplits = 256;
 constexpr int kKeepRows = 16;    // up to this many rows the logits are kept for the accounts
 
@@ -102,8 +104,9 @@ template <int AUX>
 LDEV uint4 load_16(window_t w, uint32_t lane_offset, int offset) {
   return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane_offset, offset, AUX));
 }
+template <int AUX>
 LDEV uint2 load_8(window_t w, uint32_t lane_offset, int offset) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane_offset, offset, kStreamed));
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane_offset, offset, AUX));
 }
 
 LDEV void store_16(window_t w, uint32_t lane_offset, int offset, f32x4 v) {
@@ -148,7 +151,7 @@ LDEV int entry_of(int place) {
   return (place / 4) * 16 + c * 4 + place % 4;
 }
 
-template <class T, int DP>
+template <class T, int DP, int AUX>
 struct Values {
   static constexpr int W = DP / 16;  // elements per lane and entry
   typedef T vec __attribute__((ext_vector_type(DP / 16)));
@@ -159,13 +162,13 @@ struct Values {
     for (int j = 0; j < 8; ++j) {
       const int at = __builtin_amdgcn_readfirstlane(((j / 4) * 16 + j % 4) * stride);  // a scalar offset
       if constexpr (W == 4) {
-        v[j] = __builtin_bit_cast(vec, load_8(w, off, at));
+        v[j] = __builtin_bit_cast(vec, load_8<AUX>(w, off, at));
       } else if constexpr (W == 8) {
-        v[j] = __builtin_bit_cast(vec, load_16<kStreamed>(w, off, at));
+        v[j] = __builtin_bit_cast(vec, load_16<AUX>(w, off, at));
       } else {
         struct Two {
           uint4 x, y;
-        } two = {load_16<kStreamed>(w, off, at), load_16<kStreamed>(w, off + 16, at)};
+        } two = {load_16<AUX>(w, off, at), load_16<AUX>(w, off + 16, at)};
         v[j] = __builtin_bit_cast(vec, two);
       }
     }
@@ -248,9 +251,10 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 ? 2 : 1) void attend_k
   // last block from an empty window: a branch here would make the compiler
   // wait for the keys where only the values are needed)
   const Keys<T, DP, EXACT> key(a);
-  const uint32_t value_off = Values<T, DP>::value_offset(a);
+  // values that no other wave reads are streamed
+  Values<T, DP, BY_ROWS ? kCached : kStreamed> v;
+  const uint32_t value_off = decltype(v)::value_offset(a);
   pack_t<T> k[2][DP / 32];
-  Values<T, DP> v;
   pack_t<T> q[NT][DP / 32];
   int limit[NT];  // the last entry this lane's row sees
 #pragma unroll
@@ -326,7 +330,9 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 ? 2 : 1) void attend_k
       }
       float top = fmaxf(fmaxf(fmaxf(z[t][0][0], z[t][0][1]), fmaxf(z[t][0][2], z[t][0][3])),
                         fmaxf(fmaxf(z[t][1][0], z[t][1][1]), fmaxf(z[t][1][2], z[t][1][3])));
-      if (__any(top > m[t])) {
+      // A maximum that grows a little stays as it is (weights up to 2^8 do no
+      // harm): the first blocks would otherwise rescale the outputs nearly every time.
+      if (__any(top > m[t] + kSlack)) {
         const float next = fmaxf(m[t], groups_max(top));
         const float f = exp2_of(m[t], next);
         l[t] *= f;
@@ -334,16 +340,15 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 ? 2 : 1) void attend_k
         for (int n = 0; n < W; ++n) o[t][n] *= f;
         m[t] = next;
       }
+      const float base = m[t] == -INFINITY ? 0.0f : m[t];
+      f32x8 p;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = exp2_of(z[t][u][i], m[t]);
-          l[t] += p;
-          hi[t][4 * u + i] = (T)p;
-          lo[t][4 * u + i] = (T)(p - (float)hi[t][4 * u + i]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(z[t][i / 4][i % 4] - base);
+        l[t] += p[i];
       }
+      hi[t] = __builtin_convertvector(p, pack_t<T>);
+      lo[t] = __builtin_convertvector(p - __builtin_convertvector(hi[t], f32x8), pack_t<T>);
     }
     // NaN or infinity among values that some row does not see must not meet
     // that row's zero weights: they are left out here and added by the join

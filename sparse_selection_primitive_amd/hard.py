@@ -22,13 +22,13 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import LapsumError, _check, _workspace, load_library
+from . import EXPORTED, LapsumError, _check, _workspace, load_library
 
 F32, BF16, F16 = 0, 1, 2
 # bound by the first call: the package can be imported without torch
 torch = None
 _TYPES, _FUNCTIONS = {}, {}
-_raw_stream = None
+_raw_stream = _current_device = None
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
 
@@ -68,13 +68,15 @@ def declare(lib):
 
 
 def _bind():
-    global torch, _raw_stream
+    global torch, _raw_stream, _current_device
     import torch as t
-    load_library()
+    lib = load_library()
+    _FUNCTIONS.update({name: getattr(lib, name) for name in EXPORTED})
     _TYPES.update({t.float32: F32, t.bfloat16: BF16, t.float16: F16})
     # torch's raw reader of the current stream takes 0.1 us, its stream object 1.9 us
     raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
     _raw_stream = raw if raw is not None else (lambda index: t.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     torch = t
 
 
@@ -131,11 +133,9 @@ def _rows(x, name):
 
 def _call(dev, name, *args):
     """A library call on a device's current stream (every entry point takes the stream last)."""
-    f = _FUNCTIONS.get(name)
-    if f is None:
-        f = _FUNCTIONS[name] = getattr(load_library(), name)
+    f = _FUNCTIONS[name]
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -242,12 +242,22 @@ def dispatch_plan(chosen, experts):
 
 
 def _slot_of(slot, dev, tokens=None):
-    _gpu(slot, "slot", 2)
-    return _array(slot, "slot", torch.int32, (slot.shape[0] if tokens is None else tokens, slot.shape[1]), dev)
+    """slot as a contiguous int32 [tokens, k] on dev: (slot, tokens, k)."""
+    if not isinstance(slot, torch.Tensor) or slot.device != dev or slot.dim() != 2 or slot.dtype != torch.int32:
+        _gpu(slot, "slot", 2, dev)
+        raise LapsumError("slot must be torch.int32")
+    n, k = slot.shape
+    if tokens is not None and n != tokens:
+        raise LapsumError(f"slot must have {tokens} rows")
+    return (slot if slot.is_contiguous() else slot.contiguous()), n, k
 
 
 def _offsets_of(offsets, dev):
-    return _array(_gpu(offsets, "offsets", 1), "offsets", torch.int32, offsets.shape, dev)
+    if not isinstance(offsets, torch.Tensor) or offsets.device != dev or offsets.dim() != 1 or \
+            offsets.dtype != torch.int32:
+        _gpu(offsets, "offsets", 1, dev)
+        raise LapsumError("offsets must be torch.int32")
+    return offsets if offsets.is_contiguous() else offsets.contiguous()
 
 
 def dispatch_forward(x, slot, offsets, *, out=None):
@@ -255,8 +265,8 @@ def dispatch_forward(x, slot, offsets, *, out=None):
     code = _dtype(_gpu(x, "x", 2), "x")
     x, tokens, width, stride = _rows(x, "x")
     dev = x.device
-    slot, offsets = _slot_of(slot, dev, tokens), _offsets_of(offsets, dev)
-    k = slot.shape[1]
+    slot, _, k = _slot_of(slot, dev, tokens)
+    offsets = _offsets_of(offsets, dev)
     xs = _out(out, "xs", x.dtype, (tokens * k, width), dev)
     if xs.numel() == 0:
         return xs
@@ -269,8 +279,8 @@ def dispatch_backward(dxs, slot, *, out=None):
     """dx [tokens, width]: the sum of each token's rows of dxs."""
     code = _dtype(_gpu(dxs, "dxs", 2), "dxs")
     dev = dxs.device
-    slot = _slot_of(slot, dev)
-    (tokens, k), width = slot.shape, dxs.shape[1]
+    slot, tokens, k = _slot_of(slot, dev)
+    width = dxs.shape[1]
     dxs = _array(dxs, "dxs", dxs.dtype, (tokens * k, width), dev)
     dx = _out(out, "dx", dxs.dtype, (tokens, width), dev)
     if dxs.numel() == 0:
@@ -283,8 +293,8 @@ def combine_forward(ys, slot, weights, *, out=None):
     """y [tokens, width]: y[t] = sum_j weights[t, j] ys[slot[t, j]]."""
     code = _dtype(_gpu(ys, "ys", 2), "ys")
     dev = ys.device
-    slot = _slot_of(slot, dev)
-    (tokens, k), width = slot.shape, ys.shape[1]
+    slot, tokens, k = _slot_of(slot, dev)
+    width = ys.shape[1]
     ys = _array(ys, "ys", ys.dtype, (tokens * k, width), dev)
     weights = _array(weights, "weights", torch.float32, (tokens, k), dev)
     y = _out(out, "y", ys.dtype, (tokens, width), dev)
@@ -300,8 +310,8 @@ def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
     code = _dtype(_gpu(dy, "dy", 2), "dy")
     dy, tokens, width, stride = _rows(dy, "dy")
     dev = dy.device
-    slot, offsets = _slot_of(slot, dev, tokens), _offsets_of(offsets, dev)
-    k = slot.shape[1]
+    slot, _, k = _slot_of(slot, dev, tokens)
+    offsets = _offsets_of(offsets, dev)
     ys = _array(ys, "ys", dy.dtype, (tokens * k, width), dev)
     weights = _array(weights, "weights", torch.float32, (tokens, k), dev)
     dys = _out(None if out is None else out[0], "dys", dy.dtype, (tokens * k, width), dev)
