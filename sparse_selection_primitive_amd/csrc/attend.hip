@@ -34,6 +34,13 @@ constexpr int kAttendWaves = 4;  // waves of a workgroup, taking its blocks in t
 constexpr int kStep = kBlock * kAttendWaves;
 constexpr float kSlack = 8.0f;   // powers of two that a row's weights may exceed 1 by
 constexpr int kMaxSplits = 256;
+// A cache goes to one workgroup whole where that is one block a wave, or where
+// there are enough caches for every compute unit (times of one call from a graph, 32 query
+// heads on 8 of width 128: 200 entries 7.3 us, by splits 8.8; 1000 entries 14.1 and 9.0; 32
+// sequences of up to 1000 21 and 28; 64 of up to 4000 148 and 167).
+constexpr int kWholeShort = 256, kWholeMax = 4096;
+constexpr int kWholeCaches = 256;
+constexpr int kWholeLogits = 16384;  // fp32 logits that it keeps in LDS, at most
 constexpr int kKeepRows = 16;    // up to this many rows the logits are kept for the accounts
 
 LDEV f32x4 mfma(pack_t<bf16> a, pack_t<bf16> b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -203,6 +210,159 @@ struct Values {
   }
 };
 
+// What becomes of a block's logits: kept in the workspace for the accounts, kept in
+// LDS, or dropped.
+struct KeepNone {
+  LDEV void operator()(int, int, f32x4, f32x4) const {}
+};
+struct KeepFar {  // [blocks][rows][32]
+  float *logits;
+  int rows, row;  // row: this lane's of the first tile
+  // rows past the last one go nowhere; no branch, so the waits for the loads stay exact
+  LDEV void operator()(int e0, int t, f32x4 z0, f32x4 z1) const {
+    const window_t to = window_of(logits + (int64_t)(e0 / kBlock) * rows * kBlock,
+                                  (int64_t)rows * kBlock * (int64_t)sizeof(float));
+    const int c = (threadIdx.x % 64) / 16, at = ((row + 16 * t) * kBlock + 4 * c) * (int)sizeof(float);
+    store_16(to, (uint32_t)at, 0, z0);
+    store_16(to, (uint32_t)at, 64, z1);
+  }
+};
+struct KeepNear {  // [rows][stride], one tile of rows
+  float *logits;
+  int rows, stride;
+  LDEV void operator()(int e0, int, f32x4 z0, f32x4 z1) const {
+    const int lane = threadIdx.x % 64, c = lane / 16, r = lane % 16;
+    if (r >= rows) return;
+    float *to = logits + r * stride + e0 + 4 * c;
+    *reinterpret_cast<f32x4 *>(to) = z0;
+    *reinterpret_cast<f32x4 *>(to + 16) = z1;
+  }
+};
+
+// One wave's pass over the blocks first, first + stride, .. of the entries up to
+// `end`, for 16 * NT rows from row0: the rows' maxima, their sums (this lane's
+// share) and outputs.  Returns whether values were left out (see drop()).
+template <class T, int DP, int NT, bool EXACT, bool ONE, int AUX, class Keep>
+LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, int first, int end, int stride,
+                         const Keep keep, float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][DP / 16]) {
+  constexpr int W = DP / 16;
+  const int lane = threadIdx.x % 64, c = lane / 16, r = lane % 16;
+  const int64_t b = bh / a.heads, h = bh % a.heads;
+  const T *keys = static_cast<const T *>(a.k) + b * a.kb + h * a.kh;
+  const T *values = static_cast<const T *>(a.v) + b * a.vb + h * a.vh;
+
+  // a block's keys are asked for as soon as the last block's are used up, its
+  // values likewise, so each is on its way while the other is worked on (past the
+  // last block from an empty window: a branch here would make the compiler
+  // wait for the keys where only the values are needed)
+  const Keys<T, DP, EXACT> key(a);
+  Values<T, DP, AUX> v;
+  const uint32_t value_off = decltype(v)::value_offset(a);
+  pack_t<T> k[2][DP / 32];
+  pack_t<T> q[NT][DP / 32];
+  int limit[NT];  // the last entry this lane's row sees
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + 16 * t + r;
+    load_queries<T, DP>(a, bh, row, q[t]);
+    limit[t] = length - a.news + row / a.group;
+  }
+  // the order of the loads is the loop's: keys before values
+  __builtin_amdgcn_sched_barrier(0);
+  {
+    const window_t w = entries(keys, a.ke, first, end, a.width);
+    key.load(w, 0, k[0]);
+    key.load(w, 16, k[1]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  v.load(entries(values, a.ve, first, end, a.width), value_off, (int)a.ve * 2);
+  __builtin_amdgcn_sched_barrier(0);
+
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = -INFINITY;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < W; ++n) o[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  bool dropped = false;
+  for (int e0 = first; e0 < end; e0 += stride) {
+    f32x4 z[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      z[t][0] = z[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        z[t][0] = mfma(k[0][i], q[t][i], z[t][0]);
+        z[t][1] = mfma(k[1][i], q[t][i], z[t][1]);
+      }
+    }
+    const window_t next_keys = entries(keys, a.ke, e0 + stride, end, a.width);
+    key.load(next_keys, 0, k[0]);
+    key.load(next_keys, 16, k[1]);
+    // some row does not see some entry of the block
+    const bool edge = e0 + kBlock > end || e0 + kBlock - 1 > length - a.news;
+    // the weights go into the product in two parts, so they keep 16 bits or more of their mantissa there
+    pack_t<T> hi[NT], lo[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[t][u][i] *= a.scale_log2;
+        }
+      }
+      if (edge) {
+        const int most = min(limit[t], end - 1) - e0 - 4 * c;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * u + i > most) z[t][u][i] = -INFINITY;
+        }
+      }
+      keep(e0, t, z[t][0], z[t][1]);
+      float top = fmaxf(fmaxf(fmaxf(z[t][0][0], z[t][0][1]), fmaxf(z[t][0][2], z[t][0][3])),
+                        fmaxf(fmaxf(z[t][1][0], z[t][1][1]), fmaxf(z[t][1][2], z[t][1][3])));
+      // A maximum that grows a little stays as it is (weights up to 2^8 do no
+      // harm): the first blocks would otherwise rescale the outputs nearly every time.
+      if (__any(top > m[t] + kSlack)) {
+        const float next = fmaxf(m[t], groups_max(top));
+        const float f = exp2_of(m[t], next);
+        l[t] *= f;
+#pragma unroll
+        for (int n = 0; n < W; ++n) o[t][n] *= f;
+        m[t] = next;
+      }
+      const float base = m[t] == -INFINITY ? 0.0f : m[t];
+      f32x8 p;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(z[t][i / 4][i % 4] - base);
+        l[t] += p[i];
+      }
+      hi[t] = __builtin_convertvector(p, pack_t<T>);
+      lo[t] = __builtin_convertvector(p - __builtin_convertvector(hi[t], f32x8), pack_t<T>);
+    }
+    // NaN or infinity among values that some row does not see must not meet
+    // that row's zero weights: they are left out here and added by the join
+    if (!ONE && edge) dropped |= v.drop();
+#pragma unroll
+    for (int n = 0; n < W; ++n) {
+      const pack_t<T> col = v.column(n);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[t][n] = mfma(col, hi[t], o[t][n]);
+        o[t][n] = mfma(col, lo[t], o[t][n]);
+      }
+    }
+    v.load(entries(values, a.ve, e0 + stride, end, a.width), value_off, (int)a.ve * 2);
+  }
+  return dropped;
+}
+
 // The waves of a workgroup share its entries (BY_ROWS false: few rows, so the
 // entries' bytes are what counts; a wave takes every fourth block and the
 // waves are joined at the end) or its rows (BY_ROWS: every wave goes through
@@ -240,129 +400,18 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 ? 2 : 1) void attend_k
     if (!ONE && threadIdx.x == 0) a.dropped[bh * a.splits + split] = 0;
     return;
   }
-  const int64_t b = bh / a.heads, h = bh % a.heads;
-  const T *keys = static_cast<const T *>(a.k) + b * a.kb + h * a.kh;
-  const T *values = static_cast<const T *>(a.v) + b * a.vb + h * a.vh;
   constexpr int kStride = BY_ROWS ? kBlock : kStep;
   const int first = begin + (BY_ROWS ? 0 : wave * kBlock);
-
-  // a block's keys are asked for as soon as the last block's are used up, its
-  // values likewise, so each is on its way while the other is worked on (past the
-  // last block from an empty window: a branch here would make the compiler
-  // wait for the keys where only the values are needed)
-  const Keys<T, DP, EXACT> key(a);
   // values that no other wave reads are streamed
-  Values<T, DP, BY_ROWS ? kCached : kStreamed> v;
-  const uint32_t value_off = decltype(v)::value_offset(a);
-  pack_t<T> k[2][DP / 32];
-  pack_t<T> q[NT][DP / 32];
-  int limit[NT];  // the last entry this lane's row sees
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int row = row0 + 16 * t + r;
-    load_queries<T, DP>(a, bh, row, q[t]);
-    limit[t] = length - a.news + row / a.group;
-  }
-  // the order of the loads is the loop's: keys before values
-  __builtin_amdgcn_sched_barrier(0);
-  {
-    const window_t w = entries(keys, a.ke, first, end, a.width);
-    key.load(w, 0, k[0]);
-    key.load(w, 16, k[1]);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  v.load(entries(values, a.ve, first, end, a.width), value_off, (int)a.ve * 2);
-  __builtin_amdgcn_sched_barrier(0);
-
+  constexpr int AUX = BY_ROWS ? kCached : kStreamed;
   float m[NT], l[NT];
   f32x4 o[NT][W];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = -INFINITY;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < W; ++n) o[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  bool dropped = false;
-  for (int e0 = first; e0 < end; e0 += kStride) {
-    f32x4 z[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      z[t][0] = z[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        z[t][0] = mfma(k[0][i], q[t][i], z[t][0]);
-        z[t][1] = mfma(k[1][i], q[t][i], z[t][1]);
-      }
-    }
-    const window_t next_keys = entries(keys, a.ke, e0 + kStride, end, a.width);
-    key.load(next_keys, 0, k[0]);
-    key.load(next_keys, 16, k[1]);
-    // some row does not see some entry of the block
-    const bool edge = e0 + kBlock > end || e0 + kBlock - 1 > length - a.news;
-    // the weights go into the product in two parts, so they keep 16 bits or more of their mantissa there
-    pack_t<T> hi[NT], lo[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[t][u][i] *= a.scale_log2;
-        }
-      }
-      if (edge) {
-        const int most = min(limit[t], end - 1) - e0 - 4 * c;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (16 * u + i > most) z[t][u][i] = -INFINITY;
-        }
-      }
-      if constexpr (KEEP) {  // rows past the last one go nowhere; no branch, so the waits for the loads stay exact
-        const window_t to = window_of(a.logits + (bh * a.blocks + e0 / kBlock) * a.rows * kBlock,
-                                      (int64_t)a.rows * kBlock * (int64_t)sizeof(float));
-        const int at = ((row0 + 16 * t + r) * kBlock + 4 * c) * (int)sizeof(float);
-        store_16(to, (uint32_t)at, 0, z[t][0]);
-        store_16(to, (uint32_t)at, 64, z[t][1]);
-      }
-      float top = fmaxf(fmaxf(fmaxf(z[t][0][0], z[t][0][1]), fmaxf(z[t][0][2], z[t][0][3])),
-                        fmaxf(fmaxf(z[t][1][0], z[t][1][1]), fmaxf(z[t][1][2], z[t][1][3])));
-      // A maximum that grows a little stays as it is (weights up to 2^8 do no
-      // harm): the first blocks would otherwise rescale the outputs nearly every time.
-      if (__any(top > m[t] + kSlack)) {
-        const float next = fmaxf(m[t], groups_max(top));
-        const float f = exp2_of(m[t], next);
-        l[t] *= f;
-#pragma unroll
-        for (int n = 0; n < W; ++n) o[t][n] *= f;
-        m[t] = next;
-      }
-      const float base = m[t] == -INFINITY ? 0.0f : m[t];
-      f32x8 p;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(z[t][i / 4][i % 4] - base);
-        l[t] += p[i];
-      }
-      hi[t] = __builtin_convertvector(p, pack_t<T>);
-      lo[t] = __builtin_convertvector(p - __builtin_convertvector(hi[t], f32x8), pack_t<T>);
-    }
-    // NaN or infinity among values that some row does not see must not meet
-    // that row's zero weights: they are left out here and added by the join
-    if (!ONE && edge) dropped |= v.drop();
-#pragma unroll
-    for (int n = 0; n < W; ++n) {
-      const pack_t<T> col = v.column(n);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        o[t][n] = mfma(col, hi[t], o[t][n]);
-        o[t][n] = mfma(col, lo[t], o[t][n]);
-      }
-    }
-    v.load(entries(values, a.ve, e0 + kStride, end, a.width), value_off, (int)a.ve * 2);
+  bool dropped;
+  if constexpr (KEEP) {
+    const KeepFar keep{a.logits + bh * a.blocks * a.rows * kBlock, a.rows, row0 + r};
+    dropped = attend_entries<T, DP, NT, EXACT, ONE, AUX>(a, bh, row0, length, first, end, kStride, keep, m, l, o);
+  } else {
+    dropped = attend_entries<T, DP, NT, EXACT, ONE, AUX>(a, bh, row0, length, first, end, kStride, KeepNone(), m, l, o);
   }
 
   int *const flag = a.dropped + bh * a.splits + split;
@@ -438,6 +487,128 @@ __global__ __launch_bounds__(64 * kAttendWaves, DP <= 128 ? 2 : 1) void attend_k
   }
 }
 
+// Infinities and NaN among the values of the newest entries that the products
+// left out, added to four elements of a row's output (one that they did not leave out is in
+// the sum already, and stays).
+template <class T>
+LDEV void add_dropped(const AttendArgs &a, int64_t bh, int row, int length, int d, f32x4 &o) {
+  const int64_t b = bh / a.heads, h = bh % a.heads;
+  const T *v = static_cast<const T *>(a.v) + b * a.vb + h * a.vh + d;
+  const int last = length - a.news + row / a.group;
+  for (int e = max(0, length - a.news - kBlock); e <= last; ++e) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float x = (float)v[(int64_t)e * a.ve + n];
+      if (!(fabsf(x) < INFINITY)) o[n] += x;
+    }
+  }
+}
+
+template <class T>
+LDEV void store_out(const AttendArgs &a, int64_t bh, int row, int d, f32x4 o) {
+  typedef T vec4 __attribute__((ext_vector_type(4)));
+  T *out = const_cast<T *>(query_row<T>(a, bh, row) - static_cast<const T *>(a.q) + static_cast<T *>(a.out));
+  *reinterpret_cast<vec4 *>(out + d) = vec4{(T)o[0], (T)o[1], (T)o[2], (T)o[3]};
+}
+
+// A short cache by one workgroup: its logits stay in LDS, so output and
+// accounts are finished here, without a workspace and a second launch.
+constexpr int whole_waves(int dp) { return dp <= 128 ? 8 : 4; }  // 8 waves have 256 registers each
+template <class T, int DP, bool EXACT, bool ONE>
+__global__ __launch_bounds__(64 * whole_waves(DP)) void attend_whole_kernel(const AttendArgs a, const int logit_stride) {
+  constexpr int W = DP / 16, WAVES = whole_waves(DP), kPad = DP + 4;
+  struct Shared {
+    float m[WAVES][16], l[WAVES][16];
+    float lse[16], inv[16];
+    int dropped[WAVES];
+    float o[4][16][kPad];
+  };
+  __shared__ Shared sh;
+  extern __shared__ float logits[];  // [rows][logit_stride]
+  lds_poison(sh);
+  const int64_t bh = grid_row();
+  if (bh >= (int64_t)a.batch * a.heads) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lane = threadIdx.x % 64, c = lane / 16, r = lane % 16;
+  const int length = length_of(a, bh);
+
+  float m[1], l[1];
+  f32x4 o[1][W];
+  bool dropped;
+  if (a.account_out != nullptr) {
+    dropped = attend_entries<T, DP, 1, EXACT, ONE, kStreamed>(a, bh, 0, length, wave * kBlock, length, WAVES * kBlock,
+                                                              KeepNear{logits, a.rows, logit_stride}, m, l, o);
+  } else {
+    dropped = attend_entries<T, DP, 1, EXACT, ONE, kStreamed>(a, bh, 0, length, wave * kBlock, length, WAVES * kBlock,
+                                                              KeepNone(), m, l, o);
+  }
+  l[0] = groups_sum(l[0]);
+  if (c == 0) {
+    sh.m[wave][r] = m[0];
+    sh.l[wave][r] = l[0];
+  }
+  if constexpr (!ONE) sh.dropped[wave] = __any(dropped) ? 1 : 0;
+  __syncthreads();
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sh.m[w][r]);
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) sum += exp2_of(sh.m[w][r], top) * sh.l[w][r];
+  if (wave == 0 && c == 0) {
+    sh.lse[r] = sum > 0.0f ? top + log2f(sum) : (sum == 0.0f ? INFINITY : sum);
+    sh.inv[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+  }
+  const float f = exp2_of(m[0], top);
+#pragma unroll
+  for (int n = 0; n < W; ++n) o[0][n] *= f;
+  // the waves' outputs in four buffers, the upper half's handed to the lower half's waves first
+  const auto each = [&](auto use) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int n = 0; n < W; n += 4)
+        use(*reinterpret_cast<f32x4 *>(&sh.o[wave & 3][r][(4 * c + i) * W + n]), n, i);
+    }
+  };
+  const auto put = [&](f32x4 &at, int n, int i) {
+    at = f32x4{o[0][n][i], o[0][n + 1][i], o[0][n + 2][i], o[0][n + 3][i]};
+  };
+  if constexpr (WAVES > 4) {
+    if (wave >= 4) each(put);
+    __syncthreads();
+    if (wave < 4) {
+      each([&](f32x4 &at, int n, int i) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[0][n + x][i] += at[x];
+      });
+    }
+    // a wave reads and writes the same places, so no barrier in between
+  }
+  if (wave < 4) each(put);
+  __syncthreads();
+  bool again = false;
+  if constexpr (!ONE) {
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) again |= sh.dropped[w] != 0;
+  }
+  const int packs = a.width / 4;
+  for (int i = threadIdx.x; i < a.rows * packs; i += blockDim.x) {
+    const int row = i / packs, d = (i % packs) * 4;
+    f32x4 x = *reinterpret_cast<const f32x4 *>(&sh.o[0][row][d]);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) x += *reinterpret_cast<const f32x4 *>(&sh.o[w][row][d]);
+    x *= sh.inv[row];
+    if (again) add_dropped<T>(a, bh, row, length, d, x);
+    store_out<T>(a, bh, row, d, x);
+  }
+  if (a.account_out == nullptr) return;
+  for (int e = threadIdx.x; e < length; e += blockDim.x) {
+    float w = 0.0f;
+    for (int i = 0; i < a.rows; ++i) w += __builtin_amdgcn_exp2f(logits[i * logit_stride + e] - sh.lse[i]);
+    a.account_out[bh * a.capacity + e] = a.account[bh * a.capacity + e] + w;
+  }
+}
+
 // The splits' maxima and sums of a row as one, by a team of 16 lanes: its
 // lse in units of log2 (+inf for a row that sees nothing, so its weights are 0).
 LDEV float row_lse(const AttendArgs &a, int64_t bh, int row) {
@@ -504,23 +675,8 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   for (int t = 1; t < teams; ++t) o += sh.o[t * packs + tid];
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   o *= inv;
-  if (again) {
-    // infinities and NaN that the products left out, of the entries this row
-    // sees (one that they did not leave out is in the sum already, and stays)
-    const int length = length_of(a, bh), last = length - a.news + row / a.group;
-    const int64_t b = bh / a.heads, h = bh % a.heads;
-    const T *v = static_cast<const T *>(a.v) + b * a.vb + h * a.vh + d;
-    for (int e = max(0, length - a.news - kBlock); e <= last; ++e) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float x = (float)v[(int64_t)e * a.ve + n];
-        if (!(fabsf(x) < INFINITY)) o[n] += x;
-      }
-    }
-  }
-  typedef T vec4 __attribute__((ext_vector_type(4)));
-  T *out = const_cast<T *>(query_row<T>(a, bh, row) - static_cast<const T *>(a.q) + static_cast<T *>(a.out));
-  *reinterpret_cast<vec4 *>(out + d) = vec4{(T)o[0], (T)o[1], (T)o[2], (T)o[3]};
+  if (again) add_dropped<T>(a, bh, row, length_of(a, bh), d, o);
+  store_out<T>(a, bh, row, d, o);
 }
 
 // The first a.rows workgroups of a cache join its rows; the others add up the
@@ -674,11 +830,23 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
       <<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);
   return hipGetLastError();
 }
+// LDS floats per row of a whole cache's logits: whole blocks, and four more so that the rows' 16-byte
+// accesses fall on all banks
+int whole_stride(int64_t capacity) { return (int)((capacity + kBlock - 1) / kBlock * kBlock + 4); }
+
 // 16 rows are one tile of the matrix instruction, 32 two that share the
 // entries (ONE: a single new token, whose row sees every entry); beyond, the waves take rows of their own.  32 rows of 256 elements would not
 // fit a wave's registers.
 template <class T, int DP, bool EXACT>
 hipError_t attend_rows(const AttendArgs &a, hipStream_t s) {
+  if (a.splits == 0) {  // whole caches
+    const int stride = whole_stride(a.capacity);
+    const size_t lds = a.account_out != nullptr ? (size_t)a.rows * stride * sizeof(float) : 0;
+    const dim3 grid = rows_grid(1, (int64_t)a.batch * a.heads), threads(64 * whole_waves(DP));
+    if (a.news == 1) attend_whole_kernel<T, DP, EXACT, true><<<grid, threads, lds, s>>>(a, stride);
+    else attend_whole_kernel<T, DP, EXACT, false><<<grid, threads, lds, s>>>(a, stride);
+    return hipGetLastError();
+  }
   const bool keep = a.logits != nullptr;  // at most 16 rows
   if (a.rows <= 16) {
     if (a.news == 1)
@@ -708,6 +876,9 @@ AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t r
                        bool accounts) {
   AttendPlan p{};
   const int64_t caches = batch * heads;
+  if (rows <= 16 && capacity <= (caches >= kWholeCaches ? kWholeMax : kWholeShort) &&
+      rows * whole_stride(capacity) <= kWholeLogits)
+    return p;  // whole caches
   // rows per workgroup, as attend_rows() chooses them
   const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)) : 64);
   const int64_t groups = caches * ((rows + rows_per - 1) / rows_per);

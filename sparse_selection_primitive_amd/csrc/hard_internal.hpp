@@ -62,7 +62,7 @@ struct AttendArgs {
   int64_t capacity;
   const int32_t *lengths;
   float scale_log2;                // scale * log2(e)
-  int splits;                      // workgroups a cache is shared by
+  int splits;                      // workgroups a cache is shared by; 0: one does it all, without a workspace
   const float *account;
   float *account_out;              // NULL: no accounts
   void *out;

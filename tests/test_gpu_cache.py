@@ -382,3 +382,29 @@ def test_evict_refusals(L):
                 lambda: L.cache_evict(k.float(), v.float(), a, p, n, 5)):
         with pytest.raises(L.LapsumError):
             bad()
+
+
+@pytest.mark.parametrize("news,group,width", [(1, 4, 64), (1, 16, 128), (3, 2, 96), (1, 1, 256), (2, 5, 64)])
+@pytest.mark.parametrize("capacity", [1, 31, 256, 700, 1500])
+def test_many_short_caches(L, capacity, news, group, width):
+    """260 caches: each is finished by one workgroup where its logits fit, with and without accounts."""
+    lengths = [max(0, capacity - 3 * i) for i in range(130)]
+    k, v = cache(130, 2, capacity, width, "bf16", seed=capacity + width)
+    few = [0, 1, 7, 129]
+    q = query(130, news, 2 * group, width, "bf16")
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    account = torch.rand(130, 2, capacity, device="cuda")
+    apart = torch.full_like(account, -7.0)
+    out = L.cache_attend(q.cuda(), k.cuda(), v.cuda(), n, account, account_out=apart)
+    # the same sequences by themselves (checked against the plain form), whatever their number chose
+    pick = torch.tensor(few)
+    alone = check_attend(L, q[pick], k[pick], v[pick], [lengths[i] for i in few], "bf16")
+    assert (out[pick.cuda()].float() - alone.float()).abs().max() <= 2.0 ** -7 * (1 + alone.float().abs().max())
+    check_attend(L, q[:3].repeat(44, 1, 1, 1)[:130], k[:3].repeat(44, 1, 1, 1)[:130], v[:3].repeat(44, 1, 1, 1)[:130],
+                 [lengths[i % 3] for i in range(130)], "bf16") if capacity <= 31 else None
+    for b in few:
+        m = lengths[b]
+        want = plain.attend(q[b:b + 1].double(), k[b:b + 1].double(), v[b:b + 1].double(), [m], width ** -0.5)[1]
+        got = apart[b].double().cpu() - account[b].double().cpu()
+        assert (got[:, :m] - want[0, :, :m]).abs().max() <= 1e-5 * news * group if m else True
+        assert (apart[b, :, m:] == -7.0).all()

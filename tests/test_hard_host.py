@@ -110,9 +110,12 @@ def test_attend_checks(lib):
     assert call(c, q=P + 2) == LAYOUT and call(c, out=P + 2) == LAYOUT
     assert call(c, q=None) == NULL and call(c, lengths=None) == NULL and call(c, out=None) == NULL
     assert call(c, account=None) == NULL and call(c, account_out=None) == NULL
-    need = lib.lapsum_cache_attend_workspace_bytes(c, 1, 4, 1)
-    assert need >= lib.lapsum_cache_attend_workspace_bytes(c, 1, 4, 0) > 0
-    assert call(c, nbytes=need - 1) == WORKSPACE and call(c, ws=P + 8) == WORKSPACE and call(c, ws=None) == NULL
+    assert lib.lapsum_cache_attend_workspace_bytes(c, 1, 4, 1) == 0  # short caches need none
+    long = cache(capacity=100000, kh=6400000, kb=12800000, vh=6400000, vb=12800000)
+    need = lib.lapsum_cache_attend_workspace_bytes(long, 1, 4, 1)
+    assert need >= lib.lapsum_cache_attend_workspace_bytes(long, 1, 4, 0) > 0
+    assert call(long, nbytes=need - 1) == WORKSPACE and call(long, ws=P + 8) == WORKSPACE
+    assert call(long, ws=None) == NULL
     assert lib.lapsum_cache_attend_workspace_bytes(cache(width=4), 1, 4, 1) == 0
 
 
