@@ -101,6 +101,30 @@ def build(jobs: int | None = None, out: str = LIB, defines=()) -> str:
     return out
 
 
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def build_binding(out: str = BINDING) -> str:
+    """The native front of the hard selections' Python binding (csrc/binding.cpp): host code only, against torch's
+    headers and libraries."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    tmp = out + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in includes], os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib}", "-lc10", "-lc10_hip",
+           "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building the native binding failed:\n{res.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 POISON_LIB = os.path.join(HERE, "liblapsum_ldspoison.so")
 
 
@@ -113,3 +137,4 @@ def build_lds_poison(jobs: int | None = None) -> str:
 
 if __name__ == "__main__":
     print(build())
+    print(build_binding())

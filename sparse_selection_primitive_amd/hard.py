@@ -21,6 +21,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
+import os
 
 from . import EXPORTED, LapsumError, _check, _workspace, load_library
 
@@ -29,6 +31,13 @@ F32, BF16, F16 = 0, 1, 2
 torch = None
 _TYPES, _FUNCTIONS = {}, {}
 _raw_stream = _current_device = None
+# the native front (csrc/binding.cpp): it takes the calls whose arguments need no conversion and returns None for all
+# others, which then go the way written out below.  Without the built file every call does.
+_native = None
+_NATIVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+_NATIVE_CALLS = ["route_forward", "route_backward", "dispatch_plan_workspace_bytes", "dispatch_plan",
+                 "dispatch_forward", "dispatch_backward", "combine_forward", "combine_backward",
+                 "cache_attend_workspace_bytes", "cache_attend", "cache_evict_workspace_bytes", "cache_evict"]
 SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
 
@@ -68,7 +77,7 @@ def declare(lib):
 
 
 def _bind():
-    global torch, _raw_stream, _current_device
+    global torch, _raw_stream, _current_device, _native
     import torch as t
     lib = load_library()
     _FUNCTIONS.update({name: getattr(lib, name) for name in EXPORTED})
@@ -78,6 +87,12 @@ def _bind():
     _raw_stream = raw if raw is not None else (lambda index: t.cuda.current_stream(index).cuda_stream)
     _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
     torch = t
+    if os.path.exists(_NATIVE_PATH):
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", _NATIVE_PATH)
+        native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(native)
+        native.bind(*[ctypes.cast(getattr(lib, "lapsum_" + name), ctypes.c_void_p).value for name in _NATIVE_CALLS])
+        _native = native
 
 
 # ----------------------------------------------------------------- checks
@@ -162,6 +177,10 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
     by default); the weights are the chosen scores (without the bias), divided
     by their sum if renormalise, times scale.  A slot without an available
     expert holds -1 and weight 0.  out: (weights, chosen) to write into."""
+    if _native is not None and out is None:
+        done = _native.route_forward(logits, bias, k, SCORES.get(score, -1), groups, top_groups, renormalise, scale)
+        if done is not None:
+            return done
     code = _dtype(_gpu(logits, "logits", 2), "logits")
     x, tokens, experts, stride = _rows(logits, "logits")
     dev = x.device
@@ -180,6 +199,10 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
 def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=True, scale=1.0, out=None):
     """dlogits [tokens, experts], of the logits' type: the gradient of the weights, the choice held fixed
     (score, renormalise and scale as in the forward)."""
+    if _native is not None and out is None:
+        done = _native.route_backward(dweights, logits, chosen, SCORES.get(score, -1), renormalise, scale)
+        if done is not None:
+            return done
     code = _dtype(_gpu(logits, "logits", 2), "logits")
     x, tokens, experts, stride = _rows(logits, "logits")
     dev = x.device
@@ -225,6 +248,10 @@ def dispatch_plan(chosen, experts):
     """The expert order of the (token, choice) pairs of chosen [tokens, k]:
     offsets int32 [experts + 1] (expert e's rows are offsets[e]:offsets[e + 1]), slot int32 [tokens, k] (a pair's row, -1
     for entries that name no expert) and order int32 [tokens * k] (the pair t * k + j of a row, -1 behind the last)."""
+    if _native is not None:
+        done = _native.dispatch_plan(chosen, experts)
+        if done is not None:
+            return done
     _gpu(chosen, "chosen", 2)
     (tokens, k), dev, experts = chosen.shape, chosen.device, int(experts)
     chosen = _array(chosen, "chosen", torch.int32, (tokens, k), dev)
@@ -262,6 +289,10 @@ def _offsets_of(offsets, dev):
 
 def dispatch_forward(x, slot, offsets, *, out=None):
     """xs [tokens * k, width]: token rows in expert order, xs[slot[t, j]] = x[t] (rows behind the last pair zero)."""
+    if _native is not None and out is None:
+        done = _native.dispatch_forward(x, slot, offsets)
+        if done is not None:
+            return done
     code = _dtype(_gpu(x, "x", 2), "x")
     x, tokens, width, stride = _rows(x, "x")
     dev = x.device
@@ -277,6 +308,10 @@ def dispatch_forward(x, slot, offsets, *, out=None):
 
 def dispatch_backward(dxs, slot, *, out=None):
     """dx [tokens, width]: the sum of each token's rows of dxs."""
+    if _native is not None and out is None:
+        done = _native.dispatch_backward(dxs, slot)
+        if done is not None:
+            return done
     code = _dtype(_gpu(dxs, "dxs", 2), "dxs")
     dev = dxs.device
     slot, tokens, k = _slot_of(slot, dev)
@@ -291,6 +326,10 @@ def dispatch_backward(dxs, slot, *, out=None):
 
 def combine_forward(ys, slot, weights, *, out=None):
     """y [tokens, width]: y[t] = sum_j weights[t, j] ys[slot[t, j]]."""
+    if _native is not None and out is None:
+        done = _native.combine_forward(ys, slot, weights)
+        if done is not None:
+            return done
     code = _dtype(_gpu(ys, "ys", 2), "ys")
     dev = ys.device
     slot, tokens, k = _slot_of(slot, dev)
@@ -307,6 +346,10 @@ def combine_forward(ys, slot, weights, *, out=None):
 
 def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
     """dys [tokens * k, width] and dweights fp32 [tokens, k]: dys[slot] = w dy[t], dweights = <dy[t], ys[slot]>."""
+    if _native is not None and out is None:
+        done = _native.combine_backward(dy, ys, slot, weights, offsets)
+        if done is not None:
+            return done
     code = _dtype(_gpu(dy, "dy", 2), "dy")
     dy, tokens, width, stride = _rows(dy, "dy")
     dev = dy.device
@@ -388,6 +431,10 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     [batch, heads, capacity, width] whose first lengths[b] entries are filled, the new tokens' own last (token i sees
     the entries up to lengths[b] - news + i).  account fp32 [batch, heads, capacity]: each entry's weight, summed over
     the new tokens and the query heads of its key head, is added to it, in place or into account_out.  scale: 1/sqrt(width) by default."""
+    if _native is not None and out is None:
+        done = _native.cache_attend(q, k, v, lengths, account, scale, account_out)
+        if done is not None:
+            return done
     cache = _cache_of(k, v)
     dev = k.device
     _gpu(q, "q", 4, dev)
@@ -432,6 +479,11 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
 
     Returns kept int32 [batch, heads, keep] (the slot each entry came from, -1 behind the last) and the new lengths
     (a new tensor)."""
+    if _native is not None:
+        done = _native.cache_evict(k, v, account, positions, lengths, keep, next_position, sinks, recent, account_out,
+                                   positions_out)
+        if done is not None:
+            return done
     cache = _cache_of(k, v)
     dev, batch, keep = k.device, k.shape[0], int(keep)
     shape = k.shape[:3]
