@@ -19,6 +19,15 @@
 // its entries 4c..4c+3 and 16+4c..16+4c+3.  For V' a lane needs one element of eight
 // entries: it loads the width/16 contiguous elements of each of its entries
 // (16 lanes read whole rows) and transposes them in registers.
+//
+// What bounds it.  A few rows: memory.  Without accounts 200001 entries of 8
+// key heads (819 MB) take 132 us, 6.2 TB/s, what a kernel that only reads reaches; the
+// kept logits add 52 MB of writes, which among the reads cost as much as 200 MB of them (a copy of the
+// access pattern without arithmetic shows the same), 165 us and 16 us for the
+// join.  Many rows: the matrix instructions (16 cycles for 16 rows, 32 entries and 32 elements) and
+// the vector instructions beside them, which share the issue of the one wave that
+// fits a SIMD: 128 rows over 16384 entries of 16 key heads take 47 us (25.8 Gflop with the two parts
+// of the weights, 550 Tflop/s) and 27 us for the accounts.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -91,10 +100,11 @@ LDEV void load_queries(const AttendArgs &a, int64_t bh, int row, pack_t<T> (&q)[
   }
 }
 
-// A window of memory that buffer loads are held to: what lies past its end
-// reads as zero.  Entries are reached through a window that starts at the block's first
-// one, so a load's address is the window (scalar registers), an offset of the lane that
-// stays the same from block to block, and a scalar offset.
+// A window of memory that buffer accesses are held to: what lies past its end
+// reads as zero and is not written.  Entries are reached through a window that starts at the
+// block's first one, so a load's address is the window (scalar registers) and a 32-bit
+// offset of the lane that stays the same from block to block.  All of the
+// offset is the lane's: an instruction's scalar offset need not count in the check.
 using window_t = __amdgpu_buffer_rsrc_t;
 LDEV window_t window_of(const void *first, int64_t bytes) {
   const int64_t most = 0x7FFFFFF0;
@@ -108,16 +118,16 @@ constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
 // cache the other halves are fetched again.
 constexpr int kCached = 0, kStreamed = 2;
 template <int AUX>
-LDEV uint4 load_16(window_t w, uint32_t lane_offset, int offset) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)lane_offset, offset, AUX));
+LDEV uint4 load_16(window_t w, uint32_t offset) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)offset, 0, AUX));
 }
 template <int AUX>
-LDEV uint2 load_8(window_t w, uint32_t lane_offset, int offset) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)lane_offset, offset, AUX));
+LDEV uint2 load_8(window_t w, uint32_t offset) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(w, (int)offset, 0, AUX));
 }
 
-LDEV void store_16(window_t w, uint32_t lane_offset, int offset, f32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), w, (int)lane_offset, offset, 0);
+LDEV void store_16(window_t w, uint32_t offset, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), w, (int)offset, 0, 0);
 }
 
 // the entries [first, end) of keys or values; none where first >= end
@@ -148,7 +158,7 @@ struct Keys {
   LDEV void load(window_t w, int at, pack_t<T> (&k)[kSteps]) const {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      k[i] = __builtin_bit_cast(pack_t<T>, load_16<kCached>(w, off[EXACT ? 0 : i] + i * 64, at * stride));
+      k[i] = __builtin_bit_cast(pack_t<T>, load_16<kCached>(w, off[EXACT ? 0 : i] + (uint32_t)(at * stride) + i * 64));
   }
 };
 
@@ -167,15 +177,15 @@ struct Values {
   LDEV void load(window_t w, uint32_t off, int stride) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int at = __builtin_amdgcn_readfirstlane(((j / 4) * 16 + j % 4) * stride);  // a scalar offset
+      const uint32_t at = off + (uint32_t)(((j / 4) * 16 + j % 4) * stride);
       if constexpr (W == 4) {
-        v[j] = __builtin_bit_cast(vec, load_8<AUX>(w, off, at));
+        v[j] = __builtin_bit_cast(vec, load_8<AUX>(w, at));
       } else if constexpr (W == 8) {
-        v[j] = __builtin_bit_cast(vec, load_16<AUX>(w, off, at));
+        v[j] = __builtin_bit_cast(vec, load_16<AUX>(w, at));
       } else {
         struct Two {
           uint4 x, y;
-        } two = {load_16<AUX>(w, off, at), load_16<AUX>(w, off + 16, at)};
+        } two = {load_16<AUX>(w, at), load_16<AUX>(w, at + 16)};
         v[j] = __builtin_bit_cast(vec, two);
       }
     }
@@ -223,8 +233,8 @@ struct KeepFar {  // [blocks][rows][32]
     const window_t to = window_of(logits + (int64_t)(e0 / kBlock) * rows * kBlock,
                                   (int64_t)rows * kBlock * (int64_t)sizeof(float));
     const int c = (threadIdx.x % 64) / 16, at = ((row + 16 * t) * kBlock + 4 * c) * (int)sizeof(float);
-    store_16(to, (uint32_t)at, 0, z0);
-    store_16(to, (uint32_t)at, 64, z1);
+    store_16(to, (uint32_t)at, z0);
+    store_16(to, (uint32_t)at + 64, z1);
   }
 };
 struct KeepNear {  // [rows][stride], one tile of rows
