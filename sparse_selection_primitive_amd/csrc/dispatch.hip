@@ -10,6 +10,11 @@
 // thread owns 16 bytes of a token's row and goes through the token's
 // k slots, so the token's side is read or written once and the experts' side
 // is touched in whole rows.
+//
+// What bounds them: memory.  8192 tokens of 2048 bf16 elements, 8 choices (268 MB
+// on the experts' side): dispatch 51 us (302 MB, 5.9 TB/s), combine and the sums of the dispatch's
+// gradient 53 us each (5.7 TB/s), combine's gradient 108 us (570 MB, 5.3 TB/s); the plan of the 65536 pairs is
+// three launches of 5 us, of up to 1024 pairs one of 3 us.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 

@@ -15,6 +15,12 @@
 // differ, and compare-exchange is a max and a min.  Each lane orders the
 // largest of its own numbers once; a round takes the maximum of the lanes' heads by a
 // DPP butterfly, and the lane that held it moves up.
+//
+// What bounds it: vector instructions, about 225 a row of 256 experts (scores 60, the fp64
+// numbers 25, ordering 55, eight rounds 50).  16384 rows of 256 fp32 logits
+// take 9.2 us (17.8 MB, 1.9 TB/s), 32768 bf16 rows with bias and groups 17.9 us, the
+// gradient of those 10.0 us (34 MB with the gathered logits' 64-byte
+// sectors, 3.4 TB/s); 16 rows 4.8 us, the length of one row's chain.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
