@@ -306,6 +306,8 @@ lapsum_status lapsum_backward_noalloc(const float *g, const float *p, const doub
  *   - Index arrays on the device (chosen, slot, lengths, ...) are checked by
  *     the kernels: an entry out of range counts as absent, never as an
  *     address.
+ *   - A workspace may be NULL where its size is 0 (plans of few pairs, short
+ *     caches).
  * Errors: LAPSUM_ERR_NULL, _SHAPE, _OPTION, _LAYOUT, _WORKSPACE (nothing
  * launched), LAPSUM_ERR_HIP (launch failed). */
 typedef enum lapsum_dtype { LAPSUM_F32 = 0, LAPSUM_BF16 = 1, LAPSUM_F16 = 2 } lapsum_dtype;

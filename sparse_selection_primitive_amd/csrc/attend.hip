@@ -50,10 +50,17 @@ constexpr int kMaxSplits = 256;
 constexpr int kWholeShort = 256, kWholeMax = 4096;
 constexpr int kWholeCaches = 256;
 constexpr int kWholeLogits = 16384;  // fp32 logits that it keeps in LDS, at most
-constexpr int kKeepRows = 16;    // up to this many rows the logits are kept for the accounts
+// Up to this many rows the logits are kept for the accounts; beyond they are formed again from the
+// keys (4 rows of 64 sequences of 8192 entries: kept 421 us, formed again 505;
+// 16 rows of 20000 entries: 27.7 and 35.9; more rows keep more than the keys' bytes).
+constexpr int kKeepRows = 16;
 
-LDEV f32x4 mfma(pack_t<bf16> a, pack_t<bf16> b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-LDEV f32x4 mfma(pack_t<f16> a, pack_t<f16> b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+LDEV f32x4 mfma(pack_t<bf16> a, pack_t<bf16> b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+LDEV f32x4 mfma(pack_t<f16> a, pack_t<f16> b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
 
 LDEV float exp2_of(float z, float m) { return m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(z - m); }
 
@@ -834,6 +841,8 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
   const bool kept = a.logits != nullptr, formed = a.account_out != nullptr && !kept;
   // the rows' lse, where the logits are formed again, follow the parts' maxima and sums
   float *lse = formed ? a.part_ml + caches * a.splits * a.rows * 2 : nullptr;
+  // 512 threads where there are many parts (one sequence of 8192 entries, 91 splits: 13.7 us, 14.7 with
+  // 256), 256 where there are few (128 rows, 16 splits: 52.6 us, 56.0 with 512)
   e = a.splits > 16 ? join<T, 512>(a, lse, s) : join<T, 256>(a, lse, s);
   if (e != hipSuccess || !formed) return e;
   account_formed_kernel<T, DP, EXACT>
@@ -844,9 +853,12 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
 // accesses fall on all banks
 int whole_stride(int64_t capacity) { return (int)((capacity + kBlock - 1) / kBlock * kBlock + 4); }
 
-// 16 rows are one tile of the matrix instruction, 32 two that share the
-// entries (ONE: a single new token, whose row sees every entry); beyond, the waves take rows of their own.  32 rows of 256 elements would not
-// fit a wave's registers.
+// 16 rows are one tile of the matrix instruction, 32 two that share the entries
+// (ONE: a single new token, whose row sees every entry); beyond, each wave takes 32
+// rows of its own and all entries, which leaves waves idle at up to 96 rows but is better than
+// 16 rows each, since every wave reads the keys and values (64 rows over two
+// sequences of 16384 entries: 40.9 us, with 16 rows each 48.3).  32 rows of 256
+// elements would not fit a wave's registers.
 template <class T, int DP, bool EXACT>
 hipError_t attend_rows(const AttendArgs &a, hipStream_t s) {
   if (a.splits == 0) {  // whole caches
@@ -860,14 +872,17 @@ hipError_t attend_rows(const AttendArgs &a, hipStream_t s) {
   const bool keep = a.logits != nullptr;  // at most 16 rows
   if (a.rows <= 16) {
     if (a.news == 1)
-      return keep ? attend<T, DP, 1, EXACT, false, true, true>(a, s) : attend<T, DP, 1, EXACT, false, true, false>(a, s);
-    return keep ? attend<T, DP, 1, EXACT, false, false, true>(a, s) : attend<T, DP, 1, EXACT, false, false, false>(a, s);
+      return keep ? attend<T, DP, 1, EXACT, false, true, true>(a, s)
+                  : attend<T, DP, 1, EXACT, false, true, false>(a, s);
+    return keep ? attend<T, DP, 1, EXACT, false, false, true>(a, s)
+                : attend<T, DP, 1, EXACT, false, false, false>(a, s);
   }
   if constexpr (DP <= 128) {
     if (a.rows <= 32) return attend<T, DP, 2, EXACT, false, false, false>(a, s);
-    if (a.rows > 64) return attend<T, DP, 2, EXACT, true, false, false>(a, s);
+    return attend<T, DP, 2, EXACT, true, false, false>(a, s);
+  } else {
+    return attend<T, DP, 1, EXACT, true, false, false>(a, s);
   }
-  return attend<T, DP, 1, EXACT, true, false, false>(a, s);
 }
 template <class T, int DP>
 hipError_t attend_width(const AttendArgs &a, hipStream_t s) {
@@ -890,7 +905,7 @@ AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t r
       rows * whole_stride(capacity) <= kWholeLogits)
     return p;  // whole caches
   // rows per workgroup, as attend_rows() chooses them
-  const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)) : 64);
+  const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : 128) : 64);
   const int64_t groups = caches * ((rows + rows_per - 1) / rows_per);
   // Workgroups over all.  768 fit the chip at once (three a compute unit), and one
   // round of them is best where their shares are equal: one sequence of 200001 entries takes 132 us,
@@ -898,7 +913,11 @@ AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t r
   // entries take 188 us in three rounds, 196 in one.  With more rows, or wider ones, a
   // split's part of the outputs weighs more: 32 new tokens over 16384 entries take 56 us with
   // one workgroup a compute unit, 73 with two and 87 with half of them idle.
-  const int64_t wanted = rows > 16 || width > 128 ? 256 : (batch > 1 && one ? 2304 : 768);
+  // At up to 64 rows half of a workgroup's waves are idle, so two share a compute unit where the
+  // entries are many: 64 rows over 100000 entries take 98 us with 512 workgroups, 116 with 256, over
+  // 8192 entries 23.3 and 21.2.
+  const bool halves = rows > 32 && rows <= 64 && width <= 128 && caches * capacity >= 1 << 17;
+  const int64_t wanted = halves ? 512 : (rows > 16 || width > 128 ? 256 : (batch > 1 && one ? 2304 : 768));
   int64_t splits = (wanted + groups - 1) / groups;
   const int64_t most = (capacity + kStep - 1) / kStep;
   if (splits > most) splits = most;

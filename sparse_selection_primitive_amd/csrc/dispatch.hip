@@ -378,6 +378,10 @@ hipError_t rows_of(const RowsArgs &a, Kind kind, hipStream_t s) {
   const auto aligned = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   const bool packs = a.width % Pack<T>::N == 0 && a.stride % Pack<T>::N == 0 && aligned(a.src) && aligned(a.dst) &&
                      aligned(a.dy);
+  // A wave per token for up to 64 units, a workgroup beyond: 8192 rows of 512 bf16 elements, 8 choices,
+  // take 14.1, 13.4 and 29.1 us (dispatch, sums, combine's gradient) with a wave each, 14.3, 15.9 and
+  // 48.6 with a workgroup; of 2048 elements 75, 71 and 122 with a wave, 52, 54 and 105 with a
+  // workgroup.  Packs where widths and addresses allow them (2048 elements one by one: 109, 80 and 133).
   const int64_t units = packs ? a.width / Pack<T>::N : a.width;
   if (packs) return units <= 64 ? rows<T, true, 64>(a, kind, s) : rows<T, true, 256>(a, kind, s);
   return units <= 64 ? rows<T, false, 64>(a, kind, s) : rows<T, false, 256>(a, kind, s);

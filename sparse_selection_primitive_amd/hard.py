@@ -246,8 +246,8 @@ def _plan_bytes(tokens, k, experts):
 
 def dispatch_plan(chosen, experts):
     """The expert order of the (token, choice) pairs of chosen [tokens, k]:
-    offsets int32 [experts + 1] (expert e's rows are offsets[e]:offsets[e + 1]), slot int32 [tokens, k] (a pair's row, -1
-    for entries that name no expert) and order int32 [tokens * k] (the pair t * k + j of a row, -1 behind the last)."""
+    offsets int32 [experts + 1] (expert e's rows are offsets[e]:offsets[e + 1]), slot int32 [tokens, k] (a pair's row,
+    -1 for entries that name no expert) and order int32 [tokens * k] (the pair t * k + j of a row, -1 behind the last)."""
     if _native is not None:
         done = _native.dispatch_plan(chosen, experts)
         if done is not None:
@@ -430,7 +430,8 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     """out [batch, news, q_heads, width]: attention of the newest tokens q over a cache k, v
     [batch, heads, capacity, width] whose first lengths[b] entries are filled, the new tokens' own last (token i sees
     the entries up to lengths[b] - news + i).  account fp32 [batch, heads, capacity]: each entry's weight, summed over
-    the new tokens and the query heads of its key head, is added to it, in place or into account_out.  scale: 1/sqrt(width) by default."""
+    the new tokens and the query heads of its key head, is added to it, in place or into account_out.
+    scale: 1/sqrt(width) by default."""
     if _native is not None and out is None:
         done = _native.cache_attend(q, k, v, lengths, account, scale, account_out)
         if done is not None:
