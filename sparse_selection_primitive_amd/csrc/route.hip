@@ -139,6 +139,10 @@ LDEV void best_two(float &b1, float &b2, float y) {
   b2 = __builtin_amdgcn_fmed3f(b1, b2, y);
   b1 = fmaxf(b1, y);
 }
+// Their sum; a group with one available expert is as one with none, also where that one's c is +inf.
+LDEV float group_score(float b1, float b2, int size) {
+  return size == 1 ? b1 : (b2 == -INFINITY ? -INFINITY : b1 + b2);
+}
 template <int M>
 LDEV void best_two_across(float &b1, float &b2) {
   const float x1 = pair_lane<M>(b1), x2 = pair_lane<M>(b2);
@@ -263,7 +267,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
         if constexpr (L > 32) { if (spread > 32) best_two_across<32>(b1, b2); }
         const int e = expert_at<T, L, V>(j, i * P);
         if (e < a.experts && (j & (spread - 1)) == 0)
-          group[(uint32_t)e * a.group_magic >> 21] = a.group_size > 1 ? b1 + b2 : b1;
+          group[(uint32_t)e * a.group_magic >> 21] = group_score(b1, b2, a.group_size);
       }
     } else {
       float *sc = sh.s[wave][team];
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
       for (int g = j; g < a.groups; g += L) {
         float b1 = -INFINITY, b2 = -INFINITY;
         for (int i = 0; i < a.group_size; ++i) best_two(b1, b2, sc[place(g * a.group_size + i)]);
-        group[g] = a.group_size > 1 ? b1 + b2 : b1;
+        group[g] = group_score(b1, b2, a.group_size);
       }
     }
     wave_sync();
@@ -350,13 +354,14 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
     sum += w[i];
   }
   sum = a.renormalise != 0 ? team_sum<L>(sum) : 1.0f;
-  const float f = sum > 0.0f ? a.scale / sum : 0.0f;
+  // divided first: scale / sum overflows where all of the chosen scores are small
+  if (sum == 0.0f) sum = INFINITY;
   if (!live) return;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int at = i * L + j;
     if (at < a.k) {
-      a.weights[token * a.k + at] = nan ? NAN : w[i] * f;
+      a.weights[token * a.k + at] = nan ? NAN : w[i] / sum * a.scale;
       a.chosen[token * a.k + at] = available(mine[i]) ? expert_of(mine[i]) : -1;
     }
   }
@@ -444,21 +449,23 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(const Route
       s[r] = soft ? share_of(x[r], m) : sigmoid(x[r]);
       if (x[r] == -INFINITY) s[r] = 0.0f;
       sum += s[r];
-      mean += g[r] * s[r];
     }
+    // from here s is the share of the sum: the terms keep their size where all of the scores are small
     if (a.renormalise != 0) {
       sum = team_sum<L>(sum);
+      if (sum == 0.0f) sum = INFINITY;
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        s[r] /= sum;
+        mean += g[r] * s[r];
+      }
       mean = team_sum<L>(mean);
-    } else {
-      sum = 1.0f;
-      mean = 0.0f;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int r = 0; r < C; ++r) {
       if (e[r] < 0) continue;
-      float dx = a.scale * (g[r] - mean * inv) * inv * s[r];
-      if (!soft) dx *= 1.0f - s[r];
+      float dx = a.scale * (g[r] - mean) * s[r];
+      if (!soft) dx *= sigmoid(-x[r]);  // 1 - sigmoid(x), without the difference's rounding
       d[e[r]] = dx;
     }
     wave_sync();

@@ -301,3 +301,42 @@ def test_refusals(L):
         L.route_forward(torch.randn(4, 1025, device="cuda"), 2)
     with pytest.raises(L.LapsumError):
         L.route_backward(torch.randn(4, 3, device="cuda"), x, torch.zeros(4, 2, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("experts", [24, 64, 256])
+def test_small_scores_share_a_large_scale(L, experts):
+    """Scores near 1e-37: scale / sum would overflow, the shares do not."""
+    x = torch.full((3, experts), -85.0, dtype=torch.float64)
+    x[1, ::3] = -84.5
+    x[2, 1::2] = -86.25
+    check(L, x, 4, score="sigmoid", scale=1000.0)
+    x[:, 0] = 0.0  # the others are chosen by the bias, and their shares of the softmax are as small
+    bias = torch.full((experts,), 2.0, dtype=torch.float64)
+    bias[0] = 0.0
+    check(L, x, 4, bias, grad=False, scale=1000.0)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_slope_of_a_large_sigmoid(L, dtype):
+    """s (1 - s) keeps its relative precision where s rounds to 1."""
+    x = torch.tensor([[24.0, 18.5, 30.0, 12.25, -3.0, 2.0, 1.0, 0.0]])
+    xt = x.to(TYPES[dtype]).cuda()
+    w, c = L.route_forward(xt, 6, score="sigmoid", renormalise=False)
+    dw = torch.tensor([[1.0, -2.0, 0.5, 3.0, 1.0, -1.0]])
+    dx = L.route_backward(dw.cuda(), xt, c, score="sigmoid", renormalise=False).double().cpu()
+    s = x.double().neg()
+    want = torch.zeros(1, 8, dtype=torch.float64).scatter_(1, c.cpu().long(), dw.double())
+    want = want * torch.sigmoid(-s) * torch.sigmoid(s)
+    assert ((dx - want).abs() <= (16 * 2.0 ** -24 + HALF_ULP[dtype]) * want.abs()).all()
+
+
+@pytest.mark.parametrize("experts,groups", [(64, 8), (60, 4), (256, 8)])
+def test_group_of_one_infinite_expert(L, experts, groups):
+    """A group whose only available expert has c = +inf scores -inf, and no more groups open than asked for."""
+    x, bias = grid_logits(6, experts, 3), torch.zeros(experts)
+    size = experts // groups
+    x[:, 1:size] = -math.inf
+    bias[0] = math.inf
+    _, c = L.route_forward(x.float().cuda(), size, bias.cuda(), score="sigmoid", groups=groups, top_groups=1)
+    of = c.cpu() // size
+    assert (of == of[:, :1]).all() and (of > 0).all()
