@@ -346,7 +346,9 @@ typedef struct lapsum_route_options {
  * available expert fills gets chosen = -1 and weight 0, so a row of -inf
  * gives -1 and 0 throughout.  The softmax with logits of +inf is its limit
  * (they share the mass equally).  A NaN logit makes the row's weights NaN
- * (the choice is made among the others).  S = 0 gives weights 0. */
+ * (the choice is made among the others).  Scores below 2^-126 count as 0;
+ * S = 0 gives weights 0.  A group in which one expert alone is available
+ * counts as one with none, unless groups are of one expert. */
 lapsum_status lapsum_route_forward(const void *logits, int32_t dtype, int64_t tokens, int64_t experts,
                                    int64_t row_stride, const float *bias, const lapsum_route_options *opt,
                                    float *weights, int32_t *chosen, void *stream);
@@ -420,7 +422,8 @@ typedef struct lapsum_cache {
  * A token that sees nothing (length < news) gets out = 0 and adds nothing.
  * Entries at length and behind are not read, and neither are their accounts
  * written; what a token does not see does not reach its output, NaN and
- * infinities included.
+ * infinities included.  A NaN or infinity among the values that it does see makes that
+ * element of its output NaN or infinite; a NaN or +infinity among its logits, the whole row NaN.
  *   q, out   device [batch, news, q_heads, width] contiguous, of the cache's type;
  *            q_heads a multiple of heads, query head j reads key head j / (q_heads / heads);
  *            news * q_heads / heads <= 65536
@@ -446,7 +449,7 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
  *   next_position  device [batch] int32, or NULL when recent = 0
  *   kept           device [batch, heads, keep] int32: the slot each entry came
  *                  from, -1 at min(length, keep) and behind
- *   lengths_out    device [batch]: min(length, keep); may be lengths */
+ *   lengths_out    device [batch]: min(length, keep); not lengths itself (LAPSUM_ERR_LAYOUT): other heads still read it */
 size_t lapsum_cache_evict_workspace_bytes(const lapsum_cache *cache, int64_t keep);
 lapsum_status lapsum_cache_evict(const lapsum_cache *cache, const float *account, const int32_t *positions,
                                  const int32_t *lengths, int64_t keep, const int32_t *next_position, int32_t sinks,

@@ -41,7 +41,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBlock = 32;       // entries a wave takes at a time
 constexpr int kAttendWaves = 4;  // waves of a workgroup, taking its blocks in turn
 constexpr int kStep = kBlock * kAttendWaves;
-constexpr float kSlack = 8.0f;   // powers of two that a row's weights may exceed 1 by
+// Weights are formed against a base kLift powers of two below the maximum that set it, and may
+// grow by kSlack more before it moves.  2^15 is an fp16 number, and its smallest weight that is not
+// 0 is then 2^-31 of the largest: many entries of little weight beside one of much keep theirs.
+constexpr float kLift = 7.0f, kSlack = 8.0f;
 constexpr int kMaxSplits = 256;
 // A cache goes to one workgroup whole where that is one block a wave, or where
 // there are enough caches for every compute unit (times of one call from a graph, 32 query
@@ -257,7 +260,7 @@ struct KeepNear {  // [rows][stride], one tile of rows
 };
 
 // One wave's pass over the blocks first, first + stride, .. of the entries up to
-// `end`, for 16 * NT rows from row0: the rows' maxima, their sums (this lane's
+// `end`, for 16 * NT rows from row0: the rows' bases (see kLift), their sums (this lane's
 // share) and outputs.  Returns whether values were left out (see drop()).
 template <class T, int DP, int NT, bool EXACT, bool ONE, int AUX, class Keep>
 LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, int first, int end, int stride,
@@ -343,10 +346,10 @@ LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, 
       keep(e0, t, z[t][0], z[t][1]);
       float top = fmaxf(fmaxf(fmaxf(z[t][0][0], z[t][0][1]), fmaxf(z[t][0][2], z[t][0][3])),
                         fmaxf(fmaxf(z[t][1][0], z[t][1][1]), fmaxf(z[t][1][2], z[t][1][3])));
-      // A maximum that grows a little stays as it is (weights up to 2^8 do no
-      // harm): the first blocks would otherwise rescale the outputs nearly every time.
-      if (__any(top > m[t] + kSlack)) {
-        const float next = fmaxf(m[t], groups_max(top));
+      // A maximum that grows a little moves nothing: the first blocks would otherwise
+      // rescale the outputs nearly every time.
+      if (__any(top > m[t] + (kLift + kSlack))) {
+        const float next = fmaxf(m[t], groups_max(top) - kLift);
         const float f = exp2_of(m[t], next);
         l[t] *= f;
 #pragma unroll
@@ -358,8 +361,9 @@ LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, 
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         p[i] = __builtin_amdgcn_exp2f(z[t][i / 4][i % 4] - base);
-        l[t] += p[i];
       }
+      // the block's weights among themselves first: many small ones would each round away in a large sum
+      l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
       hi[t] = __builtin_convertvector(p, pack_t<T>);
       lo[t] = __builtin_convertvector(p - __builtin_convertvector(hi[t], f32x8), pack_t<T>);
     }

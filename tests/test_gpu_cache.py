@@ -119,6 +119,29 @@ def test_scale_and_sharp_weights(L):
         check_attend(L, q, k, v, [399], "bf16", scale=scale)
 
 
+@pytest.mark.parametrize("batch,news,capacity", [(1, 1, 200), (256, 40, 1024), (256, 1, 1000), (64, 20, 5000)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_many_light_entries_beside_a_heavy_one(L, dtype, batch, news, capacity):
+    """Entry 0 outweighs each other one 1.2e7 times and its value is 0: the output is what the others weigh together.
+    A weight's part in the products is within 2^-32 of the heaviest's, or 2^-16 of itself, and the output is rounded."""
+    z = 16.296875
+    k = torch.zeros(batch, 1, capacity, 64, dtype=TYPES[dtype], device="cuda")
+    v = torch.ones_like(k)
+    k[:, :, 0, 0], v[:, :, 0] = 4.0, 0.0
+    q = torch.zeros(batch, news, 1, 64, dtype=TYPES[dtype], device="cuda")
+    q[:, :, 0, 0] = z / 4  # a bf16 number is not needed: the logit below is that of the rounded one
+    p = math.exp(-4.0 * float(q[0, 0, 0, 0]))
+    others = torch.arange(capacity - news, capacity).double() * p
+    want = (others / (1.0 + others))[None, :, None, None]
+    n = torch.full((batch,), capacity, dtype=torch.int32, device="cuda")
+    account = torch.zeros(batch, 1, capacity, device="cuda")
+    out = L.cache_attend(q, k, v, n, account, scale=1.0).double().cpu()
+    bound = 2.0 ** -32 / p + 2.0 ** -16 + HALF_ULP[dtype] + 2.0 ** -18
+    assert ((out - want).abs() <= bound * want + 2.0 ** -25).all()
+    got = account[:, 0, 1].double().cpu() / news  # entry 1 is seen by every token
+    assert ((got / (p / (1.0 + others)).mean() - 1.0).abs() <= 2.0 ** -18).all()
+
+
 def test_many_caches(L):
     k, v = cache(40, 8, 64, 64, "bf16", seed=5)
     check_attend(L, query(40, 1, 16, 64, "bf16"), k, v, [int(x) for x in torch.arange(40) + 20], "bf16")
