@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstdint>
 
 #include "../../include/lapsum.h"
 
@@ -77,6 +78,13 @@ struct Workspace {
     bytes = n;
   }
 };
+// A 32-bit integer; anything else leaves an error set.
+int32_t int32_of(PyObject *o) {
+  int over = 0;
+  const long long x = PyLong_AsLongLongAndOverflow(o, &over);
+  if (over != 0 || x < INT32_MIN || x > INT32_MAX) PyErr_SetNone(PyExc_OverflowError);
+  return (int32_t)x;
+}
 PyObject *wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject *pair(at::Tensor a, at::Tensor b) { return Py_BuildValue("(NN)", wrap(std::move(a)), wrap(std::move(b))); }
 
@@ -102,10 +110,10 @@ PyObject *route_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const at::Tensor *x = gpu(args[0]), *bias = args[1] == Py_None ? nullptr : gpu(args[1]);
   if (!rows(x) || (args[1] != Py_None && !(plain(bias, at::kFloat, x->size(1)) && bias->dim() == 1))) return none();
   lapsum_route_options o;
-  o.k = (int32_t)PyLong_AsLong(args[2]);
-  o.score = (int32_t)PyLong_AsLong(args[3]);
-  o.groups = (int32_t)PyLong_AsLong(args[4]);
-  o.top_groups = args[5] == Py_None ? o.groups : (int32_t)PyLong_AsLong(args[5]);
+  o.k = int32_of(args[2]);
+  o.score = int32_of(args[3]);
+  o.groups = int32_of(args[4]);
+  o.top_groups = args[5] == Py_None ? o.groups : int32_of(args[5]);
   o.renormalise = PyObject_IsTrue(args[6]);
   o.scale = (float)PyFloat_AsDouble(args[7]);
   if (PyErr_Occurred() || o.k < 1 || o.k > LAPSUM_MAX_CHOICES) return none();
@@ -127,7 +135,7 @@ PyObject *route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return none();
   lapsum_route_options o{};
   o.k = (int32_t)c->size(1);
-  o.score = (int32_t)PyLong_AsLong(args[3]);
+  o.score = int32_of(args[3]);
   o.groups = o.top_groups = 1;
   o.renormalise = PyObject_IsTrue(args[4]);
   o.scale = (float)PyFloat_AsDouble(args[5]);
@@ -295,7 +303,7 @@ PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
       !per_entry(account_out, *k, at::kFloat) || !per_entry(positions_out, *k, at::kInt))
     return none();
   const int64_t keep = PyLong_AsLongLong(args[5]);
-  const int32_t sinks = (int32_t)PyLong_AsLong(args[7]), recent = (int32_t)PyLong_AsLong(args[8]);
+  const int32_t sinks = int32_of(args[7]), recent = int32_of(args[8]);
   if (PyErr_Occurred() || keep < 1 || keep > c.capacity) return none();
   at::Tensor kept = make(*k, {c.batch, c.heads, keep}, at::kInt), after = make(*k, {c.batch}, at::kInt);
   const Workspace ws(*k, entry.evict_bytes(&c, keep));

@@ -96,6 +96,13 @@ def _bind():
 
 
 # ----------------------------------------------------------------- checks
+def _int32(x, name):
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise LapsumError(f"{name} must be a 32-bit integer")
+    return x
+
+
 def _dtype(x, name, only=None):
     code = _TYPES.get(x.dtype)
     if code is None or (only is not None and code not in only):
@@ -164,7 +171,8 @@ def _call(dev, name, *args):
 def _route_options(k, score, groups, top_groups, renormalise, scale):
     if score not in SCORES:
         raise LapsumError(f"score must be one of {sorted(SCORES)}")
-    return RouteOptions(k, SCORES[score], groups, groups if top_groups is None else top_groups, int(bool(renormalise)),
+    return RouteOptions(_int32(k, "k"), SCORES[score], _int32(groups, "groups"),
+                        _int32(groups if top_groups is None else top_groups, "top_groups"), int(bool(renormalise)),
                         scale)
 
 
@@ -220,6 +228,7 @@ def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=Tru
 def route(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, renormalise=True, scale=1.0):
     """Differentiable route_forward: the weights' gradient reaches the logits.  The choice is not differentiable, so
     the bias, which takes part in nothing else, gets no gradient."""
+    _gpu(logits, "logits", 2)
 
     class _Route(torch.autograd.Function):
         @staticmethod
@@ -231,6 +240,7 @@ def route(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, r
             return weights, chosen
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dweights, _):
             x, chosen = ctx.saved_tensors
             return route_backward(dweights.contiguous(), x, chosen, score=score, renormalise=renormalise, scale=scale)
@@ -369,6 +379,7 @@ def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
 
 def dispatch(x, slot, offsets):
     """Differentiable dispatch_forward."""
+    _gpu(x, "x", 2)
 
     class _Dispatch(torch.autograd.Function):
         @staticmethod
@@ -376,6 +387,7 @@ def dispatch(x, slot, offsets):
             return dispatch_forward(x, slot, offsets)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dxs):
             return dispatch_backward(dxs.contiguous(), slot)
 
@@ -384,6 +396,7 @@ def dispatch(x, slot, offsets):
 
 def combine(ys, weights, slot, offsets):
     """Differentiable combine_forward: gradients reach the experts' outputs and the weights."""
+    _gpu(ys, "ys", 2)
 
     class _Combine(torch.autograd.Function):
         @staticmethod
@@ -392,6 +405,7 @@ def combine(ys, weights, slot, offsets):
             return combine_forward(ys, slot, weights)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dy):
             ys, weights = ctx.saved_tensors
             return combine_backward(dy, ys, slot, weights, offsets)
@@ -503,7 +517,8 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
     lengths_out = torch.empty_like(lengths)
     ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, k.shape, keep), dev)
     _call(dev, "lapsum_cache_evict", cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,
-          None if next_position is None else next_position.data_ptr(), int(sinks), int(recent),
+          None if next_position is None else next_position.data_ptr(), _int32(sinks, "sinks"),
+          _int32(recent, "recent"),
           account_out.data_ptr(), positions_out.data_ptr(), kept.data_ptr(), lengths_out.data_ptr(), wptr, wlen)
     del ws
     return kept, lengths_out

@@ -155,3 +155,27 @@ def test_calls_on_another_stream_and_in_a_graph(L, both):
         torch.cuda.synchronize()
         same((w, c), (w3, c3))
         same(want, (offsets, slot, order))
+
+
+def test_integers_past_32_bits_are_refused_by_both_fronts(L, both):
+    x = torch.randn(4, 16, device="cuda")
+    k = torch.zeros(1, 1, 8, 64, device="cuda", dtype=torch.bfloat16)
+    n, a = torch.tensor([8], dtype=torch.int32, device="cuda"), torch.zeros(1, 1, 8, device="cuda")
+    for bad in (lambda: L.route_forward(x, 2 ** 32 + 2), lambda: L.route_forward(x, 2, groups=2 ** 32 + 1),
+                lambda: L.cache_evict(k, k.clone(), a, a.int(), n, 4, sinks=2 ** 32),
+                lambda: L.cache_evict(k, k.clone(), a, a.int(), n, 4, next_position=n, recent=2 ** 32 + 1)):
+        def refused():
+            with pytest.raises(L.LapsumError):
+                bad()
+            return torch.zeros(1)
+        same(*both(refused))
+
+
+def test_second_derivatives_are_refused(L):
+    x = torch.randn(4, 16, device="cuda", requires_grad=True)
+    w, c = L.route(x, 2)
+    offsets, slot, _ = L.dispatch_plan(c, 16)
+    y = L.combine(L.dispatch(x, slot, offsets), w, slot, offsets)
+    g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()

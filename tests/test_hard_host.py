@@ -149,3 +149,23 @@ def test_no_cpu_path():
                  lambda: L.cache_attend(x, x, x, x), lambda: L.cache_evict(x, x, x, x, x, 1)):
         with pytest.raises(L.LapsumError):
             call()
+
+
+def test_the_first_call_may_be_a_differentiable_one(monkeypatch):
+    import torch
+    monkeypatch.setattr(hard, "torch", None)  # as before any call
+    x = torch.zeros(2, 4)
+    for call in (lambda: L.route(x, 1), lambda: L.dispatch(x, x, x), lambda: L.combine(x, x, x, x)):
+        with pytest.raises(L.LapsumError):
+            call()
+        hard.torch = None
+
+
+def test_integers_past_32_bits_are_refused():
+    with pytest.raises(L.LapsumError):
+        hard._route_options(2 ** 32 + 2, "softmax", 1, 1, True, 1.0)
+    with pytest.raises(L.LapsumError):
+        hard._route_options(2, "softmax", 2 ** 32 + 1, None, True, 1.0)
+    with pytest.raises(L.LapsumError):
+        hard._int32(-2 ** 31 - 1, "sinks")
+    assert hard._int32(2 ** 31 - 1, "recent") == 2 ** 31 - 1
