@@ -117,7 +117,7 @@ def build_binding(out: str = BINDING) -> str:
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
            "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{d}" for d in includes], os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib}", "-lc10", "-lc10_hip",
-           "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+           "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"building the native binding failed:\n{res.stderr}")

@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -42,10 +42,10 @@ PyObject *none() {
 }
 
 // A GPU tensor on the current device, or null.
-const at::Tensor *gpu(PyObject *o) {
+const at::Tensor *gpu(int dev, PyObject *o) {
   if (!THPVariable_Check(o)) return nullptr;
   const at::Tensor &t = THPVariable_Unpack(o);
-  return t.is_cuda() && t.device().index() == c10::hip::current_device() && t.numel() > 0 ? &t : nullptr;
+  return t.is_cuda() && t.device().index() == dev && t.numel() > 0 ? &t : nullptr;
 }
 int dtype_of(const at::Tensor &t) {
   switch (t.scalar_type()) {
@@ -63,16 +63,19 @@ bool rows(const at::Tensor *t) {  // [tokens, n], rows in order
   return t != nullptr && t->dim() == 2 && t->stride(1) == 1 && t->stride(0) >= t->size(1) && dtype_of(*t) >= 0;
 }
 void *stream_of(const at::Tensor &t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
-at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType type) {
-  return at::empty(shape, like.options().dtype(type).requires_grad(false));
+// A new tensor on the current device, from torch's pool for its current stream (without
+// the dispatcher, which takes as long again).
+at::Tensor make(int dev, at::IntArrayRef shape, at::ScalarType type) {
+  return at::Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::DeviceType::CUDA, (c10::DeviceIndex)dev),
+                                           std::nullopt));
 }
 struct Workspace {
   at::Tensor buffer;
   void *at = nullptr;
   size_t bytes = 0;
-  Workspace(const at::Tensor &like, size_t n) {
+  Workspace(int dev, size_t n) {
     if (n == 0) return;
-    buffer = make(like, {(int64_t)n + 256}, at::kByte);
+    buffer = make(dev, {(int64_t)n + 256}, at::kByte);
     const uintptr_t p = reinterpret_cast<uintptr_t>(buffer.data_ptr()), up = (p + 255) / 256 * 256;
     at = reinterpret_cast<void *>(up);
     bytes = n;
@@ -88,9 +91,10 @@ int32_t int32_of(PyObject *o) {
 PyObject *wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject *pair(at::Tensor a, at::Tensor b) { return Py_BuildValue("(NN)", wrap(std::move(a)), wrap(std::move(b))); }
 
-#define BODY(count)                 \
-  if (n != (count)) return none();  \
-  try {
+#define BODY(count)                \
+  if (n != (count)) return none(); \
+  try {                            \
+    const int dev = c10::hip::current_device();
 #define END                        \
   }                                \
   catch (const std::exception &) { \
@@ -107,7 +111,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // (logits, bias, k, score, groups, top_groups, renormalise, scale)
 PyObject *route_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(8)
-  const at::Tensor *x = gpu(args[0]), *bias = args[1] == Py_None ? nullptr : gpu(args[1]);
+  const at::Tensor *x = gpu(dev, args[0]), *bias = args[1] == Py_None ? nullptr : gpu(dev, args[1]);
   if (!rows(x) || (args[1] != Py_None && !(plain(bias, at::kFloat, x->size(1)) && bias->dim() == 1))) return none();
   lapsum_route_options o;
   o.k = int32_of(args[2]);
@@ -117,7 +121,7 @@ PyObject *route_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   o.renormalise = PyObject_IsTrue(args[6]);
   o.scale = (float)PyFloat_AsDouble(args[7]);
   if (PyErr_Occurred() || o.k < 1 || o.k > LAPSUM_MAX_CHOICES) return none();
-  at::Tensor w = make(*x, {x->size(0), o.k}, at::kFloat), c = make(*x, {x->size(0), o.k}, at::kInt);
+  at::Tensor w = make(dev, {x->size(0), o.k}, at::kFloat), c = make(dev, {x->size(0), o.k}, at::kInt);
   if (entry.route_forward(x->data_ptr(), dtype_of(*x), x->size(0), x->size(1), x->stride(0),
                           bias ? static_cast<const float *>(bias->data_ptr()) : nullptr, &o,
                           static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(c.data_ptr()), stream_of(*x)))
@@ -129,7 +133,7 @@ PyObject *route_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // (dweights, logits, chosen, score, renormalise, scale)
 PyObject *route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(6)
-  const at::Tensor *dw = gpu(args[0]), *x = gpu(args[1]), *c = gpu(args[2]);
+  const at::Tensor *dw = gpu(dev, args[0]), *x = gpu(dev, args[1]), *c = gpu(dev, args[2]);
   if (!rows(x) || c == nullptr || c->dim() != 2 || c->size(0) != x->size(0) || !plain(c, at::kInt, c->numel()) ||
       !plain(dw, at::kFloat, c->numel()) || dw->sizes() != c->sizes())
     return none();
@@ -140,7 +144,7 @@ PyObject *route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   o.renormalise = PyObject_IsTrue(args[4]);
   o.scale = (float)PyFloat_AsDouble(args[5]);
   if (PyErr_Occurred()) return none();
-  at::Tensor dx = make(*x, {x->size(0), x->size(1)}, x->scalar_type());
+  at::Tensor dx = make(dev, {x->size(0), x->size(1)}, x->scalar_type());
   if (entry.route_backward(static_cast<const float *>(dw->data_ptr()), x->data_ptr(), dtype_of(*x), x->size(0),
                            x->size(1), x->stride(0), static_cast<const int32_t *>(c->data_ptr()), &o, dx.data_ptr(),
                            stream_of(*x)))
@@ -152,15 +156,15 @@ PyObject *route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // (chosen, experts)
 PyObject *dispatch_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(2)
-  const at::Tensor *c = gpu(args[0]);
+  const at::Tensor *c = gpu(dev, args[0]);
   const int64_t experts = PyLong_AsLongLong(args[1]);
   if (PyErr_Occurred() || c == nullptr || c->dim() != 2 || !plain(c, at::kInt, c->numel()) || experts < 1 ||
       experts > LAPSUM_MAX_EXPERTS)
     return none();
   const int64_t tokens = c->size(0), k = c->size(1);
-  at::Tensor offsets = make(*c, {experts + 1}, at::kInt), slot = make(*c, {tokens, k}, at::kInt);
-  at::Tensor order = make(*c, {tokens * k}, at::kInt);
-  const Workspace ws(*c, entry.plan_bytes(tokens, k, experts));
+  at::Tensor offsets = make(dev, {experts + 1}, at::kInt), slot = make(dev, {tokens, k}, at::kInt);
+  at::Tensor order = make(dev, {tokens * k}, at::kInt);
+  const Workspace ws(dev, entry.plan_bytes(tokens, k, experts));
   if (entry.plan(static_cast<const int32_t *>(c->data_ptr()), tokens, k, experts,
                  static_cast<int32_t *>(offsets.data_ptr()), static_cast<int32_t *>(slot.data_ptr()),
                  static_cast<int32_t *>(order.data_ptr()), ws.at, ws.bytes, stream_of(*c)))
@@ -175,9 +179,9 @@ bool offsets_of(const at::Tensor *o) { return o != nullptr && o->dim() == 1 && p
 // (x, slot, offsets)
 PyObject *dispatch_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(3)
-  const at::Tensor *x = gpu(args[0]), *s = gpu(args[1]), *o = gpu(args[2]);
+  const at::Tensor *x = gpu(dev, args[0]), *s = gpu(dev, args[1]), *o = gpu(dev, args[2]);
   if (!rows(x) || !slots(s) || s->size(0) != x->size(0) || !offsets_of(o)) return none();
-  at::Tensor xs = make(*x, {s->numel(), x->size(1)}, x->scalar_type());
+  at::Tensor xs = make(dev, {s->numel(), x->size(1)}, x->scalar_type());
   if (entry.dispatch_forward(x->data_ptr(), dtype_of(*x), x->size(0), s->size(1), x->size(1), x->stride(0),
                              static_cast<const int32_t *>(s->data_ptr()),
                              static_cast<const int32_t *>(o->data_ptr()), o->numel() - 1, xs.data_ptr(),
@@ -195,9 +199,9 @@ bool expert_rows(const at::Tensor *t, const at::Tensor *s) {
 // (dxs, slot)
 PyObject *dispatch_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(2)
-  const at::Tensor *t = gpu(args[0]), *s = gpu(args[1]);
+  const at::Tensor *t = gpu(dev, args[0]), *s = gpu(dev, args[1]);
   if (!slots(s) || !expert_rows(t, s)) return none();
-  at::Tensor dx = make(*t, {s->size(0), t->size(1)}, t->scalar_type());
+  at::Tensor dx = make(dev, {s->size(0), t->size(1)}, t->scalar_type());
   if (entry.dispatch_backward(t->data_ptr(), dtype_of(*t), s->size(0), s->size(1), t->size(1),
                               static_cast<const int32_t *>(s->data_ptr()), dx.data_ptr(), stream_of(*t)))
     return none();
@@ -208,9 +212,9 @@ PyObject *dispatch_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // (ys, slot, weights)
 PyObject *combine_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(3)
-  const at::Tensor *t = gpu(args[0]), *s = gpu(args[1]), *w = gpu(args[2]);
+  const at::Tensor *t = gpu(dev, args[0]), *s = gpu(dev, args[1]), *w = gpu(dev, args[2]);
   if (!slots(s) || !expert_rows(t, s) || !plain(w, at::kFloat, s->numel()) || w->sizes() != s->sizes()) return none();
-  at::Tensor y = make(*t, {s->size(0), t->size(1)}, t->scalar_type());
+  at::Tensor y = make(dev, {s->size(0), t->size(1)}, t->scalar_type());
   if (entry.combine_forward(t->data_ptr(), dtype_of(*t), s->size(0), s->size(1), t->size(1),
                             static_cast<const int32_t *>(s->data_ptr()), static_cast<const float *>(w->data_ptr()),
                             y.data_ptr(), stream_of(*t)))
@@ -222,13 +226,13 @@ PyObject *combine_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // (dy, ys, slot, weights, offsets)
 PyObject *combine_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(5)
-  const at::Tensor *dy = gpu(args[0]), *t = gpu(args[1]), *s = gpu(args[2]), *w = gpu(args[3]), *o = gpu(args[4]);
+  const at::Tensor *dy = gpu(dev, args[0]), *t = gpu(dev, args[1]), *s = gpu(dev, args[2]), *w = gpu(dev, args[3]), *o = gpu(dev, args[4]);
   if (!rows(dy) || !slots(s) || s->size(0) != dy->size(0) || !expert_rows(t, s) || t->size(1) != dy->size(1) ||
       t->scalar_type() != dy->scalar_type() || !plain(w, at::kFloat, s->numel()) || w->sizes() != s->sizes() ||
       !offsets_of(o))
     return none();
-  at::Tensor dys = make(*t, {t->size(0), t->size(1)}, t->scalar_type());
-  at::Tensor dw = make(*t, {s->size(0), s->size(1)}, at::kFloat);
+  at::Tensor dys = make(dev, {t->size(0), t->size(1)}, t->scalar_type());
+  at::Tensor dw = make(dev, {s->size(0), s->size(1)}, at::kFloat);
   if (entry.combine_backward(dy->data_ptr(), dy->stride(0), t->data_ptr(), dtype_of(*t), s->size(0), s->size(1),
                              t->size(1), static_cast<const int32_t *>(s->data_ptr()),
                              static_cast<const float *>(w->data_ptr()), static_cast<const int32_t *>(o->data_ptr()),
@@ -268,19 +272,19 @@ bool per_sequence(const at::Tensor *t, const at::Tensor &k) {
 // (q, k, v, lengths, account, scale, account_out); scale None: 1/sqrt(width)
 PyObject *cache_attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(7)
-  const at::Tensor *q = gpu(args[0]), *k = gpu(args[1]), *v = gpu(args[2]), *lengths = gpu(args[3]);
+  const at::Tensor *q = gpu(dev, args[0]), *k = gpu(dev, args[1]), *v = gpu(dev, args[2]), *lengths = gpu(dev, args[3]);
   lapsum_cache c{};
   if (!cache_of(k, v, c) || q == nullptr || q->dim() != 4 || q->scalar_type() != k->scalar_type() ||
       !q->is_contiguous() || q->size(0) != c.batch || q->size(3) != c.width || !per_sequence(lengths, *k))
     return none();
   const bool accounts = args[4] != Py_None;
-  const at::Tensor *in = accounts ? gpu(args[4]) : nullptr;
-  const at::Tensor *to = args[6] != Py_None ? gpu(args[6]) : in;
+  const at::Tensor *in = accounts ? gpu(dev, args[4]) : nullptr;
+  const at::Tensor *to = args[6] != Py_None ? gpu(dev, args[6]) : in;
   if (accounts ? !per_entry(in, *k, at::kFloat) || !per_entry(to, *k, at::kFloat) : args[6] != Py_None) return none();
   const double scale = args[5] == Py_None ? 1.0 / std::sqrt((double)c.width) : PyFloat_AsDouble(args[5]);
   if (PyErr_Occurred()) return none();
-  at::Tensor out = make(*q, q->sizes(), q->scalar_type());
-  const Workspace ws(*q, entry.attend_bytes(&c, q->size(1), q->size(2), accounts ? 1 : 0));
+  at::Tensor out = make(dev, q->sizes(), q->scalar_type());
+  const Workspace ws(dev, entry.attend_bytes(&c, q->size(1), q->size(2), accounts ? 1 : 0));
   if (entry.attend(q->data_ptr(), &c, static_cast<const int32_t *>(lengths->data_ptr()), q->size(1), q->size(2),
                    (float)scale, accounts ? static_cast<const float *>(in->data_ptr()) : nullptr,
                    accounts ? static_cast<float *>(to->data_ptr()) : nullptr, out.data_ptr(), ws.at, ws.bytes,
@@ -293,10 +297,10 @@ PyObject *cache_attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // (k, v, account, positions, lengths, keep, next_position, sinks, recent, account_out, positions_out)
 PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(11)
-  const at::Tensor *k = gpu(args[0]), *v = gpu(args[1]), *account = gpu(args[2]), *positions = gpu(args[3]);
-  const at::Tensor *lengths = gpu(args[4]), *next = args[6] == Py_None ? nullptr : gpu(args[6]);
-  const at::Tensor *account_out = args[9] == Py_None ? account : gpu(args[9]);
-  const at::Tensor *positions_out = args[10] == Py_None ? positions : gpu(args[10]);
+  const at::Tensor *k = gpu(dev, args[0]), *v = gpu(dev, args[1]), *account = gpu(dev, args[2]), *positions = gpu(dev, args[3]);
+  const at::Tensor *lengths = gpu(dev, args[4]), *next = args[6] == Py_None ? nullptr : gpu(dev, args[6]);
+  const at::Tensor *account_out = args[9] == Py_None ? account : gpu(dev, args[9]);
+  const at::Tensor *positions_out = args[10] == Py_None ? positions : gpu(dev, args[10]);
   lapsum_cache c{};
   if (!cache_of(k, v, c) || !per_entry(account, *k, at::kFloat) || !per_entry(positions, *k, at::kInt) ||
       !per_sequence(lengths, *k) || (args[6] != Py_None && !per_sequence(next, *k)) ||
@@ -305,8 +309,8 @@ PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const int64_t keep = PyLong_AsLongLong(args[5]);
   const int32_t sinks = int32_of(args[7]), recent = int32_of(args[8]);
   if (PyErr_Occurred() || keep < 1 || keep > c.capacity) return none();
-  at::Tensor kept = make(*k, {c.batch, c.heads, keep}, at::kInt), after = make(*k, {c.batch}, at::kInt);
-  const Workspace ws(*k, entry.evict_bytes(&c, keep));
+  at::Tensor kept = make(dev, {c.batch, c.heads, keep}, at::kInt), after = make(dev, {c.batch}, at::kInt);
+  const Workspace ws(dev, entry.evict_bytes(&c, keep));
   if (entry.evict(&c, static_cast<const float *>(account->data_ptr()),
                   static_cast<const int32_t *>(positions->data_ptr()),
                   static_cast<const int32_t *>(lengths->data_ptr()), keep,
