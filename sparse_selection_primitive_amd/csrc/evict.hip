@@ -15,12 +15,12 @@
 //
 // Rows of up to 16384 entries: one workgroup holds the row's keys in its
 // registers, so the accounts are read once.  Longer rows: tiles of 4096
-// entries on as many workgroups, one launch a digit, joined by counts.
+// entries on as many workgroups, one launch a digit; the last leaves the tiles' counts.
 //
 // What bounds it.  One entry over the budget: one pass over the accounts and
 // positions, 7.6 us for 256 rows of 4097 (8.4 MB; a launch and a chain of memory
 // latencies).  130001 entries of 8 rows to a quarter: the moves, 39 us for 201 MB
-// (5.2 TB/s), and six launches of 5 to 12 us before them that find the key and the places.
+// (5.2 TB/s), and five launches of 5 to 13 us before them that find the key and the places.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -30,8 +30,8 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / 64;
 // Entries of a row that one workgroup holds: 16 a thread, what its registers allow.
-// One workgroup is faster all the way up there (8 rows of 16384 to a half: 41 us, by tiles 49;
-// 256 rows 272 and 361; of 8192 23 and 44).
+// 8 rows of 8192 to a half take 23 us, by tiles 33; 256 rows of 16384 273 and 326, and 12 and 29 where one entry
+// leaves; only few rows of 16384 that lose many are better by tiles (8 to a half: 41 and 36).
 constexpr int kRowMax = 16384;
 // Up to this many entries the selecting workgroup moves itself, beyond a second launch
 // does (256 rows, 64 of 4160 entries leave: 15.8 us, with the second launch 21.0).
@@ -47,9 +47,8 @@ struct RowKeys {
   const float *account;
   const int32_t *positions;
   int32_t sinks, from;  // protected: position < sinks or position >= from
-  LDEV uint32_t key(int64_t i) const {
-    const int32_t p = positions[i];
-    const float x = account[i];
+  LDEV uint32_t key(int64_t i) const { return key(positions[i], account[i]); }
+  LDEV uint32_t key(int32_t p, float x) const {
     if (p < sinks || p >= from) return 0xFFFFFFFFu;
     return x != x ? 0u : key_of(x + 0.0f);  // -0 counts as 0
   }
@@ -356,7 +355,7 @@ Tiles tiles_of(int64_t capacity, int64_t keep) {
 }
 
 struct LongRow {  // a row's state in the workspace
-  uint32_t prefix[3], want[3];  // after each digit: the key's digits so far, and how many of those stay
+  uint32_t prefix[2], want[2];  // after a digit: the key's digits so far, and how many of those stay
   int32_t moves;
   int32_t pad;
 };
@@ -365,7 +364,8 @@ struct LongArgs {
   Tiles t;
   LongRow *state;      // [rows]
   uint32_t *hist;      // [rows][3][2048]
-  int2 *counts;        // [rows][tiles]: entries above the key, entries that hold it
+  uint32_t *tails;     // [rows][tiles][kTail]: entries of a tile whose key is at least that of the first two
+                       // digits found and last digit b (b = 1024: those above the first two digits)
   int32_t *holes, *movers;  // [rows][limit]
   int64_t limit;       // most entries that can move
 };
@@ -373,6 +373,7 @@ constexpr int kDigits = 3;
 constexpr int kBins = 2048;
 LDEV int digit_shift(int d) { return d == 0 ? 21 : (d == 1 ? 10 : 0); }
 LDEV uint32_t digit_mask(int d) { return d == 2 ? 1023u : 2047u; }
+constexpr int kTail = 1025;
 
 LDEV void tile_range(const LongArgs &a, int n, int tile, int &begin, int &end) {
   const int keep = (int)a.e.keep;
@@ -380,66 +381,6 @@ LDEV void tile_range(const LongArgs &a, int n, int tile, int &begin, int &end) {
   const int64_t stop = tile < a.t.front ? keep : n;
   begin = (int)first;
   end = (int)(first + a.t.size < stop ? first + a.t.size : stop);
-}
-
-// What is wanted of digit d - 1's bin, by the whole workgroup (>= 64 threads); hist: 2048 words of LDS.
-LDEV void settle_digit(const LongArgs &a, int64_t row, int d, uint32_t *hist, uint32_t *found, uint32_t &prefix,
-                       uint32_t &want) {
-  prefix = 0;
-  want = (uint32_t)a.e.keep;
-  if (d == 0) return;
-  if (d > 1) {
-    prefix = a.state[row].prefix[d - 2];
-    want = a.state[row].want[d - 2];
-  }
-  const uint32_t *from = a.hist + (row * kDigits + d - 1) * kBins;
-  for (int i = threadIdx.x; i < kBins; i += blockDim.x) hist[i] = from[i];
-  __syncthreads();
-  if (threadIdx.x < 64) find_bin<11>(hist, want, &found[0], &found[1]);
-  __syncthreads();
-  prefix |= found[0] << digit_shift(d - 1);
-  want = found[1];
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    a.state[row].prefix[d - 1] = prefix;
-    a.state[row].want[d - 1] = want;
-  }
-  __syncthreads();
-}
-
-__global__ __launch_bounds__(256) void evict_clear_kernel(uint32_t *p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
-}
-
-// Digit d of the keys that begin with the digits found so far.
-__global__ __launch_bounds__(kTileThreads) void evict_digit_kernel(const LongArgs a, const int d) {
-  struct Shared {
-    uint32_t hist[kBins];
-    uint32_t found[2];
-  };
-  __shared__ Shared sh;
-  lds_poison(sh);
-  const int64_t row = grid_row();
-  if (row >= a.e.batch * a.e.heads) return;
-  const int n = evict_length(a.e, row);
-  if (n <= a.e.keep) return;
-  uint32_t prefix, want;
-  settle_digit(a, row, d, sh.hist, sh.found, prefix, want);
-  for (int i = threadIdx.x; i < kBins; i += kTileThreads) sh.hist[i] = 0;
-  __syncthreads();
-  const RowKeys keys = row_keys(a.e, row);
-  int begin, end;
-  tile_range(a, n, blockIdx.x, begin, end);
-  const int shift = digit_shift(d);
-  const uint32_t mask = digit_mask(d), high = d == 0 ? 0u : ~((mask << shift) | ((1u << shift) - 1u));
-#pragma unroll 4
-  for (int i = begin + (int)threadIdx.x; i < end; i += kTileThreads) {
-    const uint32_t k = keys.key(i);
-    if ((k & high) == prefix) atomicAdd(&sh.hist[(k >> shift) & mask], 1u);
-  }
-  __syncthreads();
-  uint32_t *to = a.hist + (row * kDigits + d) * kBins;
-  for (int i = threadIdx.x; i < kBins; i += kTileThreads)
-    if (sh.hist[i] != 0) atomicAdd(&to[i], sh.hist[i]);
 }
 
 LDEV int block_sum(int v, int *waves) {
@@ -473,8 +414,61 @@ LDEV int block_before(int v, int *waves, int &all) {
   return before;
 }
 
-// Entries above the last key, and entries that hold it, of each tile.
-__global__ __launch_bounds__(kTileThreads) void evict_count_kernel(const LongArgs a) {
+// The digits found so far, and how many of the entries that begin with them stay: digit d - 1 is
+// the bin of its histogram in which the last survivor lies, two bins a thread.
+LDEV void settle_digit(const LongArgs &a, int64_t row, int d, int *waves, uint32_t *found, uint32_t &prefix,
+                       uint32_t &want) {
+  prefix = 0;
+  want = (uint32_t)a.e.keep;
+  if (d == 0) return;
+  static_assert(kBins == 2 * kTileThreads, "two bins a thread");
+  const int pair = kTileThreads - 1 - (int)threadIdx.x;  // from the top
+  const uint2 n = reinterpret_cast<const uint2 *>(a.hist + (row * kDigits + d - 1) * kBins)[pair];
+  if (d > 1) {
+    prefix = a.state[row].prefix[d - 2];
+    want = a.state[row].want[d - 2];
+  }
+  int all;
+  const uint32_t before = (uint32_t)block_before((int)(n.x + n.y), waves, all);
+  if (before < want && want <= before + n.x + n.y) {
+    const bool upper = want <= before + n.y;
+    found[0] = 2 * (uint32_t)pair + (upper ? 1u : 0u);
+    found[1] = want - before - (upper ? 0u : n.y);
+  }
+  __syncthreads();
+  prefix |= found[0] << digit_shift(d - 1);
+  want = found[1];
+  if (d < kDigits && blockIdx.x == 0 && threadIdx.x == 0) {
+    a.state[row].prefix[d - 1] = prefix;
+    a.state[row].want[d - 1] = want;
+  }
+  __syncthreads();
+}
+
+// A tile's first kTileRounds rounds, one entry a thread and round: asked for before the digits are
+// settled, so that one latency covers the other (with that, and the digits found by the whole workgroup,
+// 8 rows of 131072 take 70 us instead of 81).  All of a tile in rows of up to 2^19 entries.
+struct Ahead {
+  int32_t position[kTileRounds];
+  float account[kTileRounds];
+  LDEV Ahead(const RowKeys &keys, int begin, int n) {
+#pragma unroll
+    for (int x = 0; x < kTileRounds; ++x) {
+      const int i = min(begin + x * kTileThreads + (int)threadIdx.x, n - 1);
+      position[x] = keys.positions[i];
+      account[x] = keys.account[i];
+    }
+  }
+};
+
+__global__ __launch_bounds__(256) void evict_clear_kernel(uint32_t *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+// Digit d of the keys that begin with the digits found so far.  With the last one a tile also
+// leaves its counts from every digit on, so that the next launch, which finds the
+// digit, has the tiles' survivors at once (8 rows of 131072: 83 us with a launch of its own for that, 81 without).
+__global__ __launch_bounds__(kTileThreads) void evict_digit_kernel(const LongArgs a, const int d) {
   struct Shared {
     uint32_t hist[kBins];
     uint32_t found[2];
@@ -486,28 +480,48 @@ __global__ __launch_bounds__(kTileThreads) void evict_count_kernel(const LongArg
   if (row >= a.e.batch * a.e.heads) return;
   const int n = evict_length(a.e, row);
   if (n <= a.e.keep) return;
-  uint32_t key, want;
-  settle_digit(a, row, kDigits, sh.hist, sh.found, key, want);
   const RowKeys keys = row_keys(a.e, row);
-  int begin, end, above = 0, same = 0;
+  int begin, end;
   tile_range(a, n, blockIdx.x, begin, end);
+  const Ahead ahead(keys, begin, n);
+  for (int i = threadIdx.x; i < kBins; i += kTileThreads) sh.hist[i] = 0;
+  uint32_t prefix, want;
+  settle_digit(a, row, d, sh.waves, sh.found, prefix, want);
+  __syncthreads();
+  const int shift = digit_shift(d);
+  const uint32_t mask = digit_mask(d), high = d == 0 ? 0u : ~((mask << shift) | ((1u << shift) - 1u));
+  int above = 0;
+  const auto count = [&](uint32_t k) {
+    if ((k & high) == prefix) atomicAdd(&sh.hist[(k >> shift) & mask], 1u);
+    above += (k & high) > prefix ? 1 : 0;
+  };
+#pragma unroll
+  for (int x = 0; x < kTileRounds; ++x)
+    if (begin + x * kTileThreads + (int)threadIdx.x < end) count(keys.key(ahead.position[x], ahead.account[x]));
 #pragma unroll 4
-  for (int i = begin + (int)threadIdx.x; i < end; i += kTileThreads) {
-    const uint32_t k = keys.key(i);
-    above += k > key ? 1 : 0;
-    same += k == key ? 1 : 0;
-  }
+  for (int i = begin + kTileMin + (int)threadIdx.x; i < end; i += kTileThreads) count(keys.key(i));
+  __syncthreads();
+  uint32_t *to = a.hist + (row * kDigits + d) * kBins;
+  for (int i = threadIdx.x; i < kBins; i += kTileThreads)
+    if (sh.hist[i] != 0) atomicAdd(&to[i], sh.hist[i]);
+  if (d != kDigits - 1) return;
+  static_assert(kTileThreads == kTail - 1, "one thread for each last digit");
   above = block_sum(above, sh.waves);
-  same = block_sum(same, sh.waves);
-  if (threadIdx.x == 0) a.counts[row * a.t.count + blockIdx.x] = int2{above, same};
+  const int digit = kTileThreads - 1 - (int)threadIdx.x, here = (int)sh.hist[digit];
+  int all;
+  const int more = block_before(here, sh.waves, all);
+  uint32_t *tail = a.tails + (row * a.t.count + blockIdx.x) * kTail;
+  tail[digit] = (uint32_t)(above + more + here);
+  if (threadIdx.x == 0) tail[kTail - 1] = (uint32_t)above;
 }
 
 // Ranks of the holes and of the survivors that fill them; the accounts and
 // positions of the entries that stay where they are.
 __global__ __launch_bounds__(kTileThreads) void evict_place_kernel(const LongArgs a) {
   struct Shared {
+    uint32_t found[2];
     int waves[kTileThreads / 64];
-    int pre[kMaxTiles];
+    int pre[2];
   };
   __shared__ Shared sh;
   lds_poison(sh);
@@ -534,11 +548,21 @@ __global__ __launch_bounds__(kTileThreads) void evict_place_kernel(const LongArg
     }
     return;
   }
-  const uint32_t key = a.state[row].prefix[kDigits - 1];
-  const int want = (int)a.state[row].want[kDigits - 1];
+  const RowKeys keys = row_keys(a.e, row);
+  int begin, end;
+  tile_range(a, n, tile, begin, end);
+  const Ahead ahead(keys, begin, n);
+  uint32_t key, of_key;
+  settle_digit(a, row, kDigits, sh.waves, sh.found, key, of_key);
+  const int want = (int)of_key;
   // tiles' survivors: entries above the key, and of those that hold it the first `want` of the row
   int all;
-  const int2 mine = tid < a.t.count ? a.counts[row * a.t.count + tid] : int2{0, 0};
+  int2 mine = {0, 0};  // entries above the key, entries that hold it
+  if (tid < a.t.count) {
+    const uint32_t *tail = a.tails + (row * a.t.count + tid) * kTail + (key & digit_mask(kDigits - 1));
+    mine.x = (int)tail[1];
+    mine.y = (int)(tail[0] - tail[1]);
+  }
   const int same_before = block_before(mine.y, sh.waves, all);
   int left = want - same_before;
   left = left < 0 ? 0 : (left < mine.y ? left : mine.y);
@@ -554,14 +578,10 @@ __global__ __launch_bounds__(kTileThreads) void evict_place_kernel(const LongArg
   int same_at = sh.pre[0], stay_at = sh.pre[1];
   if (tile == 0 && tid == 0) a.state[row].moves = keep - front;
 
-  const RowKeys keys = row_keys(a.e, row);
-  int begin, end;
-  tile_range(a, n, tile, begin, end);
   const int lane = tid % 64, wave = tid / 64;
   const unsigned long long below = (1ull << lane) - 1ull;
-  for (int at = begin; at < end; at += kTileThreads) {
+  const auto round = [&](int at, uint32_t k) {
     const int i = at + tid;
-    const uint32_t k = i < end ? keys.key(i) : 0u;
     const bool same = i < end && k == key;
     // both counts of a wave in one word
     const unsigned long long ms = __ballot(same), mg = __ballot(i < end && k > key);
@@ -601,7 +621,12 @@ __global__ __launch_bounds__(kTileThreads) void evict_place_kernel(const LongArg
     const int same_next = same_at + same_all;
     stay_at += above_all + (same_next < want ? same_next : want) - (same_at < want ? same_at : want);
     same_at = same_next;
-  }
+  };
+#pragma unroll
+  for (int x = 0; x < kTileRounds; ++x)
+    if (begin + x * kTileThreads < end)  // the same for the whole workgroup
+      round(begin + x * kTileThreads, keys.key(ahead.position[x], ahead.account[x]));
+  for (int at = begin + kTileMin; at < end; at += kTileThreads) round(at, keys.key(min(at + tid, n - 1)));
 }
 
 // The entries that move, a team of lanes each.
@@ -627,7 +652,7 @@ __global__ __launch_bounds__(256) void evict_fill_kernel(const LongArgs a) {
 }
 
 struct LongLayout {
-  size_t state, hist, counts, holes, movers, bytes;
+  size_t state, hist, tails, holes, movers, bytes;
   int64_t limit;
 };
 LongLayout long_layout(int64_t rows, int64_t capacity, int64_t keep) {
@@ -643,7 +668,7 @@ LongLayout long_layout(int64_t rows, int64_t capacity, int64_t keep) {
   if (l.limit < 1) l.limit = 1;
   l.state = take((size_t)rows * sizeof(LongRow));
   l.hist = take((size_t)rows * kDigits * kBins * sizeof(uint32_t));
-  l.counts = take((size_t)rows * t.count * sizeof(int2));
+  l.tails = take((size_t)rows * t.count * kTail * sizeof(uint32_t));
   l.holes = take((size_t)(rows * l.limit) * sizeof(int32_t));
   l.movers = take((size_t)(rows * l.limit) * sizeof(int32_t));
   l.bytes = at;
@@ -659,7 +684,7 @@ hipError_t evict_long(const EvictArgs &e, hipStream_t s) {
   a.t = tiles_of(e.capacity, e.keep);
   a.state = reinterpret_cast<LongRow *>(ws + l.state);
   a.hist = reinterpret_cast<uint32_t *>(ws + l.hist);
-  a.counts = reinterpret_cast<int2 *>(ws + l.counts);
+  a.tails = reinterpret_cast<uint32_t *>(ws + l.tails);
   a.holes = reinterpret_cast<int32_t *>(ws + l.holes);
   a.movers = reinterpret_cast<int32_t *>(ws + l.movers);
   a.limit = l.limit;
@@ -671,9 +696,6 @@ hipError_t evict_long(const EvictArgs &e, hipStream_t s) {
     evict_digit_kernel<<<grid, threads, 0, s>>>(a, d);
     err = hipGetLastError();
   }
-  if (err != hipSuccess) return err;
-  evict_count_kernel<<<grid, threads, 0, s>>>(a);
-  err = hipGetLastError();
   if (err != hipSuccess) return err;
   evict_place_kernel<<<grid, threads, 0, s>>>(a);
   err = hipGetLastError();
