@@ -662,7 +662,8 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + bh * a.splits * a.rows + row;
   float2 x = {-INFINITY, 0.0f};
   if (tid < a.splits) x = ml[(int64_t)tid * a.rows];
-  const bool again = a.news > 1 && __syncthreads_or(tid < a.splits && a.dropped[bh * a.splits + tid] != 0) != 0;
+  const bool again =
+      a.dropped != nullptr && __syncthreads_or(tid < a.splits && a.dropped[bh * a.splits + tid] != 0) != 0;
   float top = team_max<64>(x.x);
   if (tid % 64 == 0) sh.top[wave] = top;
   __syncthreads();
@@ -845,9 +846,11 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
   const bool kept = a.logits != nullptr, formed = a.account_out != nullptr && !kept;
   // the rows' lse, where the logits are formed again, follow the parts' maxima and sums
   float *lse = formed ? a.part_ml + caches * a.splits * a.rows * 2 : nullptr;
+  AttendArgs j = a;
+  if (ONE) j.dropped = nullptr;  // nothing was left out, and no flags were written
   // 512 threads where there are many parts (one sequence of 8192 entries, 91 splits: 13.7 us, 14.7 with
   // 256), 256 where there are few (128 rows, 16 splits: 52.6 us, 56.0 with 512)
-  e = a.splits > 16 ? join<T, 512>(a, lse, s) : join<T, 256>(a, lse, s);
+  e = a.splits > 16 ? join<T, 512>(j, lse, s) : join<T, 256>(j, lse, s);
   if (e != hipSuccess || !formed) return e;
   account_formed_kernel<T, DP, EXACT>
       <<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);
@@ -858,7 +861,8 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
 int whole_stride(int64_t capacity) { return (int)((capacity + kBlock - 1) / kBlock * kBlock + 4); }
 
 // 16 rows are one tile of the matrix instruction, 32 two that share the entries
-// (ONE: a single new token, whose row sees every entry); beyond, each wave takes 32
+// (ONE: up to 16 rows of a single new token, which see every entry; more rows of one token run as those of
+// several do, their values checked and joined in the same way); beyond, each wave takes 32
 // rows of its own and all entries, which leaves waves idle at up to 96 rows but is better than
 // 16 rows each, since every wave reads the keys and values (64 rows over two
 // sequences of 16384 entries: 40.9 us, with 16 rows each 48.3).  32 rows of 256
