@@ -96,6 +96,14 @@ LDEV const T *query_row(const AttendArgs &a, int64_t bh, int row) {
   return static_cast<const T *>(a.q) + ((b * a.news + i) * ((int64_t)a.heads * a.group) + h * a.group + g) * a.width;
 }
 
+// The first row that sees entry e (they are in the order of their tokens).  The accounts leave out
+// those before it rather than add their weights of 0: a row of NaN has an lse of NaN, and
+// -inf - NaN would reach entries that it does not see.
+LDEV int first_row(const AttendArgs &a, int length, int e) {
+  const int i = e - (length - a.news);
+  return i > 0 ? i * a.group : 0;
+}
+
 // this lane's part of 16 query rows (second factor of Z'): row lane % 16, zero past the rows and the width
 template <class T, int DP>
 LDEV void load_queries(const AttendArgs &a, int64_t bh, int row, pack_t<T> (&q)[DP / 32]) {
@@ -625,7 +633,8 @@ __global__ __launch_bounds__(64 * whole_waves(DP)) void attend_whole_kernel(cons
   if (a.account_out == nullptr) return;
   for (int e = threadIdx.x; e < length; e += blockDim.x) {
     float w = 0.0f;
-    for (int i = 0; i < a.rows; ++i) w += __builtin_amdgcn_exp2f(logits[i * logit_stride + e] - sh.lse[i]);
+    for (int i = ONE ? 0 : first_row(a, length, e); i < a.rows; ++i)
+      w += __builtin_amdgcn_exp2f(logits[i * logit_stride + e] - sh.lse[i]);
     a.account_out[bh * a.capacity + e] = a.account[bh * a.capacity + e] + w;
   }
 }
@@ -730,11 +739,20 @@ __global__ __launch_bounds__(TH) void attend_join_kernel(const AttendArgs a, flo
   if (e >= length) return;
   f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
   const float *z = a.logits + (bh * a.blocks + e / kBlock) * a.rows * kBlock + e % kBlock;
+  if (e + 3 <= length - a.news) {  // every row sees all four
 #pragma unroll 4
-  for (int i = 0; i < a.rows; ++i) {
-    const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
+    for (int i = 0; i < a.rows; ++i) {
+      const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) w[n] += __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
+      for (int n = 0; n < 4; ++n) w[n] += __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
+    }
+  } else {
+    for (int i = first_row(a, length, e); i < a.rows; ++i) {
+      const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        w[n] += i < first_row(a, length, e + n) ? 0.0f : __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
+    }
   }
 #pragma unroll
   for (int n = 0; n < 4; ++n)

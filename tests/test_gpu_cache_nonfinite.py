@@ -59,3 +59,31 @@ def test_value_that_the_newest_token_sees(L, caches, width, group, news):
             assert torch.equal(out[~seen], clean[~seen])
             assert torch.equal(added, account)  # the weights do not depend on the values
             assert torch.equal(torch.isnan(L.cache_attend(q, k, w, n)), torch.isnan(out))
+
+
+@pytest.mark.parametrize("news,group", [(4, 2), (4, 4), (9, 4), (40, 1)])
+@pytest.mark.parametrize("batch,capacity", [(2, 120), (2, 700), (130, 300)])
+def test_row_of_nan_gives_to_what_it_sees(L, batch, capacity, news, group):
+    """A query of NaN makes the accounts of the entries that its token sees NaN, not those of the newer ones."""
+    q, k, v = inputs(batch, 2, capacity, 64, news, group, seed=1)
+    n = torch.tensor([capacity, capacity - 37] * (batch // 2), dtype=torch.int32, device="cuda")
+    account = torch.rand(batch, 2, capacity, device="cuda")
+    bad = q.clone()
+    bad[:, 0, 0] = math.nan  # of the first new token, on key head 0
+    got = torch.full_like(account, -7.0)
+    out = L.cache_attend(bad, k, v, n, account, account_out=got)
+    clean = torch.full_like(account, -7.0)
+    want = L.cache_attend(q, k, v, n, account, account_out=clean)
+    assert torch.isnan(out[:, 0, 0]).all()
+    hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    hit[:, 0, 0] = True
+    # rows of a tile share the steps at which their bases move, so the others' bits may change: twice the bound of
+    # test_gpu_cache, with logits below 16 (delta 7e-5) and a mean |v| below 1.5
+    off = (out.float() - want.float()).abs()[~hit]
+    assert (off <= 2.0 ** -10 + 2.0 ** -7 * want.float().abs()[~hit]).all()
+    entry = torch.arange(capacity, device="cuda")
+    sees = entry[None] <= n[:, None] - news  # what the first new token sees
+    assert torch.isnan(got[:, 0][sees]).all()
+    # a newer entry gets nothing from that row either way
+    for a, b in ((got[:, 0][~sees], clean[:, 0][~sees]), (got[:, 1], clean[:, 1])):
+        assert ((a - b).abs() <= 2.0 ** -11 * (1.0 + b.abs())).all()
