@@ -800,8 +800,10 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
 #pragma unroll
     for (int n = 0; n < DP / 32; ++n) {
       const int d = n * 32 + c * 8;
-      const uint4 w = *reinterpret_cast<const uint4 *>(p + (EXACT || d < a.width ? d : 0));
-      x.q[n] = __builtin_bit_cast(pack_t<T>, w);  // past the width the keys are zero
+      const bool there = EXACT || d < a.width;
+      const uint4 w = *reinterpret_cast<const uint4 *>(p + (there ? d : 0));
+      // zero past the width, as the keys are: an infinity of the row itself would meet their zeros
+      x.q[n] = __builtin_bit_cast(pack_t<T>, there ? w : uint4{0, 0, 0, 0});
     }
     x.off = lse[bh * a.rows + row];
     x.most = row0 + r < a.rows ? length - a.news + i - e0 - 4 * c : -1;

@@ -87,3 +87,27 @@ def test_row_of_nan_gives_to_what_it_sees(L, batch, capacity, news, group):
     # a newer entry gets nothing from that row either way
     for a, b in ((got[:, 0][~sees], clean[:, 0][~sees]), (got[:, 1], clean[:, 1])):
         assert ((a - b).abs() <= 2.0 ** -11 * (1.0 + b.abs())).all()
+
+
+@pytest.mark.parametrize("width", [40, 64, 72, 96, 136, 200])
+@pytest.mark.parametrize("news,group", [(2, 4), (7, 3), (20, 4)])
+def test_row_of_minus_infinite_logits_gives_nothing(L, width, news, group):
+    """A query that makes every logit -inf has no weight: zeros, and the accounts are the other rows' alone."""
+    q, k, v = inputs(1, 1, 400, width, news, group, seed=2)
+    k[..., 0] = k[..., 0].abs() + 0.5
+    n = torch.tensor([391], dtype=torch.int32, device="cuda")
+    q[0, news - 1, group - 1, 0] = -math.inf
+    account = torch.zeros(1, 1, 400, device="cuda")
+    out = L.cache_attend(q, k, v, n, account)
+    assert (out[0, news - 1, group - 1] == 0).all()
+    q64 = q.double().cpu()
+    q64[0, news - 1, group - 1] = 0.0
+    want, added, _ = plain.attend(q64, k.double().cpu(), v.double().cpu(), [391], width ** -0.5)
+    # that row, with a query of zeros, gave each of its 391 entries the same
+    added -= 1.0 / 391
+    got = account.double().cpu()[0, 0, :391]
+    assert torch.isfinite(got).all()
+    # logits are sums of `width` products below 8 * 4 each in fp32, weights within e^(2 delta) (as in test_gpu_cache)
+    delta = (width + 4) * 2.0 ** -24 * width ** 0.5 * 32
+    bound = (2 * delta + 2.0 ** -22 + news * group * 2.0 ** -23) * (added[0, 0, :391] + 1.0 / 391) + 1e-9
+    assert ((got - added[0, 0, :391]).abs() <= bound).all()
