@@ -347,8 +347,11 @@ typedef struct lapsum_route_options {
  * gives -1 and 0 throughout.  The softmax with logits of +inf is its limit
  * (they share the mass equally).  A NaN logit makes the row's weights NaN
  * (the choice is made among the others).  Scores below 2^-126 count as 0;
- * S = 0 gives weights 0.  A group in which one expert alone is available
- * counts as one with none, unless groups are of one expert. */
+ * S = 0 gives weights 0.  The weights of a renormalised softmax are the softmax
+ * of the chosen logits alone, times scale: they are formed against the largest
+ * of these, so they do not underflow however far below the row's maximum a
+ * bias or the groups have put the choice.  A group in which one expert alone is
+ * available counts as one with none, unless groups are of one expert. */
 lapsum_status lapsum_route_forward(const void *logits, int32_t dtype, int64_t tokens, int64_t experts,
                                    int64_t row_stride, const float *bias, const lapsum_route_options *opt,
                                    float *weights, int32_t *chosen, void *stream);

@@ -339,19 +339,35 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
     }
   }
 
-  // the chosen scores: the c themselves, or formed again from the logits where a bias is in them
+  // The chosen scores: the c themselves, or formed again from the logits where a bias is in them, or where a
+  // renormalised softmax may have left out the row's maximum (by the bias, or by the groups): its weights
+  // are the softmax of the chosen logits alone, so they are formed against the maximum of those,
+  // as the gradient's are, and keep their size however far the choice lies below the row's maximum.
   float w[C], sum = 0.0f;
+  const bool soft = a.score == LAPSUM_SCORE_SOFTMAX, alone = soft && a.renormalise != 0;
+  if (a.bias == nullptr && !(alone && a.groups > 1)) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const bool there = available(mine[i]);
-    if (a.bias == nullptr) {
+    for (int i = 0; i < C; ++i) {
       const unsigned long long u = (unsigned long long)__double_as_longlong(mine[i]) & ~1023ull;
-      w[i] = there ? (float)__longlong_as_double((long long)u) : 0.0f;
-    } else {
-      const float y = there ? (float)row[expert_of(mine[i])] : -INFINITY;
-      w[i] = a.score == LAPSUM_SCORE_SOFTMAX ? share_of(y, m) * r : sigmoid(y);
+      w[i] = available(mine[i]) ? (float)__longlong_as_double((long long)u) : 0.0f;
+      sum += w[i];
     }
-    sum += w[i];
+  } else {
+    float y[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) y[i] = available(mine[i]) ? (float)row[expert_of(mine[i])] : -INFINITY;
+    if (alone) {
+      m = y[0];
+#pragma unroll
+      for (int i = 1; i < C; ++i) m = fmaxf(m, y[i]);
+      m = team_max<L>(m);
+      r = 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      w[i] = !available(mine[i]) ? 0.0f : (soft ? share_of(y[i], m) * r : sigmoid(y[i]));
+      sum += w[i];
+    }
   }
   sum = a.renormalise != 0 ? team_sum<L>(sum) : 1.0f;
   // divided first: scale / sum overflows where all of the chosen scores are small
