@@ -351,7 +351,8 @@ typedef struct lapsum_route_options {
  * of the chosen logits alone, times scale: they are formed against the largest
  * of these, so they do not underflow however far below the row's maximum a
  * bias or the groups have put the choice.  A group in which one expert alone is
- * available counts as one with none, unless groups are of one expert. */
+ * available counts as one with none, unless groups are of one expert; any
+ * two that are available come before that, whatever their sum. */
 lapsum_status lapsum_route_forward(const void *logits, int32_t dtype, int64_t tokens, int64_t experts,
                                    int64_t row_stride, const float *bias, const lapsum_route_options *opt,
                                    float *weights, int32_t *chosen, void *stream);

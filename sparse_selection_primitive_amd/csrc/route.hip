@@ -140,8 +140,9 @@ LDEV void best_two(float &b1, float &b2, float y) {
   b1 = fmaxf(b1, y);
 }
 // Their sum; a group with one available expert is as one with none, also where that one's c is +inf.
+// Two that are available never score as none: a sum below the range is the lowest number.
 LDEV float group_score(float b1, float b2, int size) {
-  return size == 1 ? b1 : (b2 == -INFINITY ? -INFINITY : b1 + b2);
+  return size == 1 ? b1 : (b2 == -INFINITY ? -INFINITY : fmaxf(b1 + b2, -kLargest));
 }
 template <int M>
 LDEV void best_two_across(float &b1, float &b2) {
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (x[v] == -INFINITY || c[v] != c[v]) c[v] = -INFINITY;
+    if (x[v] == -INFINITY || !(c[v] > -kLargest)) c[v] = -INFINITY;  // not available: NaN and the lowest number too
 
   if (a.groups > 1) {
     float *group = sh.group[wave][team];

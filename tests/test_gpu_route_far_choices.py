@@ -83,3 +83,32 @@ def test_gradient_is_the_forwards(L):
         e = torch.zeros_like(x)
         e[0, i] = h
         assert float((weights(x + e) - weights(x - e)) / (2 * h)) == pytest.approx(float(dx[0, i]), abs=4 * h * h + 1e-4)
+
+
+@pytest.mark.parametrize("experts,groups", [(8, 2), (64, 8), (60, 4), (256, 8)])
+def test_group_score_past_the_range_is_a_score(L, experts, groups):
+    """Two experts whose c are each below half of the lowest fp32 number are available: their group, whose sum is past
+    the range, comes before one without experts."""
+    size = experts // groups
+    x, bias = r.grid_logits(5, experts, 7), torch.zeros(experts)
+    x[:, :-size] = -math.inf
+    bias[-size:] = -3.0e38
+    _, c = L.route_forward(x.float().cuda(), 2, bias.cuda(), score="sigmoid", groups=groups, top_groups=1)
+    assert c.cpu().tolist() == [[experts - size, experts - size + 1]] * 5  # c are equal in fp32
+
+
+@pytest.mark.parametrize("experts,groups", [(8, 2), (64, 8), (60, 4), (256, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_mask_of_the_lowest_number_is_one_of_minus_infinity(L, score, experts, groups):
+    """In a bias, the lowest fp32 number takes an expert out as -inf does, for its group's score as well."""
+    size = experts // groups
+    x = r.grid_logits(6, experts, 13).float().cuda()
+    for left in ([], [1], [1, 2], [0, 3]):  # the experts that stay in the last group; the other groups have none
+        out = []
+        for mask in (-math.inf, torch.finfo(torch.float32).min):
+            bias = torch.full((experts,), mask)
+            bias[[experts - size + i for i in left]] = 0.25
+            out.append(L.route_forward(x, 2, bias.cuda(), score=score, groups=groups, top_groups=1))
+        assert torch.equal(out[0][1], out[1][1]) and torch.equal(out[0][0], out[1][0])
+        want = [experts - size + i for i in left] if len(left) > 1 else [-1, -1]
+        assert sorted(out[0][1][0].tolist()) == want
