@@ -443,7 +443,8 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
 /* Eviction: of the entries 0 .. length - 1 of each sequence and head the
  * first `keep` in this order stay: protected entries, then by account
  * descending (NaN last), then by slot ascending.  An entry is protected if
- * its position is below `sinks`, or at least next_position[b] - recent.
+ * its position is below `sinks` (a negative one always is), or, where recent is
+ * not 0, at least next_position[b] - recent.
  * Survivors at slot `keep` and behind move into the holes before it, the
  * n-th survivor into the n-th hole; the others stay where they are.  k and v
  * are changed in place.

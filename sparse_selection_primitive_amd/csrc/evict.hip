@@ -46,10 +46,10 @@ LDEV int evict_length(const EvictArgs &a, int64_t row) {
 struct RowKeys {
   const float *account;
   const int32_t *positions;
-  int32_t sinks, from;  // protected: position < sinks or position >= from
+  int32_t sinks, past;  // protected: position < sinks or position > past
   LDEV uint32_t key(int64_t i) const { return key(positions[i], account[i]); }
   LDEV uint32_t key(int32_t p, float x) const {
-    if (p < sinks || p >= from) return 0xFFFFFFFFu;
+    if (p < sinks || p > past) return 0xFFFFFFFFu;
     return x != x ? 0u : key_of(x + 0.0f);  // -0 counts as 0
   }
 };
@@ -58,10 +58,10 @@ LDEV RowKeys row_keys(const EvictArgs &a, int64_t row) {
   k.account = a.account + row * a.capacity;
   k.positions = a.positions + row * a.capacity;
   k.sinks = a.sinks;
-  k.from = INT32_MAX;
+  k.past = INT32_MAX;  // none
   if (a.recent > 0) {
-    const int64_t f = (int64_t)a.next_position[row / a.heads] - a.recent;
-    k.from = (int32_t)(f < INT32_MIN ? INT32_MIN : f);
+    const int64_t past = (int64_t)a.next_position[row / a.heads] - a.recent - 1;
+    k.past = (int32_t)(past < INT32_MIN ? INT32_MIN : past);  // the lowest position is below the sinks, so all are protected
   }
   return k;
 }

@@ -488,7 +488,7 @@ def _evict_bytes(code, k_shape, keep):
 def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, sinks=0, recent=0, account_out=None,
                 positions_out=None):
     """Brings every cache row down to `keep` entries: protected entries (position below sinks, or at least
-    next_position[b] - recent) stay first, then those of the highest account (ties: the lowest slot).  Survivors
+    next_position[b] - recent where recent is not 0) stay first, then those of the highest account (ties: the lowest slot).  Survivors
     behind slot keep move into the holes before it, keys, values, accounts and positions; k and v are changed in
     place, account and positions too unless account_out and positions_out are given.
 
