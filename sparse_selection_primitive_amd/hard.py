@@ -384,11 +384,14 @@ def dispatch(x, slot, offsets):
     class _Dispatch(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x):
-            return dispatch_forward(x, slot, offsets)
+            xs = dispatch_forward(x, slot, offsets)
+            ctx.save_for_backward(slot)  # autograd notices if it is written again before the backward
+            return xs
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dxs):
+            slot, = ctx.saved_tensors
             return dispatch_backward(dxs.contiguous(), slot)
 
     return _Dispatch.apply(x)
@@ -401,13 +404,14 @@ def combine(ys, weights, slot, offsets):
     class _Combine(torch.autograd.Function):
         @staticmethod
         def forward(ctx, ys, weights):
-            ctx.save_for_backward(ys, weights)
-            return combine_forward(ys, slot, weights)
+            y = combine_forward(ys, slot, weights)
+            ctx.save_for_backward(ys, weights, slot, offsets)
+            return y
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dy):
-            ys, weights = ctx.saved_tensors
+            ys, weights, slot, offsets = ctx.saved_tensors
             return combine_backward(dy, ys, slot, weights, offsets)
 
     return _Combine.apply(ys, weights)

@@ -1,0 +1,101 @@
+"""The differentiable entry points of the hard selections: what they keep for the backward, and for how long.
+
+The CPU cases run them over plain forms in place of the kernels' calls, which need a GPU."""
+import gc
+import weakref
+
+import pytest
+
+import sparse_selection_primitive_amd as L
+from sparse_selection_primitive_amd import hard
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    """hard.py's calls by torch on the CPU."""
+    def pick(rows, slot):
+        return rows[slot.clamp(min=0).long()] * (slot >= 0)[..., None]
+
+    def route_forward(x, k, bias=None, **kw):
+        top = torch.topk(x if bias is None else x + bias, k, 1).indices
+        return torch.softmax(x.gather(1, top), 1), top.int()
+
+    def route_backward(dw, x, chosen, **kw):
+        with torch.enable_grad():
+            y = x.detach().requires_grad_(True)
+            return torch.autograd.grad(torch.softmax(y.gather(1, chosen.long()), 1), y, dw)[0]
+
+    def dispatch_forward(x, slot, offsets):
+        xs = x.new_zeros(slot.numel(), x.shape[1])
+        xs[slot.flatten().long()] = x.repeat_interleave(slot.shape[1], 0)
+        return xs
+    monkeypatch.setattr(hard, "torch", torch)
+    monkeypatch.setattr(hard, "_gpu", lambda x, *a: x)
+    monkeypatch.setattr(hard, "route_forward", route_forward)
+    monkeypatch.setattr(hard, "route_backward", route_backward)
+    monkeypatch.setattr(hard, "dispatch_forward", dispatch_forward)
+    monkeypatch.setattr(hard, "dispatch_backward", lambda d, slot: pick(d, slot).sum(1))
+    monkeypatch.setattr(hard, "combine_forward", lambda ys, slot, w: (pick(ys, slot) * w[..., None]).sum(1))
+    monkeypatch.setattr(hard, "combine_backward", lambda dy, ys, slot, w, o: (
+        dispatch_forward(dy, slot, o) * w.flatten()[torch.argsort(slot.flatten())][:, None],
+        (pick(ys, slot) * dy[:, None]).sum(2)))
+
+
+def pairs(device="cpu"):
+    slot = torch.tensor([[1, 3], [0, 2], [5, 4]], dtype=torch.int32, device=device)
+    return slot, torch.tensor([0, 2, 4, 6], dtype=torch.int32, device=device)
+
+
+def test_gradients(plain):
+    slot, offsets = pairs()
+    x = torch.randn(3, 5, dtype=torch.float64, requires_grad=True)
+    logits = torch.randn(3, 4, dtype=torch.float64, requires_grad=True)
+    bias = torch.randn(4, dtype=torch.float64, requires_grad=True)
+
+    def f(x, logits):
+        w, chosen = L.route(logits, 2, bias)
+        assert not chosen.requires_grad
+        return L.combine(3.0 * L.dispatch(x, slot, offsets), w, slot, offsets)
+    assert torch.autograd.gradcheck(f, (x, logits))
+    f(x, logits).sum().backward()
+    assert bias.grad is None
+    # the bias alone has no gradient to give
+    assert not L.route(logits.detach(), 2, bias)[0].requires_grad
+    # one of combine's two
+    ys, w = torch.randn(6, 5, dtype=torch.float64), torch.rand(3, 2, dtype=torch.float64)
+    for a, b in ((True, False), (False, True)):
+        y, v = ys.clone().requires_grad_(a), w.clone().requires_grad_(b)
+        L.combine(y, v, slot, offsets).sum().backward()
+        assert (y.grad is not None) == a and (v.grad is not None) == b
+
+
+def test_what_is_written_before_the_backward_is_noticed(plain):
+    """A buffer of slots that holds the next batch's when the backward runs must not give a wrong gradient in silence."""
+    check_written("cpu")
+
+
+def check_written(device):
+    x = torch.randn(3, 8, device=device, requires_grad=True)
+    w = torch.rand(3, 2, device=device, requires_grad=True)
+    for what in ("slot", "offsets"):
+        for call in ("dispatch", "combine"):
+            slot, offsets = pairs(device)
+            if call == "dispatch":
+                y = L.dispatch(x, slot, offsets)
+                if what == "offsets":
+                    continue  # its backward does not use them
+            else:
+                y = L.combine(torch.ones(6, 8, device=device), w, slot, offsets)
+            (slot if what == "slot" else offsets).fill_(0)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.sum().backward()
+
+
+@pytest.mark.gpu
+def test_on_the_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    L.dispatch_plan(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 1)  # binds
+    check_written("cuda")
