@@ -229,23 +229,9 @@ def route(logits, k, bias=None, *, score="softmax", groups=1, top_groups=None, r
     """Differentiable route_forward: the weights' gradient reaches the logits.  The choice is not differentiable, so
     the bias, which takes part in nothing else, gets no gradient."""
     _gpu(logits, "logits", 2)
-
-    class _Route(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x):
-            weights, chosen = route_forward(x, k, bias, score=score, groups=groups, top_groups=top_groups,
-                                            renormalise=renormalise, scale=scale)
-            ctx.save_for_backward(x, chosen)
-            ctx.mark_non_differentiable(chosen)
-            return weights, chosen
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, dweights, _):
-            x, chosen = ctx.saved_tensors
-            return route_backward(dweights.contiguous(), x, chosen, score=score, renormalise=renormalise, scale=scale)
-
-    return _Route.apply(logits)
+    if bias is not None and getattr(bias, "requires_grad", False):
+        bias = bias.detach()  # or weights that cannot have a gradient would ask for one
+    return _differentiable()[0].apply(logits, k, bias, score, groups, top_groups, renormalise, scale)
 
 
 # --------------------------------------------------------------- dispatch
@@ -380,41 +366,66 @@ def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
 def dispatch(x, slot, offsets):
     """Differentiable dispatch_forward."""
     _gpu(x, "x", 2)
-
-    class _Dispatch(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, x):
-            xs = dispatch_forward(x, slot, offsets)
-            ctx.save_for_backward(slot)  # autograd notices if it is written again before the backward
-            return xs
-
-        @staticmethod
-        @torch.autograd.function.once_differentiable
-        def backward(ctx, dxs):
-            slot, = ctx.saved_tensors
-            return dispatch_backward(dxs.contiguous(), slot)
-
-    return _Dispatch.apply(x)
+    return _differentiable()[1].apply(x, slot, offsets)
 
 
 def combine(ys, weights, slot, offsets):
     """Differentiable combine_forward: gradients reach the experts' outputs and the weights."""
     _gpu(ys, "ys", 2)
+    return _differentiable()[2].apply(ys, weights, slot, offsets)
 
-    class _Combine(torch.autograd.Function):
+
+# ---------------------------------------------------------- differentiable
+@functools.lru_cache(maxsize=None)
+def _differentiable():
+    """The autograd functions of route, dispatch and combine, made once torch is bound (a class made by each call takes
+    longer than the call, and as a cycle keeps what it closes over until the collector runs)."""
+    once = torch.autograd.function.once_differentiable
+
+    class Route(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, ys, weights):
+        def forward(ctx, x, k, bias, score, groups, top_groups, renormalise, scale):
+            weights, chosen = route_forward(x, k, bias, score=score, groups=groups, top_groups=top_groups,
+                                            renormalise=renormalise, scale=scale)
+            ctx.save_for_backward(x, chosen)
+            ctx.options = dict(score=score, renormalise=renormalise, scale=scale)
+            ctx.mark_non_differentiable(chosen)
+            return weights, chosen
+
+        @staticmethod
+        @once
+        def backward(ctx, dweights, _):
+            x, chosen = ctx.saved_tensors
+            return (route_backward(dweights.contiguous(), x, chosen, **ctx.options), *[None] * 7)
+
+    # slots and offsets are saved, so autograd notices if they are written again before the backward
+    class Dispatch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, slot, offsets):
+            xs = dispatch_forward(x, slot, offsets)
+            ctx.save_for_backward(slot)
+            return xs
+
+        @staticmethod
+        @once
+        def backward(ctx, dxs):
+            slot, = ctx.saved_tensors
+            return dispatch_backward(dxs.contiguous(), slot), None, None
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ys, weights, slot, offsets):
             y = combine_forward(ys, slot, weights)
             ctx.save_for_backward(ys, weights, slot, offsets)
             return y
 
         @staticmethod
-        @torch.autograd.function.once_differentiable
+        @once
         def backward(ctx, dy):
             ys, weights, slot, offsets = ctx.saved_tensors
-            return combine_backward(dy, ys, slot, weights, offsets)
+            return (*combine_backward(dy, ys, slot, weights, offsets), None, None)
 
-    return _Combine.apply(ys, weights)
+    return Route, Dispatch, Combine
 
 
 # ------------------------------------------------------------------ cache

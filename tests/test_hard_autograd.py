@@ -93,9 +93,43 @@ def check_written(device):
                 y.sum().backward()
 
 
+def check_released(device):
+    """Nothing is kept by a cycle: what a call took is free once its results are."""
+    gc.collect()
+    gc.disable()
+    try:
+        slot, offsets = pairs(device)
+        bias = torch.zeros(4, device=device)
+        x = torch.randn(3, 8, device=device, requires_grad=True)
+        logits = torch.randn(3, 4, device=device, requires_grad=True)
+        w, chosen = L.route(logits, 2, bias)
+        y = L.combine(L.dispatch(x, slot, offsets), w, slot, offsets)
+        y.sum().backward()
+        refs = [weakref.ref(t) for t in (slot, offsets, bias, x, logits, w, chosen)]
+        del slot, offsets, bias, x, logits, w, chosen, y
+        assert [r() is None for r in refs] == [True] * len(refs)
+    finally:
+        gc.enable()
+
+
+def test_nothing_outlives_a_call(plain):
+    check_released("cpu")
+
+
+def test_one_class_each(plain):
+    """The node of the graph is of the same class at every call."""
+    slot, offsets = pairs()
+    x = torch.randn(3, 8, requires_grad=True)
+    w = torch.rand(3, 2, requires_grad=True)
+    nodes = [[type(L.route(x, 2)[0].grad_fn), type(L.dispatch(x, slot, offsets).grad_fn),
+              type(L.combine(torch.ones(6, 8), w, slot, offsets).grad_fn)] for _ in range(2)]
+    assert nodes[0] == nodes[1]
+
+
 @pytest.mark.gpu
 def test_on_the_gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     L.dispatch_plan(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 1)  # binds
     check_written("cuda")
+    check_released("cuda")
