@@ -483,6 +483,9 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     elif account_out is not None:
         raise LapsumError("account_out needs an account")
     if q.numel() == 0:
+        if account is not None and account_out is not account:  # nothing is added to what the entries have
+            there = torch.arange(k.shape[2], device=dev) < lengths[:, None, None]
+            account_out.copy_(torch.where(there, account, account_out))
         return out
     nbytes = _attend_bytes(cache.dtype, k.shape, news, q_heads, int(account is not None))
     ws, wptr, wlen = _workspace(nbytes, dev)

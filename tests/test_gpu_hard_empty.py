@@ -1,0 +1,30 @@
+"""Calls without tokens, or without sequences, and sizes that nothing can be allocated for."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import sparse_selection_primitive_amd as lib
+    lib.load_library()
+    return lib
+
+
+def test_attend_without_new_tokens(L):
+    """Nothing is added: account_out is account, in the filled entries."""
+    k = torch.randn(3, 2, 40, 64, device="cuda").bfloat16()
+    q = torch.empty(3, 0, 4, 64, device="cuda", dtype=torch.bfloat16)
+    n = torch.tensor([40, -3, 17], dtype=torch.int32, device="cuda")
+    account = torch.rand(3, 2, 40, device="cuda")
+    before, to = account.clone(), torch.full_like(account, -7.0)
+    out = L.cache_attend(q, k, k, n, account, account_out=to)
+    assert out.shape == (3, 0, 4, 64) and torch.equal(account, before)
+    there = torch.arange(40, device="cuda") < n[:, None, None].expand(3, 2, 1)
+    assert torch.equal(to, torch.where(there, account, -7.0))
+    assert L.cache_attend(q, k, k, n, account).shape == (3, 0, 4, 64) and torch.equal(account, before)
+    assert L.cache_attend(q, k, k, n).shape == (3, 0, 4, 64)
