@@ -533,6 +533,8 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
         next_position = _array(next_position, "next_position", torch.int32, (batch,), dev)
     kept = torch.empty((*shape[:2], max(keep, 0)), dtype=torch.int32, device=dev)
     lengths_out = torch.empty_like(lengths)
+    if shape[0] * shape[1] == 0 and 1 <= keep <= shape[2]:  # no cache
+        return kept, lengths.clamp(0, keep)
     ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, k.shape, keep), dev)
     _call(dev, "lapsum_cache_evict", cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,
           None if next_position is None else next_position.data_ptr(), _int32(sinks, "sinks"),

@@ -28,3 +28,17 @@ def test_attend_without_new_tokens(L):
     assert torch.equal(to, torch.where(there, account, -7.0))
     assert L.cache_attend(q, k, k, n, account).shape == (3, 0, 4, 64) and torch.equal(account, before)
     assert L.cache_attend(q, k, k, n).shape == (3, 0, 4, 64)
+
+
+@pytest.mark.parametrize("batch,heads", [(0, 2), (3, 0), (0, 0)])
+def test_no_cache(L, batch, heads):
+    k = torch.empty(batch, heads, 40, 64, device="cuda", dtype=torch.bfloat16)
+    a = torch.empty(batch, heads, 40, device="cuda")
+    n = torch.tensor([40, -3, 17][:batch], dtype=torch.int32, device="cuda")
+    kept, after = L.cache_evict(k, k.clone(), a, a.int(), n, 20)
+    assert kept.shape == (batch, heads, 20) and kept.dtype == torch.int32
+    assert after.tolist() == [20, 0, 17][:batch] and after.dtype == torch.int32
+    with pytest.raises(L.LapsumError):
+        L.cache_evict(k, k.clone(), a, a.int(), n, 41)
+    with pytest.raises(L.LapsumError):
+        L.cache_evict(k, k.clone(), a, a.int(), n, 0)
