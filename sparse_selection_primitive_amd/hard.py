@@ -103,6 +103,14 @@ def _int32(x, name):
     return x
 
 
+def _size(x, name, most):
+    """A size that arrays are made by: checked before they are."""
+    x = int(x)
+    if not 1 <= x <= most:
+        raise LapsumError(f"{name} must be 1 to {most}")
+    return x
+
+
 def _dtype(x, name, only=None):
     code = _TYPES.get(x.dtype)
     if code is None or (only is not None and code not in only):
@@ -192,7 +200,7 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
     code = _dtype(_gpu(logits, "logits", 2), "logits")
     x, tokens, experts, stride = _rows(logits, "logits")
     dev = x.device
-    opt = _route_options(int(k), score, int(groups), top_groups, renormalise, float(scale))
+    opt = _route_options(_size(k, "k", min(experts, MAX_CHOICES)), score, int(groups), top_groups, renormalise, float(scale))
     if bias is not None:
         bias = _array(bias, "bias", torch.float32, (experts,), dev)
     weights = _out(None if out is None else out[0], "weights", torch.float32, (tokens, opt.k), dev)
@@ -249,7 +257,7 @@ def dispatch_plan(chosen, experts):
         if done is not None:
             return done
     _gpu(chosen, "chosen", 2)
-    (tokens, k), dev, experts = chosen.shape, chosen.device, int(experts)
+    (tokens, k), dev, experts = chosen.shape, chosen.device, _size(experts, "experts", MAX_EXPERTS)
     chosen = _array(chosen, "chosen", torch.int32, (tokens, k), dev)
     if tokens * k == 0:
         return (torch.zeros(experts + 1, dtype=torch.int32, device=dev), torch.empty_like(chosen),
@@ -518,7 +526,7 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
         if done is not None:
             return done
     cache = _cache_of(k, v)
-    dev, batch, keep = k.device, k.shape[0], int(keep)
+    dev, batch, keep = k.device, k.shape[0], _size(keep, "keep", k.shape[2])
     shape = k.shape[:3]
     # arrays that are written in place have to be usable as they are
     account = _out(account, "account", torch.float32, shape, dev) if account_out is None else _array(
@@ -531,9 +539,9 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
     lengths = _array(lengths, "lengths", torch.int32, (batch,), dev)
     if next_position is not None:
         next_position = _array(next_position, "next_position", torch.int32, (batch,), dev)
-    kept = torch.empty((*shape[:2], max(keep, 0)), dtype=torch.int32, device=dev)
+    kept = torch.empty((*shape[:2], keep), dtype=torch.int32, device=dev)
     lengths_out = torch.empty_like(lengths)
-    if shape[0] * shape[1] == 0 and 1 <= keep <= shape[2]:  # no cache
+    if shape[0] * shape[1] == 0:  # no cache
         return kept, lengths.clamp(0, keep)
     ws, wptr, wlen = _workspace(_evict_bytes(cache.dtype, k.shape, keep), dev)
     _call(dev, "lapsum_cache_evict", cache, account.data_ptr(), positions.data_ptr(), lengths.data_ptr(), keep,

@@ -42,3 +42,21 @@ def test_no_cache(L, batch, heads):
         L.cache_evict(k, k.clone(), a, a.int(), n, 41)
     with pytest.raises(L.LapsumError):
         L.cache_evict(k, k.clone(), a, a.int(), n, 0)
+
+
+@pytest.mark.parametrize("size", [2 ** 29, 2 ** 31, 2 ** 40, 2 ** 62, 2 ** 64 + 5, 10 ** 30])
+def test_sizes_out_of_range_are_refused_before_anything_is_allocated(L, size):
+    k = torch.zeros(64, 64, 8, 64, device="cuda", dtype=torch.bfloat16)
+    a = torch.zeros(64, 64, 8, device="cuda")
+    n = torch.full((64,), 8, dtype=torch.int32, device="cuda")
+    x = torch.randn(4096, 16, device="cuda")
+    c = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    for sign in (1, -1):
+        for bad in (lambda: L.cache_evict(k, k, a, a.int(), n, sign * size), lambda: L.route_forward(x, sign * size),
+                    lambda: L.dispatch_plan(c, sign * size), lambda: L.dispatch_plan(c[:0], sign * size)):
+            with pytest.raises(L.LapsumError):
+                bad()
+    assert torch.cuda.max_memory_allocated() - held < 2 ** 20
