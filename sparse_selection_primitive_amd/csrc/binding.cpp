@@ -1,7 +1,7 @@
 // Native front of the hard selections' Python binding: the calls of hard.py
 // for arguments that need no conversion (right types, contiguous, on the current
 // device), without the interpreter's share of the checks and allocations (about 4 us a
-// call).  Every function returns None for anything else, errors included, and hard.py then
+// call).  Every function returns None for anything else, refusals included, and hard.py then
 // takes its own way, which converts or raises.  It holds no kernel and no formula: it calls
 // the C ABI through addresses that hard.py hands over.
 #define PY_SSIZE_T_CLEAN
@@ -39,6 +39,19 @@ Entries entry{};
 PyObject *none() {
   if (PyErr_Occurred()) PyErr_Clear();
   Py_RETURN_NONE;
+}
+
+PyObject *failed = nullptr;  // raises for (status, name)
+
+// After a C call that did not succeed.  Arguments that it refuses are hard.py's to explain; a
+// launch that failed is raised here and not sent again, since an earlier one of the same call may
+// have changed what it works on.
+PyObject *refused(lapsum_status st, const char *name) {
+  if (st != LAPSUM_ERR_HIP || failed == nullptr) return none();
+  PyObject *done = PyObject_CallFunction(failed, "is", (int)st, name);
+  if (done == nullptr) return nullptr;
+  Py_DECREF(done);
+  return none();
 }
 
 // A GPU tensor on the current device, or null.
@@ -108,6 +121,15 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// (callable): what raises for a status and a name
+PyObject *on_failure(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n != 1) return none();
+  Py_INCREF(args[0]);
+  Py_XDECREF(failed);
+  failed = args[0];
+  Py_RETURN_NONE;
+}
+
 // (logits, bias, k, score, groups, top_groups, renormalise, scale)
 PyObject *route_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   BODY(8)
@@ -122,10 +144,11 @@ PyObject *route_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   o.scale = (float)PyFloat_AsDouble(args[7]);
   if (PyErr_Occurred() || o.k < 1 || o.k > LAPSUM_MAX_CHOICES) return none();
   at::Tensor w = make(dev, {x->size(0), o.k}, at::kFloat), c = make(dev, {x->size(0), o.k}, at::kInt);
-  if (entry.route_forward(x->data_ptr(), dtype_of(*x), x->size(0), x->size(1), x->stride(0),
+  const lapsum_status st =
+      entry.route_forward(x->data_ptr(), dtype_of(*x), x->size(0), x->size(1), x->stride(0),
                           bias ? static_cast<const float *>(bias->data_ptr()) : nullptr, &o,
-                          static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(c.data_ptr()), stream_of(*x)))
-    return none();
+                          static_cast<float *>(w.data_ptr()), static_cast<int32_t *>(c.data_ptr()), stream_of(*x));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_route_forward");
   return pair(std::move(w), std::move(c));
   END
 }
@@ -145,10 +168,11 @@ PyObject *route_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   o.scale = (float)PyFloat_AsDouble(args[5]);
   if (PyErr_Occurred()) return none();
   at::Tensor dx = make(dev, {x->size(0), x->size(1)}, x->scalar_type());
-  if (entry.route_backward(static_cast<const float *>(dw->data_ptr()), x->data_ptr(), dtype_of(*x), x->size(0),
+  const lapsum_status st =
+      entry.route_backward(static_cast<const float *>(dw->data_ptr()), x->data_ptr(), dtype_of(*x), x->size(0),
                            x->size(1), x->stride(0), static_cast<const int32_t *>(c->data_ptr()), &o, dx.data_ptr(),
-                           stream_of(*x)))
-    return none();
+                           stream_of(*x));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_route_backward");
   return wrap(std::move(dx));
   END
 }
@@ -165,10 +189,11 @@ PyObject *dispatch_plan(PyObject *, PyObject *const *args, Py_ssize_t n) {
   at::Tensor offsets = make(dev, {experts + 1}, at::kInt), slot = make(dev, {tokens, k}, at::kInt);
   at::Tensor order = make(dev, {tokens * k}, at::kInt);
   const Workspace ws(dev, entry.plan_bytes(tokens, k, experts));
-  if (entry.plan(static_cast<const int32_t *>(c->data_ptr()), tokens, k, experts,
+  const lapsum_status st =
+      entry.plan(static_cast<const int32_t *>(c->data_ptr()), tokens, k, experts,
                  static_cast<int32_t *>(offsets.data_ptr()), static_cast<int32_t *>(slot.data_ptr()),
-                 static_cast<int32_t *>(order.data_ptr()), ws.at, ws.bytes, stream_of(*c)))
-    return none();
+                 static_cast<int32_t *>(order.data_ptr()), ws.at, ws.bytes, stream_of(*c));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_dispatch_plan");
   return Py_BuildValue("(NNN)", wrap(std::move(offsets)), wrap(std::move(slot)), wrap(std::move(order)));
   END
 }
@@ -182,11 +207,12 @@ PyObject *dispatch_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const at::Tensor *x = gpu(dev, args[0]), *s = gpu(dev, args[1]), *o = gpu(dev, args[2]);
   if (!rows(x) || !slots(s) || s->size(0) != x->size(0) || !offsets_of(o)) return none();
   at::Tensor xs = make(dev, {s->numel(), x->size(1)}, x->scalar_type());
-  if (entry.dispatch_forward(x->data_ptr(), dtype_of(*x), x->size(0), s->size(1), x->size(1), x->stride(0),
+  const lapsum_status st =
+      entry.dispatch_forward(x->data_ptr(), dtype_of(*x), x->size(0), s->size(1), x->size(1), x->stride(0),
                              static_cast<const int32_t *>(s->data_ptr()),
                              static_cast<const int32_t *>(o->data_ptr()), o->numel() - 1, xs.data_ptr(),
-                             stream_of(*x)))
-    return none();
+                             stream_of(*x));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_dispatch_forward");
   return wrap(std::move(xs));
   END
 }
@@ -202,9 +228,10 @@ PyObject *dispatch_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const at::Tensor *t = gpu(dev, args[0]), *s = gpu(dev, args[1]);
   if (!slots(s) || !expert_rows(t, s)) return none();
   at::Tensor dx = make(dev, {s->size(0), t->size(1)}, t->scalar_type());
-  if (entry.dispatch_backward(t->data_ptr(), dtype_of(*t), s->size(0), s->size(1), t->size(1),
-                              static_cast<const int32_t *>(s->data_ptr()), dx.data_ptr(), stream_of(*t)))
-    return none();
+  const lapsum_status st =
+      entry.dispatch_backward(t->data_ptr(), dtype_of(*t), s->size(0), s->size(1), t->size(1),
+                              static_cast<const int32_t *>(s->data_ptr()), dx.data_ptr(), stream_of(*t));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_dispatch_backward");
   return wrap(std::move(dx));
   END
 }
@@ -215,10 +242,11 @@ PyObject *combine_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const at::Tensor *t = gpu(dev, args[0]), *s = gpu(dev, args[1]), *w = gpu(dev, args[2]);
   if (!slots(s) || !expert_rows(t, s) || !plain(w, at::kFloat, s->numel()) || w->sizes() != s->sizes()) return none();
   at::Tensor y = make(dev, {s->size(0), t->size(1)}, t->scalar_type());
-  if (entry.combine_forward(t->data_ptr(), dtype_of(*t), s->size(0), s->size(1), t->size(1),
+  const lapsum_status st =
+      entry.combine_forward(t->data_ptr(), dtype_of(*t), s->size(0), s->size(1), t->size(1),
                             static_cast<const int32_t *>(s->data_ptr()), static_cast<const float *>(w->data_ptr()),
-                            y.data_ptr(), stream_of(*t)))
-    return none();
+                            y.data_ptr(), stream_of(*t));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_combine_forward");
   return wrap(std::move(y));
   END
 }
@@ -233,11 +261,12 @@ PyObject *combine_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return none();
   at::Tensor dys = make(dev, {t->size(0), t->size(1)}, t->scalar_type());
   at::Tensor dw = make(dev, {s->size(0), s->size(1)}, at::kFloat);
-  if (entry.combine_backward(dy->data_ptr(), dy->stride(0), t->data_ptr(), dtype_of(*t), s->size(0), s->size(1),
+  const lapsum_status st =
+      entry.combine_backward(dy->data_ptr(), dy->stride(0), t->data_ptr(), dtype_of(*t), s->size(0), s->size(1),
                              t->size(1), static_cast<const int32_t *>(s->data_ptr()),
                              static_cast<const float *>(w->data_ptr()), static_cast<const int32_t *>(o->data_ptr()),
-                             o->numel() - 1, dys.data_ptr(), static_cast<float *>(dw.data_ptr()), stream_of(*t)))
-    return none();
+                             o->numel() - 1, dys.data_ptr(), static_cast<float *>(dw.data_ptr()), stream_of(*t));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_combine_backward");
   return pair(std::move(dys), std::move(dw));
   END
 }
@@ -285,11 +314,12 @@ PyObject *cache_attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (PyErr_Occurred()) return none();
   at::Tensor out = make(dev, q->sizes(), q->scalar_type());
   const Workspace ws(dev, entry.attend_bytes(&c, q->size(1), q->size(2), accounts ? 1 : 0));
-  if (entry.attend(q->data_ptr(), &c, static_cast<const int32_t *>(lengths->data_ptr()), q->size(1), q->size(2),
+  const lapsum_status st =
+      entry.attend(q->data_ptr(), &c, static_cast<const int32_t *>(lengths->data_ptr()), q->size(1), q->size(2),
                    (float)scale, accounts ? static_cast<const float *>(in->data_ptr()) : nullptr,
                    accounts ? static_cast<float *>(to->data_ptr()) : nullptr, out.data_ptr(), ws.at, ws.bytes,
-                   stream_of(*q)))
-    return none();
+                   stream_of(*q));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_cache_attend");
   return wrap(std::move(out));
   END
 }
@@ -311,20 +341,22 @@ PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (PyErr_Occurred() || keep < 1 || keep > c.capacity) return none();
   at::Tensor kept = make(dev, {c.batch, c.heads, keep}, at::kInt), after = make(dev, {c.batch}, at::kInt);
   const Workspace ws(dev, entry.evict_bytes(&c, keep));
-  if (entry.evict(&c, static_cast<const float *>(account->data_ptr()),
+  const lapsum_status st =
+      entry.evict(&c, static_cast<const float *>(account->data_ptr()),
                   static_cast<const int32_t *>(positions->data_ptr()),
                   static_cast<const int32_t *>(lengths->data_ptr()), keep,
                   next ? static_cast<const int32_t *>(next->data_ptr()) : nullptr, sinks, recent,
                   static_cast<float *>(account_out->data_ptr()), static_cast<int32_t *>(positions_out->data_ptr()),
                   static_cast<int32_t *>(kept.data_ptr()), static_cast<int32_t *>(after.data_ptr()), ws.at, ws.bytes,
-                  stream_of(*k)))
-    return none();
+                  stream_of(*k));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_cache_evict");
   return pair(std::move(kept), std::move(after));
   END
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),
+                         METHOD(on_failure),
                          METHOD(route_forward),
                          METHOD(route_backward),
                          METHOD(dispatch_plan),

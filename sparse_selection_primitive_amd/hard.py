@@ -92,6 +92,7 @@ def _bind():
         native = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(native)
         native.bind(*[ctypes.cast(getattr(lib, "lapsum_" + name), ctypes.c_void_p).value for name in _NATIVE_CALLS])
+        native.on_failure(_check)
         _native = native
 
 
