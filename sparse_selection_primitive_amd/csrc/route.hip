@@ -296,11 +296,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
       constexpr unsigned long long kTeam = L == 64 ? ~0ull : (1ull << (L % 64)) - 1ull;
       open |= ((in >> (team * L)) & kTeam) << g;
     }
+    // lanes past the last expert may name a group past the 64th; whatever bit they read, their c stays -inf
+    const auto shut_at = [&](int e) { return ((open >> (((uint32_t)e * a.group_magic >> 21) & 63u)) & 1ull) == 0; };
     if (spread > 0) {
 #pragma unroll
       for (int i = 0; i < V / P; ++i) {
-        const int e = expert_at<T, L, V>(j, i * P);
-        const bool shut = ((open >> ((uint32_t)e * a.group_magic >> 21)) & 1ull) == 0;
+        const bool shut = shut_at(expert_at<T, L, V>(j, i * P));
 #pragma unroll
         for (int v = 0; v < P; ++v)
           if (shut) c[i * P + v] = -INFINITY;
@@ -308,8 +309,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_forward_kernel(const RouteA
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int e = expert_at<T, L, V>(j, v);
-        if (((open >> ((uint32_t)e * a.group_magic >> 21)) & 1ull) == 0) c[v] = -INFINITY;
+        if (shut_at(expert_at<T, L, V>(j, v))) c[v] = -INFINITY;
       }
     }
   }

@@ -112,3 +112,13 @@ def test_a_mask_of_the_lowest_number_is_one_of_minus_infinity(L, score, experts,
         assert torch.equal(out[0][1], out[1][1]) and torch.equal(out[0][0], out[1][0])
         want = [experts - size + i for i in left] if len(left) > 1 else [-1, -1]
         assert sorted(out[0][1][0].tolist()) == want
+
+
+@pytest.mark.parametrize("experts", [64, 65, 130, 200, 260])
+def test_places_past_the_last_group(L, experts):
+    """Groups of one expert, as many as there can be: a wave's last places name groups that do not exist."""
+    groups = max(g for g in range(1, 65) if experts % g == 0)
+    x, bias = r.grid_logits(9, experts, experts), r.grid_bias(experts, 2)
+    kw = dict(score="sigmoid", groups=groups, top_groups=max(1, groups - 1))
+    keep = r.settled(x, bias, kw)
+    r.check(L, x[keep], min(8, experts // groups * kw["top_groups"]), bias, **kw)
