@@ -553,8 +553,9 @@ __global__ __launch_bounds__(64 * whole_waves(DP)) void attend_whole_kernel(cons
     float o[4][16][kPad];
   };
   __shared__ Shared sh;
-  extern __shared__ float logits[];  // [rows][logit_stride]
+  extern __shared__ float logits[];  // [rows][logit_stride], where there are accounts
   lds_poison(sh);
+  if (a.account_out != nullptr) lds_poison(logits, a.rows * logit_stride * (int)sizeof(float));
   const int64_t bh = grid_row();
   if (bh >= (int64_t)a.batch * a.heads) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);

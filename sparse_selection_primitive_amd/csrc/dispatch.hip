@@ -50,6 +50,7 @@ LDEV int rank_in_wave(uint16_t *count, int experts, int e, bool live, int bits) 
 __global__ __launch_bounds__(kPlanTile) void plan_count_kernel(const int32_t *chosen, int64_t pairs, int experts,
                                                                int bits, int tiles, uint32_t *counts) {
   extern __shared__ uint16_t count[];  // [kPlanWaves][experts]
+  lds_poison(count, kPlanWaves * experts * (int)sizeof(uint16_t));
   for (int i = threadIdx.x; i < kPlanWaves * experts; i += kPlanTile) count[i] = 0;
   __syncthreads();
   const int64_t i = (int64_t)blockIdx.x * kPlanTile + threadIdx.x;
@@ -125,6 +126,8 @@ __global__ __launch_bounds__(kPlanTile) void plan_place_kernel(const int32_t *ch
                                                                int32_t *slot, int32_t *order) {
   extern __shared__ uint16_t count[];  // [kPlanWaves][experts], then the experts' starts [experts]
   __shared__ uint32_t wave_sums[kPlanWaves];
+  lds_poison(wave_sums);
+  lds_poison(count, experts * (kPlanWaves * (int)sizeof(uint16_t) + (int)sizeof(uint32_t)));
   uint32_t *start = reinterpret_cast<uint32_t *>(count + kPlanWaves * experts);
   for (int i = threadIdx.x; i < kPlanWaves * experts; i += kPlanTile) count[i] = 0;
   __syncthreads();

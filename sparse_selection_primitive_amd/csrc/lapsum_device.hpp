@@ -68,6 +68,18 @@ LDEV void lds_poison(T &obj) {
 #endif
 }
 
+// The same for LDS whose size the launch gives.
+LDEV void lds_poison(void *words, int bytes) {
+#ifdef LAPSUM_LDS_POISON
+  uint32_t *q = static_cast<uint32_t *>(words);
+  for (int i = (int)threadIdx.x; i < bytes / 4; i += (int)blockDim.x) q[i] = 0xFFFFFFFFu;
+  __syncthreads();
+#else
+  (void)words;
+  (void)bytes;
+#endif
+}
+
 // ------------------------------------------------------------------ keys
 // Order-preserving map of fp32 onto uint32: the unsigned order of keys is
 // the numeric order of finite values (-0.0 sorts just below +0.0).
