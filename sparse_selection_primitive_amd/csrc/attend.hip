@@ -634,8 +634,11 @@ __global__ __launch_bounds__(64 * whole_waves(DP)) void attend_whole_kernel(cons
   if (a.account_out == nullptr) return;
   for (int e = threadIdx.x; e < length; e += blockDim.x) {
     float w = 0.0f;
-    for (int i = ONE ? 0 : first_row(a, length, e); i < a.rows; ++i)
-      w += __builtin_amdgcn_exp2f(logits[i * logit_stride + e] - sh.lse[i]);
+    const int from = ONE ? 0 : first_row(a, length, e);
+    for (int i = 0; i < a.rows; ++i) {
+      const float off = sh.lse[i];
+      w += __builtin_amdgcn_exp2f(logits[i * logit_stride + e] - (i < from ? 0.0f : off));
+    }
     a.account_out[bh * a.capacity + e] = a.account[bh * a.capacity + e] + w;
   }
 }
@@ -658,7 +661,7 @@ LDEV float row_lse(const AttendArgs &a, int64_t bh, int row) {
 }
 
 // out of one row: its parts, each weighed by its maximum, summed over the splits
-template <class T, int TH>
+template <class T, int TH, bool ONE>
 LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   struct Shared {
     float weight[TH];
@@ -672,8 +675,7 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml) + bh * a.splits * a.rows + row;
   float2 x = {-INFINITY, 0.0f};
   if (tid < a.splits) x = ml[(int64_t)tid * a.rows];
-  const bool again =
-      a.dropped != nullptr && __syncthreads_or(tid < a.splits && a.dropped[bh * a.splits + tid] != 0) != 0;
+  const bool again = !ONE && __syncthreads_or(tid < a.splits && a.dropped[bh * a.splits + tid] != 0) != 0;
   float top = team_max<64>(x.x);
   if (tid % 64 == 0) sh.top[wave] = top;
   __syncthreads();
@@ -711,17 +713,8 @@ LDEV void join_row(const AttendArgs &a, int64_t bh, int row, float *lse) {
   store_out<T>(a, bh, row, d, o);
 }
 
-// The first a.rows workgroups of a cache join its rows; the others add up the
-// accounts of 4 entries a thread from the kept logits:
-// account_out = account + sum over rows of 2^(z - lse).
-template <class T, int TH>
-__global__ __launch_bounds__(TH) void attend_join_kernel(const AttendArgs a, float *lse) {
-  const int64_t bh = grid_row();
-  if (bh >= (int64_t)a.batch * a.heads) return;
-  if ((int)blockIdx.x < a.rows) {
-    join_row<T, TH>(a, bh, (int)blockIdx.x, lse);
-    return;
-  }
+template <int TH, bool ONE>
+LDEV void add_kept(const AttendArgs &a, int64_t bh) {
   const int length = length_of(a, bh);
   const int base = ((int)blockIdx.x - a.rows) * (4 * TH);
   if (base >= length) return;
@@ -740,7 +733,9 @@ __global__ __launch_bounds__(TH) void attend_join_kernel(const AttendArgs a, flo
   if (e >= length) return;
   f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
   const float *z = a.logits + (bh * a.blocks + e / kBlock) * a.rows * kBlock + e % kBlock;
-  if (e + 3 <= length - a.news) {  // every row sees all four
+  // Whether some row does not see some entry is asked for the wave as a whole, so it goes through the rows once
+  // (2 sequences of 16384 entries, 4 new tokens: 35.4 us; by lane, so twice in one wave, 42.0).
+  if (ONE || !__any(e + 3 > length - a.news)) {
 #pragma unroll 4
     for (int i = 0; i < a.rows; ++i) {
       const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
@@ -748,16 +743,36 @@ __global__ __launch_bounds__(TH) void attend_join_kernel(const AttendArgs a, flo
       for (int n = 0; n < 4; ++n) w[n] += __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
     }
   } else {
-    for (int i = first_row(a, length, e); i < a.rows; ++i) {
-      const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
+    int from[4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        w[n] += i < first_row(a, length, e + n) ? 0.0f : __builtin_amdgcn_exp2f(y[n] - sh.lse[i]);
+    for (int n = 0; n < 4; ++n) from[n] = first_row(a, length, e + n);
+#pragma unroll 4
+    for (int i = 0; i < a.rows; ++i) {
+      const f32x4 y = *reinterpret_cast<const f32x4 *>(z + i * kBlock);
+      const float off = sh.lse[i];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) w[n] += __builtin_amdgcn_exp2f(y[n] - (i < from[n] ? 0.0f : off));  // y is -inf before
     }
   }
 #pragma unroll
   for (int n = 0; n < 4; ++n)
     if (e + n < length) a.account_out[bh * a.capacity + e + n] = a.account[bh * a.capacity + e + n] + w[n];
+}
+
+// The first a.rows workgroups of a cache join its rows; the others (KEEP) add up the
+// accounts of 4 entries a thread from the kept logits:
+// account_out = account + sum over rows of 2^(z - lse).  ONE (nothing was left out, and every row
+// sees every entry) and KEEP as in the attend_kernel before it, so that no case carries the
+// other's code: with it the join of 64 rows took 8.8 us for 6.7.
+template <class T, int TH, bool ONE, bool KEEP>
+__global__ __launch_bounds__(TH) void attend_join_kernel(const AttendArgs a, float *lse) {
+  const int64_t bh = grid_row();
+  if (bh >= (int64_t)a.batch * a.heads) return;
+  if ((int)blockIdx.x < a.rows) {
+    join_row<T, TH, ONE>(a, bh, (int)blockIdx.x, lse);
+    return;
+  }
+  if constexpr (KEEP) add_kept<TH, ONE>(a, bh);
 }
 
 // the same, z formed again: a wave takes 64 entries and goes through all rows
@@ -848,10 +863,10 @@ __global__ __launch_bounds__(256) void account_formed_kernel(const AttendArgs a,
   if (mine < length) a.account_out[bh * a.capacity + mine] = before + sum;
 }
 
-template <class T, int TH>
+template <class T, int TH, bool ONE, bool KEEP>
 hipError_t join(const AttendArgs &a, float *lse, hipStream_t s) {
-  const int64_t sums = a.logits != nullptr ? (a.capacity + 4 * TH - 1) / (4 * TH) : 0;
-  attend_join_kernel<T, TH>
+  const int64_t sums = KEEP ? (a.capacity + 4 * TH - 1) / (4 * TH) : 0;
+  attend_join_kernel<T, TH, ONE, KEEP>
       <<<rows_grid((unsigned)(a.rows + sums), (int64_t)a.batch * a.heads), dim3(TH), 0, s>>>(a, lse);
   return hipGetLastError();
 }
@@ -864,14 +879,12 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
       <<<rows_grid((unsigned)(a.splits * row_blocks), caches), dim3(64 * kAttendWaves), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const bool kept = a.logits != nullptr, formed = a.account_out != nullptr && !kept;
+  const bool formed = a.account_out != nullptr && !KEEP;
   // the rows' lse, where the logits are formed again, follow the parts' maxima and sums
   float *lse = formed ? a.part_ml + caches * a.splits * a.rows * 2 : nullptr;
-  AttendArgs j = a;
-  if (ONE) j.dropped = nullptr;  // nothing was left out, and no flags were written
   // 512 threads where there are many parts (one sequence of 8192 entries, 91 splits: 13.7 us, 14.7 with
   // 256), 256 where there are few (128 rows, 16 splits: 52.6 us, 56.0 with 512)
-  e = a.splits > 16 ? join<T, 512>(j, lse, s) : join<T, 256>(j, lse, s);
+  e = a.splits > 16 ? join<T, 512, ONE, KEEP>(a, lse, s) : join<T, 256, ONE, KEEP>(a, lse, s);
   if (e != hipSuccess || !formed) return e;
   account_formed_kernel<T, DP, EXACT>
       <<<rows_grid((unsigned)((a.capacity + 255) / 256), caches), dim3(256), 0, s>>>(a, lse);

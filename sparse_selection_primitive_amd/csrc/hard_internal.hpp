@@ -70,7 +70,7 @@ struct AttendArgs {
   float *part_ml;                  // [batch * heads][splits][rows][2]
   float *logits;                   // [batch * heads][blocks][rows][32], or NULL: formed again
   int64_t blocks;                  // of 32 entries
-  int *dropped;                    // [batch * heads][splits]: infinities or NaN left out; the join: NULL if none can be
+  int *dropped;                    // [batch * heads][splits]: infinities or NaN left out, where that can be
 };
 struct AttendPlan {
   int splits;
