@@ -26,7 +26,7 @@
 // access pattern without arithmetic shows the same), 165 us and 16 us for the
 // join.  Many rows: the matrix instructions (16 cycles for 16 rows, 32 entries and 32 elements) and
 // the vector instructions beside them, which share the issue of the one wave that
-// fits a SIMD: 128 rows over 16384 entries of 16 key heads take 47 us (25.8 Gflop with the two parts
+// fits a SIMD: 128 rows over 16384 entries of 16 key heads take 47 us (34.4 Gflop with the three parts
 // of the weights, 550 Tflop/s) and 27 us for the accounts.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
@@ -45,6 +45,13 @@ constexpr int kStep = kBlock * kAttendWaves;
 // grow by kSlack more before it moves.  2^15 is an fp16 number, and its smallest weight that is not
 // 0 is then 2^-31 of the largest: many entries of little weight beside one of much keep theirs.
 constexpr float kLift = 7.0f, kSlack = 8.0f;
+// A weight goes into the matrix product as the sum of this many numbers of the cache's type, each the rounding
+// of what the ones before leave: three of bf16's 8 bits, or two of fp16's 11, are all 24 bits of an fp32 number.
+// With two parts of bf16, 16 bits, outputs that cancel were off by 2^-17.6 of sum p |v| where 24 give 2^-21;
+// the third part costs nothing up to 32 rows, where memory is the bound, and of the time of
+// 64 rows over two sequences of 16384 entries 9% (43.9 us for 40.1), of 128 rows 4% (54.8 for 52.7).
+template <class T>
+constexpr int kParts = sizeof(T) == 2 && (float)(T)65536.0f == 65536.0f ? 3 : 2;
 constexpr int kMaxSplits = 256;
 // A cache goes to one workgroup whole where that is one block a wave, or where
 // there are enough caches for every compute unit (times of one call from a graph, 32 query
@@ -331,8 +338,7 @@ LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, 
     key.load(next_keys, 16, k[1]);
     // some row does not see some entry of the block
     const bool edge = e0 + kBlock > end || e0 + kBlock - 1 > length - a.news;
-    // the weights go into the product in two parts, so they keep 16 bits or more of their mantissa there
-    pack_t<T> hi[NT], lo[NT];
+    pack_t<T> part[NT][kParts<T>];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -372,8 +378,11 @@ LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, 
       }
       // the block's weights among themselves first: many small ones would each round away in a large sum
       l[t] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-      hi[t] = __builtin_convertvector(p, pack_t<T>);
-      lo[t] = __builtin_convertvector(p - __builtin_convertvector(hi[t], f32x8), pack_t<T>);
+#pragma unroll
+      for (int i = 0; i < kParts<T>; ++i) {
+        part[t][i] = __builtin_convertvector(p, pack_t<T>);
+        p -= __builtin_convertvector(part[t][i], f32x8);
+      }
     }
     // NaN or infinity among values that some row does not see must not meet
     // that row's zero weights: they are left out here and added by the join
@@ -383,8 +392,8 @@ LDEV bool attend_entries(const AttendArgs &a, int64_t bh, int row0, int length, 
       const pack_t<T> col = v.column(n);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        o[t][n] = mfma(col, hi[t], o[t][n]);
-        o[t][n] = mfma(col, lo[t], o[t][n]);
+#pragma unroll
+        for (int i = 0; i < kParts<T>; ++i) o[t][n] = mfma(col, part[t][i], o[t][n]);
       }
     }
     v.load(entries(values, a.ve, e0 + stride, end, a.width), value_off, (int)a.ve * 2);
