@@ -101,6 +101,10 @@ int32_t int32_of(PyObject *o) {
   if (over != 0 || x < INT32_MIN || x > INT32_MAX) PyErr_SetNone(PyExc_OverflowError);
   return (int32_t)x;
 }
+// A tensor of the caller has been changed in place, for autograd.
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 PyObject *wrap(at::Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject *pair(at::Tensor a, at::Tensor b) { return Py_BuildValue("(NN)", wrap(std::move(a)), wrap(std::move(b))); }
 
@@ -320,6 +324,7 @@ PyObject *cache_attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
                    accounts ? static_cast<float *>(to->data_ptr()) : nullptr, out.data_ptr(), ws.at, ws.bytes,
                    stream_of(*q));
   if (st != LAPSUM_OK) return refused(st, "lapsum_cache_attend");
+  if (accounts) written(*to);
   return wrap(std::move(out));
   END
 }
@@ -350,6 +355,7 @@ PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
                   static_cast<int32_t *>(kept.data_ptr()), static_cast<int32_t *>(after.data_ptr()), ws.at, ws.bytes,
                   stream_of(*k));
   if (st != LAPSUM_OK) return refused(st, "lapsum_cache_evict");
+  for (const at::Tensor *t : {k, v, account_out, positions_out}) written(*t);
   return pair(std::move(kept), std::move(after));
   END
 }

@@ -153,6 +153,13 @@ def _out(x, name, dtype, shape, dev):
     return x
 
 
+def _written(*tensors):
+    """Tensors of the caller that a call has written: autograd learns of it, as of any change in place."""
+    for x in tensors:
+        if x is not None and not x.is_inference():
+            torch.autograd.graph.increment_version(x)
+
+
 def _rows(x, name):
     """[tokens, n] with contiguous rows (any distance between them): (x, tokens, n, stride)."""
     tokens, n = x.shape
@@ -210,6 +217,8 @@ def route_forward(logits, k, bias=None, *, score="softmax", groups=1, top_groups
         return weights, chosen
     _call(dev, "lapsum_route_forward", x.data_ptr(), code, tokens, experts, stride,
           None if bias is None else bias.data_ptr(), opt, weights.data_ptr(), chosen.data_ptr())
+    if out is not None:
+        _written(*out)
     return weights, chosen
 
 
@@ -231,6 +240,7 @@ def route_backward(dweights, logits, chosen, *, score="softmax", renormalise=Tru
         return dlogits
     _call(dev, "lapsum_route_backward", dweights.data_ptr(), x.data_ptr(), code, tokens, experts, stride,
           chosen.data_ptr(), opt, dlogits.data_ptr())
+    _written(out)
     return dlogits
 
 
@@ -308,6 +318,7 @@ def dispatch_forward(x, slot, offsets, *, out=None):
         return xs
     _call(dev, "lapsum_dispatch_forward", x.data_ptr(), code, tokens, k, width, stride, slot.data_ptr(),
           offsets.data_ptr(), offsets.numel() - 1, xs.data_ptr())
+    _written(out)
     return xs
 
 
@@ -326,6 +337,7 @@ def dispatch_backward(dxs, slot, *, out=None):
     if dxs.numel() == 0:
         return dx.zero_()
     _call(dev, "lapsum_dispatch_backward", dxs.data_ptr(), code, tokens, k, width, slot.data_ptr(), dx.data_ptr())
+    _written(out)
     return dx
 
 
@@ -346,6 +358,7 @@ def combine_forward(ys, slot, weights, *, out=None):
         return y.zero_()
     _call(dev, "lapsum_combine_forward", ys.data_ptr(), code, tokens, k, width, slot.data_ptr(), weights.data_ptr(),
           y.data_ptr())
+    _written(out)
     return y
 
 
@@ -369,6 +382,8 @@ def combine_backward(dy, ys, slot, weights, offsets, *, out=None):
     _call(dev, "lapsum_combine_backward", dy.data_ptr(), stride, ys.data_ptr(), code, tokens, k, width,
           slot.data_ptr(), weights.data_ptr(), offsets.data_ptr(), offsets.numel() - 1, dys.data_ptr(),
           dweights.data_ptr())
+    if out is not None:
+        _written(*out)
     return dys, dweights
 
 
@@ -482,7 +497,7 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
         raise LapsumError("q must be [batch, news, q_heads, width] of the cache's type")
     q = q.contiguous()
     lengths = _array(lengths, "lengths", torch.int32, (batch,), dev)
-    out = _out(out, "out", q.dtype, q.shape, dev)
+    given, out = out, _out(out, "out", q.dtype, q.shape, dev)
     if account is not None:
         if account_out is None:
             account_out = account  # written in place: not a copy of it
@@ -501,6 +516,7 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     _call(dev, "lapsum_cache_attend", q.data_ptr(), cache, lengths.data_ptr(), news, q_heads,
           width ** -0.5 if scale is None else float(scale), None if account is None else account.data_ptr(),
           None if account is None else account_out.data_ptr(), out.data_ptr(), wptr, wlen)
+    _written(account_out, given)
     del ws
     return out
 
@@ -549,5 +565,6 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
           None if next_position is None else next_position.data_ptr(), _int32(sinks, "sinks"),
           _int32(recent, "recent"),
           account_out.data_ptr(), positions_out.data_ptr(), kept.data_ptr(), lengths_out.data_ptr(), wptr, wlen)
+    _written(k, v, account_out, positions_out)
     del ws
     return kept, lengths_out
