@@ -21,13 +21,13 @@
 // (16 lanes read whole rows) and transposes them in registers.
 //
 // What bounds it.  A few rows: memory.  Without accounts 200001 entries of 8
-// key heads (819 MB) take 132 us, 6.2 TB/s, what a kernel that only reads reaches; the
+// key heads (819 MB) take 137 us with the join, 6.0 TB/s, where a kernel that only reads reaches 6.2; the
 // kept logits add 52 MB of writes, which among the reads cost as much as 200 MB of them (a copy of the
 // access pattern without arithmetic shows the same), 165 us and 16 us for the
-// join.  Many rows: the matrix instructions (16 cycles for 16 rows, 32 entries and 32 elements) and
-// the vector instructions beside them, which share the issue of the one wave that
-// fits a SIMD: 128 rows over 16384 entries of 16 key heads take 47 us (34.4 Gflop with the three parts
-// of the weights, 550 Tflop/s) and 27 us for the accounts.
+// join.  Many rows: one wave a SIMD, whose vector instructions (46% of its time), matrix
+// instructions (33%; 16 cycles for 16 rows, 32 entries and 32 elements) and waits for memory (22%) follow one
+// another: 128 rows over 16384 entries of 16 key heads take 50 us (34.4 Gflop with the three parts
+// of the weights, 680 Tflop/s) and 27 us for the accounts.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -49,20 +49,21 @@ constexpr float kLift = 7.0f, kSlack = 8.0f;
 // of what the ones before leave: three of bf16's 8 bits, or two of fp16's 11, are all 24 bits of an fp32 number.
 // With two parts of bf16, 16 bits, outputs that cancel were off by 2^-17.6 of sum p |v| where 24 give 2^-21;
 // the third part costs nothing up to 32 rows, where memory is the bound, and of the time of
-// 64 rows over two sequences of 16384 entries 9% (43.9 us for 40.1), of 128 rows 4% (54.8 for 52.7).
+// 64 rows over two sequences of 16384 entries 9% (43.0 us for 39.6), of 128 rows 1 to 4% (52.6 for 52.2, 54.8 for 52.7).
 template <class T>
 constexpr int kParts = sizeof(T) == 2 && (float)(T)65536.0f == 65536.0f ? 3 : 2;
 constexpr int kMaxSplits = 256;
 // A cache goes to one workgroup whole where that is one block a wave, or where
 // there are enough caches for every compute unit (times of one call from a graph, 32 query
-// heads on 8 of width 128: 200 entries 7.3 us, by splits 8.8; 1000 entries 14.1 and 9.0; 32
-// sequences of up to 1000 21 and 28; 64 of up to 4000 148 and 167).
+// heads on 8 of width 128: 200 entries 7.7 us, by splits 9.0; 1000 entries 14.5 and 9.2; 32
+// sequences of 500 to 1000 20.7 and 28.5; 64 of 2000 to 4000 137 and 169).  By the capacity, which the host
+// knows, not the lengths: 1000 entries in a cache for 131072 take 10.6 us.
 constexpr int kWholeShort = 256, kWholeMax = 4096;
 constexpr int kWholeCaches = 256;
 constexpr int kWholeLogits = 16384;  // fp32 logits that it keeps in LDS, at most
 // Up to this many rows the logits are kept for the accounts; beyond they are formed again from the
-// keys (4 rows of 64 sequences of 8192 entries: kept 421 us, formed again 505;
-// 16 rows of 20000 entries: 27.7 and 35.9; more rows keep more than the keys' bytes).
+// keys (4 rows of 64 sequences of 8192 entries: kept 426 us, formed again 507;
+// 16 rows of 20000 entries: 27.3 and 35.9; more rows keep more than the keys' bytes).
 constexpr int kKeepRows = 16;
 
 LDEV f32x4 mfma(pack_t<bf16> a, pack_t<bf16> b, f32x4 c) {
@@ -138,8 +139,8 @@ LDEV window_t window_of(const void *first, int64_t bytes) {
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
 
-// Values are read as streamed (not kept in the cache): 200001 entries in 154
-// us instead of 174.  Keys are not: a load touches 16 rows' half lines, and without the
+// Values are read as streamed (not kept in the cache): 200001 entries in 137
+// us instead of 146.  Keys are not: a load touches 16 rows' half lines, and without the
 // cache the other halves are fetched again.
 constexpr int kCached = 0, kStreamed = 2;
 template <int AUX>
@@ -891,8 +892,8 @@ hipError_t attend(const AttendArgs &a, hipStream_t s) {
   const bool formed = a.account_out != nullptr && !KEEP;
   // the rows' lse, where the logits are formed again, follow the parts' maxima and sums
   float *lse = formed ? a.part_ml + caches * a.splits * a.rows * 2 : nullptr;
-  // 512 threads where there are many parts (one sequence of 8192 entries, 91 splits: 13.7 us, 14.7 with
-  // 256), 256 where there are few (128 rows, 16 splits: 52.6 us, 56.0 with 512)
+  // 512 threads where there are many parts (one sequence of 8192 entries, 64 splits: 14.0 us, 15.5 with
+  // 256), 256 where there are few (128 rows, 16 splits: 52.6 us, 61.5 with 512)
   e = a.splits > 16 ? join<T, 512, ONE, KEEP>(a, lse, s) : join<T, 256, ONE, KEEP>(a, lse, s);
   if (e != hipSuccess || !formed) return e;
   account_formed_kernel<T, DP, EXACT>
@@ -908,7 +909,7 @@ int whole_stride(int64_t capacity) { return (int)((capacity + kBlock - 1) / kBlo
 // several do, their values checked and joined in the same way); beyond, each wave takes 32
 // rows of its own and all entries, which leaves waves idle at up to 96 rows but is better than
 // 16 rows each, since every wave reads the keys and values (64 rows over two
-// sequences of 16384 entries: 40.9 us, with 16 rows each 48.3).  32 rows of 256
+// sequences of 16384 entries: 43.0 us, with 16 rows each 50.0).  32 rows of 256
 // elements would not fit a wave's registers.
 template <class T, int DP, bool EXACT>
 hipError_t attend_rows(const AttendArgs &a, hipStream_t s) {
@@ -959,14 +960,15 @@ AttendPlan attend_plan(int64_t batch, int64_t heads, int64_t capacity, int64_t r
   const int64_t rows_per = rows <= 16 ? 16 : (width <= 128 ? (rows <= 32 ? 32 : 128) : 64);
   const int64_t groups = caches * ((rows + rows_per - 1) / rows_per);
   // Workgroups over all.  768 fit the chip at once (three a compute unit), and one
-  // round of them is best where their shares are equal: one sequence of 200001 entries takes 132 us,
-  // in three rounds 145.  Sequences of several lengths need a finer grain: 64 of 512 to 8192
-  // entries take 188 us in three rounds, 196 in one.  With more rows, or wider ones, a
-  // split's part of the outputs weighs more: 32 new tokens over 16384 entries take 56 us with
-  // one workgroup a compute unit, 73 with two and 87 with half of them idle.
+  // round of them is best where their shares are equal: one sequence of 200001 entries takes 137 us,
+  // in three rounds 146.  Sequences of several lengths need a finer grain: 64 of 512 to 8192
+  // entries, at random, take 1 to 8% less in three rounds, 8 of 100 to 32768 up to 17%; evenly spread lengths 2% more,
+  // 3 of 50000 to 100000 4%.  With more rows, or wider ones, a
+  // split's part of the outputs weighs more: 32 new tokens over 16384 entries take 53 us with
+  // one workgroup a compute unit, 65 with two and 85 with half of them idle.
   // At up to 64 rows half of a workgroup's waves are idle, so two share a compute unit where the
-  // entries are many: 64 rows over 100000 entries take 98 us with 512 workgroups, 116 with 256, over
-  // 8192 entries 23.3 and 21.2.
+  // entries are many: 64 rows over 100000 entries take 109 us with 512 workgroups, 133 with 256, over
+  // 8192 entries 24.8 and 21.9.
   const bool halves = rows > 32 && rows <= 64 && width <= 128 && caches * capacity >= 1 << 17;
   const int64_t wanted = halves ? 512 : (rows > 16 || width > 128 ? 256 : (batch > 1 && one ? 2304 : 768));
   int64_t splits = (wanted + groups - 1) / groups;

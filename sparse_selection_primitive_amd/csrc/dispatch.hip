@@ -12,9 +12,10 @@
 // is touched in whole rows.
 //
 // What bounds them: memory.  8192 tokens of 2048 bf16 elements, 8 choices (268 MB
-// on the experts' side): dispatch 51 us (302 MB, 5.9 TB/s), combine and the sums of the dispatch's
-// gradient 53 us each (5.7 TB/s), combine's gradient 108 us (570 MB, 5.3 TB/s); the plan of the 65536 pairs is
-// three launches of 5 us, of up to 1024 pairs one of 3 us.
+// on the experts' side): dispatch 54 us (302 MB, 5.6 TB/s), combine and the sums of the dispatch's
+// gradient 54 us each (5.6 TB/s), combine's gradient 109 us (570 MB, 5.2 TB/s).  The plan of the 65536 pairs is
+// three launches of 5 us (10.5 from a graph), of up to 1024 pairs one of 3 us: launches and chains of
+// latencies, its bytes are few.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -382,9 +383,9 @@ hipError_t rows_of(const RowsArgs &a, Kind kind, hipStream_t s) {
   const bool packs = a.width % Pack<T>::N == 0 && a.stride % Pack<T>::N == 0 && aligned(a.src) && aligned(a.dst) &&
                      aligned(a.dy);
   // A wave per token for up to 64 units, a workgroup beyond: 8192 rows of 512 bf16 elements, 8 choices,
-  // take 14.1, 13.4 and 29.1 us (dispatch, sums, combine's gradient) with a wave each, 14.3, 15.9 and
-  // 48.6 with a workgroup; of 2048 elements 75, 71 and 122 with a wave, 52, 54 and 105 with a
-  // workgroup.  Packs where widths and addresses allow them (2048 elements one by one: 109, 80 and 133).
+  // take 14.5, 14.3 and 30.7 us (dispatch, sums, combine's gradient) with a wave each, 15.0, 16.4 and
+  // 49.2 with a workgroup; of 2048 elements 78, 72 and 128 with a wave, 55, 55 and 109 with a
+  // workgroup.  Packs where widths and addresses allow them (2048 elements one by one: 106, 78 and 137).
   const int64_t units = packs ? a.width / Pack<T>::N : a.width;
   if (packs) return units <= 64 ? rows<T, true, 64>(a, kind, s) : rows<T, true, 256>(a, kind, s);
   return units <= 64 ? rows<T, false, 64>(a, kind, s) : rows<T, false, 256>(a, kind, s);

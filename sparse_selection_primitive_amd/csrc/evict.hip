@@ -17,10 +17,11 @@
 // registers, so the accounts are read once.  Longer rows: tiles of 4096
 // entries on as many workgroups, one launch a digit; the last leaves the tiles' counts.
 //
-// What bounds it.  One entry over the budget: one pass over the accounts and
-// positions, 7.6 us for 256 rows of 4097 (8.4 MB; a launch and a chain of memory
-// latencies).  130001 entries of 8 rows to a quarter: the moves, 39 us for 201 MB
-// (5.2 TB/s), and five launches of 5 to 13 us before them that find the key and the places.
+// What bounds it.  One entry over the budget: a chain of latencies, 7.5 us for 256 rows of 4097
+// (the accounts and positions, 8.4 MB, read; a minimum over the row; then, read again from the cache, written with
+// the slots, 12.6 MB).  130001 entries of 8 rows to a quarter: the moves, 39 us for 201 MB
+// (5.2 TB/s), and five launches of 5 to 12 us before them that find the key and the places, the longest of
+// them for its barriers, two in each of four rounds.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -30,11 +31,12 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWaves = kSelectThreads / 64;
 // Entries of a row that one workgroup holds: 16 a thread, what its registers allow.
-// 8 rows of 8192 to a half take 23 us, by tiles 33; 256 rows of 16384 273 and 326, and 12 and 29 where one entry
-// leaves; only few rows of 16384 that lose many are better by tiles (8 to a half: 41 and 36).
+// 8 rows of 8192 to a half take 23 us, by tiles 33; 256 rows of 16384 275 and 327, and 26 and 99 where one entry
+// leaves; only few rows of 16384 that lose many are better by tiles (8 to a half: 41 and 36).  By the
+// capacity, which the host knows, not the lengths: of 20000 slots one entry leaves 8 rows in 29 us, of 16384 in 12.
 constexpr int kRowMax = 16384;
 // Up to this many entries the selecting workgroup moves itself, beyond a second launch
-// does (256 rows, 64 of 4160 entries leave: 15.8 us, with the second launch 21.0).
+// does (256 rows, 64 of 4160 entries leave: 15.7 us, with the second launch 21.1).
 constexpr int kFewMoves = 64;
 constexpr int kMoveSlots = 256;
 
@@ -728,6 +730,9 @@ size_t evict_workspace(int64_t batch, int64_t heads, int64_t capacity, int64_t k
 
 hipError_t launch_evict(const EvictArgs &a, hipStream_t s) {
   if (a.capacity > kRowMax) return evict_long(a, s);
+  // Entries a thread by the row's slots.  5, so that a budget of 4096 and the entry over it do not take 8 (256 rows
+  // of 4097 slots: 7.2 us, with 8 a thread 7.9; of 3000 6.5 and 7.2; 8 rows of 4097 to 2048 17.0 and 18.5).
+  // 3, 9 and 12 as well would save 0.1 us of 2049 slots, 1.0 of 8193 and 0.8 of 12000, and are not built.
   if (a.capacity <= 2 * kSelectThreads) return evict_rows<2>(a, s);
   if (a.capacity <= 5 * kSelectThreads) return evict_rows<5>(a, s);
   if (a.capacity <= 8 * kSelectThreads) return evict_rows<8>(a, s);

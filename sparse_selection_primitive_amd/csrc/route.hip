@@ -18,9 +18,9 @@
 //
 // What bounds it: vector instructions, about 225 a row of 256 experts (scores 60, the fp64
 // numbers 25, ordering 55, eight rounds 50).  16384 rows of 256 fp32 logits
-// take 9.2 us (17.8 MB, 1.9 TB/s), 32768 bf16 rows with bias and groups 17.9 us, the
-// gradient of those 10.0 us (34 MB with the gathered logits' 64-byte
-// sectors, 3.4 TB/s); 16 rows 4.8 us, the length of one row's chain.
+// take 9.3 us (17.8 MB, 1.9 TB/s), 32768 bf16 rows with bias and groups 18.0 us, the
+// gradient of those 10.2 us (34 MB with the gathered logits' 64-byte
+// sectors, 3.3 TB/s); 16 rows 4.9 us, the length of one row's chain.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -515,10 +515,10 @@ hipError_t forward(const RouteArgs &a, hipStream_t s) {
   const bool packs = a.experts % N == 0 && a.stride % N == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
   int spread = a.group_size % P == 0 ? a.group_size / P : 0;
   if (spread > L || (spread & (spread - 1)) != 0) spread = 0;
-  // 16384 bf16 rows of 256 in 8 groups: 10.0 us by butterflies, 11.8 through LDS
+  // 16384 bf16 rows of 256 in 8 groups: 10.2 us by butterflies, 12.6 through LDS
   constexpr int rows = kWaves * (64 / L);
   const dim3 grid((unsigned)((a.tokens + rows - 1) / rows)), threads(64 * kWaves);
-  // a lane orders its 8 or 32 largest: for 8 choices of 256 experts 9.0 us, with the longer order 14.4
+  // a lane orders its 8 or 32 largest: for 8 choices of 256 experts 9.1 us, with the longer order 14.7
   if (a.k <= 8) route_forward_kernel<T, L, V, 8><<<grid, threads, 0, s>>>(a, packs, spread);
   else route_forward_kernel<T, L, V, 32><<<grid, threads, 0, s>>>(a, packs, spread);
   return hipGetLastError();
@@ -537,8 +537,8 @@ hipError_t backward(const RouteArgs &a, hipStream_t s) {
 
 // Lanes and scores per lane by the number of experts: 16 scores a lane keep
 // a wave's share of the butterflies small (several rows share each step).
-// 16384 rows of 256 take 9.0 us on 16 lanes, 14.8 on 32; of 128 5.6 on 8, 8.1 on 16; of 64
-// 4.1 with 8 scores a lane, 5.1 with 16.
+// 16384 rows of 256 take 9.1 us on 16 lanes, 15.1 on 32; of 128 5.6 on 8, 8.6 on 16; of 64
+// 4.1 with 8 scores a lane, 5.2 with 16.
 template <class T>
 hipError_t forward_of(const RouteArgs &a, hipStream_t s) {
   if (a.experts <= 64) return forward<T, 8, 8>(a, s);

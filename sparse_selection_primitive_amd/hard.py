@@ -484,7 +484,7 @@ def cache_attend(q, k, v, lengths, account=None, *, scale=None, account_out=None
     [batch, heads, capacity, width] whose first lengths[b] entries are filled, the new tokens' own last (token i sees
     the entries up to lengths[b] - news + i).  account fp32 [batch, heads, capacity]: each entry's weight, summed over
     the new tokens and the query heads of its key head, is added to it, in place or into account_out.
-    scale: 1/sqrt(width) by default."""
+    scale: 1/sqrt(width) by default.  No gradient: the results do not require one, whatever the arguments do."""
     if _native is not None and out is None:
         done = _native.cache_attend(q, k, v, lengths, account, scale, account_out)
         if done is not None:
