@@ -447,7 +447,8 @@ lapsum_status lapsum_cache_attend(const void *q, const lapsum_cache *cache, cons
  * not 0, at least next_position[b] - recent.
  * Survivors at slot `keep` and behind move into the holes before it, the
  * n-th survivor into the n-th hole; the others stay where they are.  k and v
- * are changed in place.
+ * are changed in place, so no two of their entries may share memory
+ * (LAPSUM_ERR_LAYOUT): sorted, each stride passes what the smaller ones span.
  *   account, positions          device [batch, heads, capacity]
  *   account_out, positions_out  same shape (each may be its input): the
  *                  slots below min(length, keep) are written

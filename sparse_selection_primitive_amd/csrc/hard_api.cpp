@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <utility>
 
 #include "hard_internal.hpp"
 
@@ -110,6 +111,26 @@ lapsum_status check_cache(const lapsum_cache *c) {
 lapsum_status check_cache_pointers(const lapsum_cache *c) {
   if (!c->k || !c->v) return LAPSUM_ERR_NULL;
   return aligned(c->k, 16) && aligned(c->v, 16) ? LAPSUM_OK : LAPSUM_ERR_LAYOUT;
+}
+
+// Whether no two entries share memory, by the order of the strides: each has to pass what the
+// smaller ones span.  (Layouts whose dimensions are woven into each other without meeting are not told from those that
+// meet.)
+bool apart(const lapsum_cache &c, int64_t batch, int64_t head, int64_t entry) {
+  if (entry < c.width) return false;
+  struct {
+    int64_t stride, size;
+  } d[] = {{entry, c.capacity}, {head, c.heads}, {batch, c.batch}};
+  if (d[1].stride < d[0].stride) std::swap(d[0], d[1]);
+  if (d[2].stride < d[1].stride) std::swap(d[1], d[2]);
+  if (d[1].stride < d[0].stride) std::swap(d[0], d[1]);
+  __int128 span = c.width;
+  for (const auto &x : d) {
+    if (x.size == 1) continue;
+    if (x.stride < span) return false;
+    span += (__int128)x.stride * (x.size - 1);
+  }
+  return true;
 }
 
 lapsum_status check_attend(const lapsum_cache *c, int64_t news, int64_t q_heads) {
@@ -297,9 +318,8 @@ lapsum_status lapsum_cache_evict(const lapsum_cache *cache, const float *account
   if (keep < 1 || keep > cache->capacity) return LAPSUM_ERR_SHAPE;
   if (sinks < 0 || recent < 0) return LAPSUM_ERR_OPTION;
   // entries are written: no two of them may share memory
-  if (cache->k_stride_entry < cache->width || cache->v_stride_entry < cache->width ||
-      (cache->heads > 1 && (cache->k_stride_head == 0 || cache->v_stride_head == 0)) ||
-      (cache->batch > 1 && (cache->k_stride_batch == 0 || cache->v_stride_batch == 0)))
+  if (!apart(*cache, cache->k_stride_batch, cache->k_stride_head, cache->k_stride_entry) ||
+      !apart(*cache, cache->v_stride_batch, cache->v_stride_head, cache->v_stride_entry))
     return LAPSUM_ERR_LAYOUT;
   if (!account || !positions || !lengths || !account_out || !positions_out || !kept || !lengths_out ||
       (recent > 0 && !next_position))
