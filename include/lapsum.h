@@ -462,6 +462,82 @@ lapsum_status lapsum_cache_evict(const lapsum_cache *cache, const float *account
                                  int32_t recent, float *account_out, int32_t *positions_out, int32_t *kept,
                                  int32_t *lengths_out, void *workspace, size_t workspace_bytes, void *stream);
 
+/* The experts' matrices: element (i, o) of expert e, which takes input i to
+ * output o, at e * stride_expert + i * stride_input + o * stride_output.  One of
+ * stride_input and stride_output is 1 (a matrix stored [inputs, outputs] or
+ * [outputs, inputs]) and the other at least the size that it passes. */
+typedef struct lapsum_experts {
+    void *w;       /* device */
+    int32_t dtype; /* LAPSUM_BF16 or LAPSUM_F16 */
+    int32_t reserved;
+    int64_t experts, inputs, outputs; /* inputs and outputs at most LAPSUM_MAX_EXPERT_WIDTH */
+    int64_t stride_expert, stride_input, stride_output; /* elements */
+} lapsum_experts;
+
+#define LAPSUM_MAX_EXPERT_WIDTH ((int64_t)1 << 20)
+#define LAPSUM_MAX_EXPERT_STRIDE ((int64_t)1 << 21) /* elements between two rows, of a matrix too */
+
+/* The experts' products: rows in expert order (dispatch) times the matrix of
+ * their expert, whose rows are offsets[e] .. offsets[e + 1] - 1:
+ *     ys[r] = xs[r] W_e,    dxs[r] = dys[r] W_e',    dW_e = sum of xs[r]' dys[r] over e's rows.
+ * Sums are held in fp32 and rounded once.  A row that is no expert's (before
+ * offsets[0], from offsets[experts] on) gives 0 whatever it holds, in ys and dxs, and is in no
+ * dW; so does an expert without rows in dW.  Nothing of one expert's rows or matrix reaches
+ * another's, NaN and infinities included.
+ *   xs      device [rows, inputs] of the matrices' type, rows `xs_stride` elements apart
+ *   dys     device [rows, outputs], rows `dys_stride` elements apart
+ *   ys, dxs device, contiguous;  dw: as w, its own layout, no two elements in one place
+ *   offsets device [experts + 1], taken into 0 .. rows; of offsets that do not ascend it is
+ *           not defined which rows of ys and dxs are written
+ * rows <= LAPSUM_MAX_PAIRS.  Sizes, strides and pointers that are multiples of 16 bytes
+ * are the fast ones; any others (of whole elements) are taken too. */
+lapsum_status lapsum_expert_product_forward(const void *xs, int64_t xs_stride, int64_t rows, const lapsum_experts *w,
+                                            const int32_t *offsets, void *ys, void *stream);
+lapsum_status lapsum_expert_product_backward_rows(const void *dys, int64_t dys_stride, int64_t rows,
+                                                  const lapsum_experts *w, const int32_t *offsets, void *dxs,
+                                                  void *stream);
+lapsum_status lapsum_expert_product_backward_weights(const void *xs, int64_t xs_stride, const void *dys,
+                                                     int64_t dys_stride, int64_t rows, const int32_t *offsets,
+                                                     const lapsum_experts *dw, void *stream);
+
+#define LAPSUM_MAX_BEAMS 64
+#define LAPSUM_MAX_VOCAB ((int64_t)1 << 20)
+
+/* One step of a beam search: of all continuations of a search's beams, beam i by token v, the k
+ * with the highest
+ *     score(i, v) = scores[i] + x[i, v] - log sum_u e^x[i, u],
+ * in descending order; equal ones by beam, then token, ascending.
+ *   logits     device [batch, beams, vocab] of `dtype`, the batch * beams rows `row_stride` elements apart
+ *   scores     device [batch, beams] fp32: the beams' own log probabilities
+ *   ended      device [batch, beams] bytes, or NULL: a beam whose byte is not 0 has one continuation,
+ *              end_token (in 0 .. vocab - 1), at its own score; its logits are not read
+ *   k          1 .. LAPSUM_MAX_BEAMS, also beyond `beams` (twice as many, say)
+ *   scores_out device [batch, k] fp32;  parents, tokens device [batch, k] int32
+ * Scores are compared in fp64 (the sum of exponentials is an fp32 sum) and rounded to fp32 once.  A
+ * token whose logit is -inf is no continuation; logits of +inf share the
+ * probability equally, the others have none.  A beam with a NaN among its logits, without a logit above -inf,
+ * or with a score that is not finite, has no continuation.  Places that no
+ * continuation is left for get the score -inf and parent and token -1. */
+size_t lapsum_beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int32_t k);
+lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batch, int64_t beams, int64_t vocab,
+                                 int64_t row_stride, const float *scores, const uint8_t *ended, int32_t end_token,
+                                 int32_t k, float *scores_out, int32_t *parents, int32_t *tokens, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* The caches of a search follow its beams: sequence b * beams + j of the cache becomes what
+ * sequence b * beams + parents[b, j] was, in place, without a second cache: the entries below the parent's
+ * length, and with them the accounts and positions.  Entries at that length and behind stay as they are.
+ *   cache    batch a multiple of beams (at most LAPSUM_MAX_BEAMS); no two entries may share memory
+ *            (LAPSUM_ERR_LAYOUT), as for the eviction
+ *   parents  device [batch / beams, beams] int32; one outside 0 .. beams - 1 leaves its sequence
+ *            as it is, with length 0
+ *   lengths  device [batch] int32, taken as 0 .. capacity
+ *   account, positions  device [batch, heads, capacity], each may be NULL
+ *   lengths_out         device [batch]: the parents' lengths; not lengths itself (LAPSUM_ERR_LAYOUT) */
+lapsum_status lapsum_cache_reorder(const lapsum_cache *cache, int64_t beams, const int32_t *parents,
+                                   const int32_t *lengths, float *account, int32_t *positions, int32_t *lengths_out,
+                                   void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,7 +44,10 @@ EXPORTED = ["lapsum_options_init", "lapsum_status_string", "lapsum_plan", "lapsu
             "lapsum_route_forward", "lapsum_route_backward", "lapsum_dispatch_plan_workspace_bytes",
             "lapsum_dispatch_plan", "lapsum_dispatch_forward", "lapsum_dispatch_backward",
             "lapsum_combine_forward", "lapsum_combine_backward", "lapsum_cache_attend_workspace_bytes",
-            "lapsum_cache_attend", "lapsum_cache_evict_workspace_bytes", "lapsum_cache_evict"]
+            "lapsum_cache_attend", "lapsum_cache_evict_workspace_bytes", "lapsum_cache_evict",
+            "lapsum_expert_product_forward", "lapsum_expert_product_backward_rows",
+            "lapsum_expert_product_backward_weights", "lapsum_beam_select_workspace_bytes", "lapsum_beam_select",
+            "lapsum_cache_reorder"]
 NOALLOC_SCRATCH_BYTES = 1 << 20  # LAPSUM_NOALLOC_SCRATCH_BYTES
 
 
@@ -461,5 +464,7 @@ class Operator:
 
 from . import hard  # noqa: E402  (the hard selections use the helpers above)
 from .hard import (  # noqa: E402,F401
-    cache_attend, cache_evict, combine, combine_backward, combine_forward, dispatch, dispatch_backward,
-    dispatch_forward, dispatch_plan, route, route_backward, route_forward)
+    beam_select, cache_attend, cache_evict, cache_reorder, combine, combine_backward, combine_forward, dispatch,
+    dispatch_backward, dispatch_forward, dispatch_plan, expert_product, expert_product_backward,
+    expert_product_backward_rows, expert_product_backward_weights, expert_product_forward, route, route_backward,
+    route_forward)

@@ -27,7 +27,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblapsum.so")
 SOURCES = ["api.cpp", "onchip.hip", "stream.hip", "bracket.hip", "band.hip", "sort.hip", "bisect.hip",
-           "hard_api.cpp", "route.hip", "dispatch.hip", "attend.hip", "evict.hip"]
+           "hard_api.cpp", "route.hip", "dispatch.hip", "attend.hip", "evict.hip", "product.hip",
+           "beams.hip", "reorder.hip"]
 ARCH = "gfx950"
 
 

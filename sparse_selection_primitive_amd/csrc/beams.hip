@@ -1,0 +1,347 @@
+// One step of a beam search: the k best continuations of a search's beams over beams and vocabulary.
+//
+// score(i, v) = scores[i] + (x - M) - log S with M = max_u x[i, u] and S = sum_u e^(x[i, u] - M).
+//
+// First launch: rows are cut into parts of 512 tokens (16 lanes a part); each leaves its maximum and
+// its sum of e^(x - maximum).  That is the one pass over the logits, and no selection takes part in it.
+// Second launch, a workgroup a search: the sums give every beam's log S, so the parts' maxima become scores.  All of
+// the k best continuations lie in the k best parts (by score, then by place): a part
+// that is not among them has k parts before it, each with a continuation before all of its own.  So only
+// these k parts are read again, and of their tokens only those at or above the k-th best part's score can be among the
+// k best.
+//
+// Equal scores go by their place, and places are unique, so results do not depend on the order in which candidates are
+// gathered (an atomic count in LDS).
+#include "hard_dev.hpp"
+#include "hard_internal.hpp"
+
+namespace lapsum {
+namespace {
+
+constexpr int kPart = 512;        // tokens, or a power of two times as many
+constexpr int kMostParts = 8192;  // of a search: the second launch's share stays small
+constexpr int kThreads = 1024, kRows = kThreads / 16;
+constexpr int kList = 1024;
+constexpr float kLog2e = 1.44269504f;
+
+// 16 bytes of a row, which may start at any element
+template <class T>
+struct __attribute__((packed, aligned(sizeof(T)))) Loose {
+  pack_t<T> v;
+};
+// the tokens [t, t + N) of a row, -inf past its end
+template <class T>
+LDEV void load_tokens(const T *row, int t, int vocab, float (&x)[Pack<T>::N]) {
+  constexpr int N = Pack<T>::N;
+  if (t + N <= vocab) {
+    const pack_t<T> w = reinterpret_cast<const Loose<T> *>(row + t)->v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = (float)w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = t + i < vocab ? (float)row[t + i] : -INFINITY;
+  }
+}
+
+// joins (m, s) with (m2, s2): sums of e^(x - maximum), of -inf alone (-inf, 0); where the maximum is
+// +inf, s counts what is +inf
+LDEV void join(float &m, float &s, float m2, float s2) {
+  const float to = fmaxf(m, m2);
+  // at equal maxima the difference would be NaN for infinities
+  s = (m == to ? s : s * __builtin_amdgcn_exp2f((m - to) * kLog2e)) +
+      (m2 == to ? s2 : s2 * __builtin_amdgcn_exp2f((m2 - to) * kLog2e));
+  m = to;
+}
+template <int M>
+LDEV void join_lanes(float &m, float &s) {
+  const float m2 = pair_lane<M>(m), s2 = pair_lane<M>(s);
+  join(m, s, m2, s2);
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void beam_parts_kernel(BeamArgs a) {
+  constexpr int N = Pack<T>::N, L = kPart / (16 * N);
+  const int64_t row = grid_row();
+  if (row >= a.batch * a.beams || (a.ended != nullptr && a.ended[row] != 0)) return;
+  const int part = blockIdx.x * 16 + threadIdx.x / 16, lane = threadIdx.x % 16;
+  if (part >= a.chunks) return;
+  const T *x = static_cast<const T *>(a.logits) + row * a.stride;
+  float m = -INFINITY, s = 0.0f;
+  const int64_t begin = (int64_t)part * a.chunk;
+  for (int64_t t0 = begin; t0 < begin + a.chunk && t0 < a.vocab; t0 += kPart) {
+    float v[L][N];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int64_t t = t0 + (i * 16 + lane) * N;
+      load_tokens(x, (int)(t < a.vocab ? t : a.vocab), a.vocab, v[i]);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) top = fmaxf(top, v[i][j]);
+    float sum = 0.0f;
+    if (top > -1e30f && top < 1e30f) {
+      // e^(x - top) = 2^(x c - h) 2^-l with h + l the product top c in two parts
+      const float h = top * kLog2e, l = __builtin_fmaf(top, kLog2e, -h);
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        float part_sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) part_sum += __builtin_amdgcn_exp2f(__builtin_fmaf(v[i][j], kLog2e, -h));
+        sum += part_sum;
+      }
+      sum *= __builtin_amdgcn_exp2f(-l);
+    } else {  // nothing, only masked tokens (of the type's lowest value, too), or infinities
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float d = v[i][j] == top ? 0.0f : v[i][j] - top;  // NaN stays, -inf below -inf is not counted
+          sum += top == -INFINITY && d == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(d * kLog2e);
+        }
+    }
+    join(m, s, top, sum);
+  }
+  join_lanes<1>(m, s);
+  join_lanes<2>(m, s);
+  join_lanes<4>(m, s);
+  join_lanes<8>(m, s);
+  if (lane == 0) a.parts[row * a.chunks + part] = float2{m, s};
+}
+
+// --------------------------------------------------------------- selection
+// A candidate: its score and its place.  Before another: a higher score, or an equal one and a lower place.
+struct Best {
+  double score;
+  int place;
+  LDEV bool before(const Best &o) const { return score > o.score || (score == o.score && place < o.place); }
+};
+constexpr double kNone = -INFINITY;
+
+struct Shared {
+  double base[LAPSUM_MAX_BEAMS];  // scores - log S; -inf: no continuation
+  float top[LAPSUM_MAX_BEAMS];    // M
+  int done[LAPSUM_MAX_BEAMS];     // ended
+  double row_best[kRows];
+  double least;                   // no candidate below it is among the k best
+  int listed;
+  double score[kList];
+  int place[kList];
+  double best_score[LAPSUM_MAX_BEAMS];  // of the selected ones, in order
+  int best_place[LAPSUM_MAX_BEAMS];
+  double wave_score[kThreads / 64];
+  int wave_place[kThreads / 64];
+};
+
+LDEV double score_of(const Shared &sh, int beam, float x) {
+  const float top = sh.top[beam];
+  const double s = sh.base[beam] + (x == top ? 0.0 : (double)x - (double)top);
+  return s > kNone ? s : kNone;  // NaN is none
+}
+
+// The k first of the listed candidates in their order, each ranked by how many come before it.
+LDEV void rank_listed(Shared &sh, int n, int k) {
+  for (int i = threadIdx.x; i < k; i += kThreads) {
+    sh.best_score[i] = kNone;
+    sh.best_place[i] = -1;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    const Best me{sh.score[threadIdx.x], sh.place[threadIdx.x]};
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += Best{sh.score[i], sh.place[i]}.before(me) ? 1 : 0;
+    if (rank < k) {
+      sh.best_score[rank] = me.score;
+      sh.best_place[rank] = me.place;
+    }
+  }
+  __syncthreads();
+}
+
+// The same when they do not fit the list: one after the other, each the first behind the last one.  each(f) calls
+// f(candidate) for all candidates of this thread.
+template <class Each>
+LDEV void select_in_turn(Shared &sh, int k, const Each &each) {
+  Best last{INFINITY, -1};
+  for (int j = 0; j < k; ++j) {
+    Best b{kNone, 0x7FFFFFFF};
+    each([&](const Best &c) {
+      if (c.score > kNone && last.before(c) && c.before(b)) b = c;
+    });
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const Best o{__shfl_xor(b.score, d, 64), __shfl_xor(b.place, d, 64)};
+      if (o.before(b)) b = o;
+    }
+    if (threadIdx.x % 64 == 0) {
+      sh.wave_score[threadIdx.x / 64] = b.score;
+      sh.wave_place[threadIdx.x / 64] = b.place;
+    }
+    __syncthreads();
+    for (int w = 0; w < kThreads / 64; ++w) {
+      const Best o{sh.wave_score[w], sh.wave_place[w]};
+      if (o.before(b)) b = o;
+    }
+    if (threadIdx.x == 0) {
+      sh.best_score[j] = b.score;
+      sh.best_place[j] = b.score > kNone ? b.place : -1;
+    }
+    last = b;
+    __syncthreads();
+  }
+}
+
+// The k first of all candidates at or above sh.least.
+template <class Each>
+LDEV void select(Shared &sh, int k, const Each &each) {
+  const double least = sh.least;
+  each([&](const Best &c) {
+    if (c.score > kNone && c.score >= least) {
+      const int at = atomicAdd(&sh.listed, 1);
+      if (at < kList) {
+        sh.score[at] = c.score;
+        sh.place[at] = c.place;
+      }
+    }
+  });
+  __syncthreads();
+  const int n = sh.listed;
+  if (n <= kList)
+    rank_listed(sh, n, k);
+  else
+    select_in_turn(sh, k, each);
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
+  constexpr int N = Pack<T>::N;
+  __shared__ Shared sh;
+  __shared__ int chosen[LAPSUM_MAX_BEAMS];
+  lds_poison(sh);
+  lds_poison(chosen);
+  const int64_t search = grid_row();
+  if (search >= a.batch) return;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const float2 *parts = a.parts + search * a.beams * a.chunks;
+
+  for (int i = wave; i < a.beams; i += kThreads / 64) {
+    const float score = a.scores[search * a.beams + i];
+    const bool ended = a.ended != nullptr && a.ended[search * a.beams + i] != 0;
+    float m = -INFINITY, s = 0.0f;
+    if (!ended) {
+      for (int c = lane; c < a.chunks; c += 64) {
+        const float2 x = parts[i * a.chunks + c];
+        join(m, s, x.x, x.y);
+      }
+      join_lanes<1>(m, s);
+      join_lanes<2>(m, s);
+      join_lanes<4>(m, s);
+      join_lanes<8>(m, s);
+      join_lanes<16>(m, s);
+      join_lanes<32>(m, s);
+    }
+    if (lane == 0) {
+      const bool finite = score > -INFINITY && score < INFINITY;
+      const bool none = !finite || (!ended && !(s > 0.0f));  // a NaN sum, or nothing above -inf
+      sh.base[i] = none ? kNone : (ended ? (double)score : (double)score - log((double)s));
+      sh.top[i] = ended || none ? 0.0f : m;
+      sh.done[i] = ended;
+    }
+  }
+  if (threadIdx.x == 0) sh.listed = 0;
+  __syncthreads();
+
+  // the best parts
+  const int all = a.beams * a.chunks, end_part = a.ended != nullptr ? a.end_token / a.chunk : 0;
+  const auto each_part = [&](const auto &f) {
+    for (int i = threadIdx.x; i < all; i += kThreads) {
+      const int beam = i / a.chunks;
+      if (sh.done[beam])
+        f(Best{i - beam * a.chunks == end_part ? sh.base[beam] : kNone, i});
+      else
+        f(Best{score_of(sh, beam, parts[i].x), i});
+    }
+  };
+  // the k-th best of the rows of 16 lanes' best: k candidates are at least that
+  double mine = kNone;
+  each_part([&](const Best &c) { mine = fmax(mine, c.score); });
+  mine = team_max<16>(mine);
+  if (threadIdx.x % 16 == 0) sh.row_best[threadIdx.x / 16] = mine;
+  __syncthreads();
+  {
+    const int row = threadIdx.x / 16, first = threadIdx.x % 16 * (kRows / 16);
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < kRows / 16; ++i) {
+      const Best o{sh.row_best[first + i], first + i};
+      before += o.before(Best{mine, row}) ? 1 : 0;
+    }
+    before += (int)xor_lanes<1>((uint32_t)before);
+    before += (int)xor_lanes<2>((uint32_t)before);
+    before += (int)xor_lanes<7>((uint32_t)before);
+    before += (int)xor_lanes<15>((uint32_t)before);
+    if (before == a.k - 1 && threadIdx.x % 16 == 0) sh.least = mine;
+  }
+  __syncthreads();
+  select(sh, a.k, each_part);
+
+  // the best tokens of these parts
+  if ((int)threadIdx.x < a.k) chosen[threadIdx.x] = sh.best_place[threadIdx.x];
+  if (threadIdx.x == 0) {
+    sh.least = sh.best_score[a.k - 1];
+    sh.listed = 0;
+  }
+  __syncthreads();
+  const int units = a.chunk / N;
+  const auto each_token = [&](const auto &f) {
+    for (int u = threadIdx.x; u < a.k * units; u += kThreads) {
+      const int part = chosen[u / units];
+      if (part < 0) continue;
+      const int beam = part / a.chunks, t = (part - beam * a.chunks) * a.chunk + u % units * N;
+      if (sh.done[beam]) {
+        if (a.end_token >= t && a.end_token < t + N) f(Best{sh.base[beam], beam * a.vocab + a.end_token});
+        continue;
+      }
+      if (t >= a.vocab) continue;
+      float x[N];
+      load_tokens(static_cast<const T *>(a.logits) + (search * a.beams + beam) * a.stride, t, a.vocab, x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) f(Best{score_of(sh, beam, x[j]), beam * a.vocab + t + j});
+    }
+  };
+  select(sh, a.k, each_token);
+  if ((int)threadIdx.x < a.k) {
+    const int place = sh.best_place[threadIdx.x];
+    const int64_t at = search * a.k + threadIdx.x;
+    a.scores_out[at] = (float)sh.best_score[threadIdx.x];
+    a.parents[at] = place < 0 ? -1 : place / a.vocab;
+    a.tokens[at] = place < 0 ? -1 : place % a.vocab;
+  }
+}
+
+template <class T>
+hipError_t beams(const BeamArgs &a, hipStream_t s) {
+  beam_parts_kernel<T><<<rows_grid((unsigned)((a.chunks + 15) / 16), a.batch * a.beams), dim3(256), 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  beam_select_kernel<T><<<rows_grid(1, a.batch), dim3(kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+void beam_parts(int64_t beams, int64_t vocab, int &chunk, int &chunks) {
+  int64_t size = kPart;
+  while (beams * ((vocab + size - 1) / size) > kMostParts) size *= 2;
+  chunk = (int)size;
+  chunks = (int)((vocab + size - 1) / size);
+}
+
+hipError_t launch_beam_select(const BeamArgs &a, int dtype, hipStream_t s) {
+  if (dtype == LAPSUM_F32) return beams<f32>(a, s);
+  if (dtype == LAPSUM_BF16) return beams<bf16>(a, s);
+  return beams<f16>(a, s);
+}
+
+}  // namespace lapsum

@@ -13,6 +13,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -33,6 +34,12 @@ struct Entries {
   decltype(&lapsum_cache_attend) attend;
   decltype(&lapsum_cache_evict_workspace_bytes) evict_bytes;
   decltype(&lapsum_cache_evict) evict;
+  decltype(&lapsum_expert_product_forward) product_forward;
+  decltype(&lapsum_expert_product_backward_rows) product_backward_rows;
+  decltype(&lapsum_expert_product_backward_weights) product_backward_weights;
+  decltype(&lapsum_beam_select_workspace_bytes) beam_bytes;
+  decltype(&lapsum_beam_select) beam_select;
+  decltype(&lapsum_cache_reorder) reorder;
 };
 Entries entry{};
 
@@ -360,6 +367,130 @@ PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END
 }
 
+// [experts, inputs, outputs], stored so or with inputs and outputs changed over
+bool matrices(const at::Tensor *w, lapsum_experts &e) {
+  if (w == nullptr || w->dim() != 3 || dtype_of(*w) < LAPSUM_BF16) return false;
+  e = lapsum_experts{w->data_ptr(), dtype_of(*w),   0,           w->size(0),  w->size(1),
+                     w->size(2),    w->stride(0), w->stride(1), w->stride(2)};
+  return (e.stride_output == 1 && e.stride_input >= e.outputs) || (e.stride_input == 1 && e.stride_output >= e.inputs);
+}
+bool expert_offsets(const at::Tensor *o, const lapsum_experts &e) { return offsets_of(o) && o->numel() == e.experts + 1; }
+bool expert_side(const at::Tensor *x, const at::Tensor &w, int64_t width) {
+  return rows(x) && x->scalar_type() == w.scalar_type() && x->size(1) == width && x->stride(0) <= LAPSUM_MAX_EXPERT_STRIDE;
+}
+
+// (xs, w, offsets)
+PyObject *expert_product_forward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  BODY(3)
+  const at::Tensor *x = gpu(dev, args[0]), *w = gpu(dev, args[1]), *o = gpu(dev, args[2]);
+  lapsum_experts e;
+  if (!matrices(w, e) || !expert_side(x, *w, e.inputs) || !expert_offsets(o, e)) return none();
+  at::Tensor ys = make(dev, {x->size(0), e.outputs}, w->scalar_type());
+  const lapsum_status st =
+      entry.product_forward(x->data_ptr(), x->stride(0), x->size(0), &e,
+                            static_cast<const int32_t *>(o->data_ptr()), ys.data_ptr(), stream_of(*x));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_expert_product_forward");
+  return wrap(std::move(ys));
+  END
+}
+
+// (dys, w, offsets)
+PyObject *expert_product_backward_rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  BODY(3)
+  const at::Tensor *dy = gpu(dev, args[0]), *w = gpu(dev, args[1]), *o = gpu(dev, args[2]);
+  lapsum_experts e;
+  if (!matrices(w, e) || !expert_side(dy, *w, e.outputs) || !expert_offsets(o, e)) return none();
+  at::Tensor dxs = make(dev, {dy->size(0), e.inputs}, w->scalar_type());
+  const lapsum_status st =
+      entry.product_backward_rows(dy->data_ptr(), dy->stride(0), dy->size(0), &e,
+                                  static_cast<const int32_t *>(o->data_ptr()), dxs.data_ptr(), stream_of(*dy));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_expert_product_backward_rows");
+  return wrap(std::move(dxs));
+  END
+}
+
+// (dys, xs, w, offsets)
+PyObject *expert_product_backward_weights(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  BODY(4)
+  const at::Tensor *dy = gpu(dev, args[0]), *x = gpu(dev, args[1]), *w = gpu(dev, args[2]), *o = gpu(dev, args[3]);
+  lapsum_experts e;
+  if (!matrices(w, e) || !expert_side(x, *w, e.inputs) || !expert_side(dy, *w, e.outputs) ||
+      x->size(0) != dy->size(0) || !expert_offsets(o, e))
+    return none();
+  // stored as w is
+  const bool swapped = e.stride_output != 1;
+  at::Tensor dw = swapped ? make(dev, {e.experts, e.outputs, e.inputs}, w->scalar_type())
+                          : make(dev, {e.experts, e.inputs, e.outputs}, w->scalar_type());
+  e.w = dw.data_ptr();
+  e.stride_expert = e.inputs * e.outputs;
+  e.stride_input = swapped ? 1 : e.outputs;
+  e.stride_output = swapped ? e.inputs : 1;
+  const lapsum_status st =
+      entry.product_backward_weights(x->data_ptr(), x->stride(0), dy->data_ptr(), dy->stride(0), x->size(0),
+                                     static_cast<const int32_t *>(o->data_ptr()), &e, stream_of(*x));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_expert_product_backward_weights");
+  return wrap(swapped ? dw.transpose(1, 2) : std::move(dw));
+  END
+}
+
+// (logits, scores, k, ended, end_token); k None: the beams
+PyObject *beam_select(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  BODY(5)
+  const at::Tensor *x = gpu(dev, args[0]), *scores = gpu(dev, args[1]);
+  const at::Tensor *ended = args[3] == Py_None ? nullptr : gpu(dev, args[3]);
+  if (x == nullptr || x->dim() != 3 || dtype_of(*x) < 0 || x->stride(2) != 1 || x->stride(1) < x->size(2) ||
+      x->stride(0) != x->stride(1) * x->size(1))
+    return none();
+  const int64_t batch = x->size(0), beams = x->size(1), vocab = x->size(2);
+  if (!plain(scores, at::kFloat, batch * beams) || scores->dim() != 2 || scores->size(0) != batch) return none();
+  int32_t end = 0;
+  if (args[3] != Py_None) {
+    if (!plain(ended, at::kBool, batch * beams) || ended->dim() != 2 || ended->size(0) != batch || args[4] == Py_None)
+      return none();
+    end = int32_of(args[4]);
+  }
+  const int32_t k = args[2] == Py_None ? (int32_t)std::min<int64_t>(beams, INT32_MAX) : int32_of(args[2]);
+  if (PyErr_Occurred() || k < 1 || k > LAPSUM_MAX_BEAMS) return none();
+  at::Tensor out = make(dev, {batch, k}, at::kFloat), parents = make(dev, {batch, k}, at::kInt);
+  at::Tensor tokens = make(dev, {batch, k}, at::kInt);
+  const Workspace ws(dev, entry.beam_bytes(batch, beams, vocab, k));
+  const lapsum_status st =
+      entry.beam_select(x->data_ptr(), dtype_of(*x), batch, beams, vocab, x->stride(1),
+                        static_cast<const float *>(scores->data_ptr()),
+                        ended ? static_cast<const uint8_t *>(ended->data_ptr()) : nullptr, end, k,
+                        static_cast<float *>(out.data_ptr()), static_cast<int32_t *>(parents.data_ptr()),
+                        static_cast<int32_t *>(tokens.data_ptr()), ws.at, ws.bytes, stream_of(*x));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_beam_select");
+  return Py_BuildValue("(NNN)", wrap(std::move(out)), wrap(std::move(parents)), wrap(std::move(tokens)));
+  END
+}
+
+// (k, v, parents, lengths, account, positions)
+PyObject *cache_reorder(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  BODY(6)
+  const at::Tensor *k = gpu(dev, args[0]), *v = gpu(dev, args[1]), *parents = gpu(dev, args[2]);
+  const at::Tensor *lengths = gpu(dev, args[3]);
+  const at::Tensor *account = args[4] == Py_None ? nullptr : gpu(dev, args[4]);
+  const at::Tensor *positions = args[5] == Py_None ? nullptr : gpu(dev, args[5]);
+  lapsum_cache c{};
+  if (!cache_of(k, v, c) || parents == nullptr || parents->dim() != 2 || !plain(parents, at::kInt, c.batch) ||
+      !per_sequence(lengths, *k) || (args[4] != Py_None && !per_entry(account, *k, at::kFloat)) ||
+      (args[5] != Py_None && !per_entry(positions, *k, at::kInt)))
+    return none();
+  at::Tensor after = make(dev, {c.batch}, at::kInt);
+  const lapsum_status st =
+      entry.reorder(&c, parents->size(1), static_cast<const int32_t *>(parents->data_ptr()),
+                    static_cast<const int32_t *>(lengths->data_ptr()),
+                    account ? static_cast<float *>(account->data_ptr()) : nullptr,
+                    positions ? static_cast<int32_t *>(positions->data_ptr()) : nullptr,
+                    static_cast<int32_t *>(after.data_ptr()), stream_of(*k));
+  if (st != LAPSUM_OK) return refused(st, "lapsum_cache_reorder");
+  for (const at::Tensor *t : {k, v, account, positions})
+    if (t != nullptr) written(*t);
+  return wrap(std::move(after));
+  END
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),
                          METHOD(on_failure),
@@ -372,6 +503,11 @@ PyMethodDef methods[] = {METHOD(bind),
                          METHOD(combine_backward),
                          METHOD(cache_attend),
                          METHOD(cache_evict),
+                         METHOD(expert_product_forward),
+                         METHOD(expert_product_backward_rows),
+                         METHOD(expert_product_backward_weights),
+                         METHOD(beam_select),
+                         METHOD(cache_reorder),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -141,6 +141,45 @@ lapsum_status check_attend(const lapsum_cache *c, int64_t news, int64_t q_heads)
   return LAPSUM_OK;
 }
 
+lapsum_status check_experts(const lapsum_experts *w, int64_t rows) {
+  if (!w) return LAPSUM_ERR_NULL;
+  if (w->dtype != LAPSUM_BF16 && w->dtype != LAPSUM_F16) return LAPSUM_ERR_OPTION;
+  if (w->experts < 1 || w->experts > LAPSUM_MAX_EXPERTS || w->inputs < 1 || w->inputs > LAPSUM_MAX_EXPERT_WIDTH ||
+      w->outputs < 1 || w->outputs > LAPSUM_MAX_EXPERT_WIDTH || rows < 1 || rows > LAPSUM_MAX_PAIRS)
+    return LAPSUM_ERR_SHAPE;
+  const bool out_next = w->stride_output == 1 && w->stride_input >= w->outputs;
+  const bool in_next = w->stride_input == 1 && w->stride_output >= w->inputs;
+  if (!out_next && !in_next) return LAPSUM_ERR_LAYOUT;
+  if (w->stride_input > LAPSUM_MAX_EXPERT_STRIDE || w->stride_output > LAPSUM_MAX_EXPERT_STRIDE) return LAPSUM_ERR_LAYOUT;
+  return w->stride_expert < 0 ? LAPSUM_ERR_LAYOUT : LAPSUM_OK;
+}
+lapsum_status check_row_stride(int64_t stride, int64_t width) {
+  return stride < width || stride > LAPSUM_MAX_EXPERT_STRIDE ? LAPSUM_ERR_LAYOUT : LAPSUM_OK;
+}
+// whether a matrix' outputs lie next to each other (of one column or row both hold)
+bool outputs_next(const lapsum_experts &w) { return w.stride_output == 1 && w.stride_input >= w.outputs; }
+
+ProductArgs product_args(const lapsum_experts &w, int64_t rows, const int32_t *offsets) {
+  ProductArgs a{};
+  a.rows = rows;
+  a.experts = (int)w.experts;
+  a.offsets = offsets;
+  return a;
+}
+
+lapsum_status check_beams(int32_t dtype, int64_t batch, int64_t beams, int64_t vocab, int32_t k) {
+  if (!known_dtype(dtype)) return LAPSUM_ERR_OPTION;
+  if (beams < 1 || beams > LAPSUM_MAX_BEAMS || batch < 1 || batch > LAPSUM_MAX_ROWS / beams || vocab < 1 ||
+      vocab > LAPSUM_MAX_VOCAB)
+    return LAPSUM_ERR_SHAPE;
+  return k < 1 || k > LAPSUM_MAX_BEAMS ? LAPSUM_ERR_OPTION : LAPSUM_OK;
+}
+size_t beam_bytes(int64_t batch, int64_t beams, int64_t vocab) {
+  int chunk, chunks;
+  beam_parts(beams, vocab, chunk, chunks);
+  return aligned_up((size_t)(batch * beams) * (size_t)chunks * sizeof(float2));
+}
+
 size_t attend_bytes(const AttendPlan &p) {
   return aligned_up(p.part_o) + aligned_up(p.part_ml) + aligned_up(p.dropped) + aligned_up(p.logits);
 }
@@ -357,6 +396,143 @@ lapsum_status lapsum_cache_evict(const lapsum_cache *cache, const float *account
   a.workspace = workspace;
   (void)hipGetLastError();
   return done(launch_evict(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+lapsum_status lapsum_expert_product_forward(const void *xs, int64_t xs_stride, int64_t rows, const lapsum_experts *w,
+                                            const int32_t *offsets, void *ys, void *stream) {
+  lapsum_status st = check_experts(w, rows);
+  if (st != LAPSUM_OK) return st;
+  st = check_row_stride(xs_stride, w->inputs);
+  if (st != LAPSUM_OK) return st;
+  if (!xs || !w->w || !offsets || !ys) return LAPSUM_ERR_NULL;
+  ProductArgs a = product_args(*w, rows, offsets);
+  a.a = xs;
+  a.am = xs_stride;
+  a.ak = 1;
+  a.b = w->w;
+  a.be = w->stride_expert;
+  a.bk = w->stride_input;
+  a.bn = w->stride_output;
+  a.c = ys;
+  a.cm = w->outputs;
+  a.n = (int)w->outputs;
+  a.k = (int)w->inputs;
+  (void)hipGetLastError();
+  return done(launch_product_rows(a, w->dtype, reinterpret_cast<hipStream_t>(stream)));
+}
+
+lapsum_status lapsum_expert_product_backward_rows(const void *dys, int64_t dys_stride, int64_t rows,
+                                                  const lapsum_experts *w, const int32_t *offsets, void *dxs,
+                                                  void *stream) {
+  // the same product, of the matrices with inputs and outputs changed over
+  lapsum_experts t{};
+  if (w) {
+    t = *w;
+    std::swap(t.inputs, t.outputs);
+    std::swap(t.stride_input, t.stride_output);
+  }
+  return lapsum_expert_product_forward(dys, dys_stride, rows, w ? &t : nullptr, offsets, dxs, stream);
+}
+
+lapsum_status lapsum_expert_product_backward_weights(const void *xs, int64_t xs_stride, const void *dys,
+                                                     int64_t dys_stride, int64_t rows, const int32_t *offsets,
+                                                     const lapsum_experts *dw, void *stream) {
+  lapsum_status st = check_experts(dw, rows);
+  if (st != LAPSUM_OK) return st;
+  st = check_row_stride(xs_stride, dw->inputs);
+  if (st == LAPSUM_OK) st = check_row_stride(dys_stride, dw->outputs);
+  if (st != LAPSUM_OK) return st;
+  if (!xs || !dys || !offsets || !dw->w) return LAPSUM_ERR_NULL;
+  // matrices are written: no two of them may share memory
+  const bool next = outputs_next(*dw);
+  const int64_t across = next ? dw->inputs : dw->outputs, along = next ? dw->outputs : dw->inputs;
+  const int64_t stride = next ? dw->stride_input : dw->stride_output;
+  if (dw->experts > 1 && dw->stride_expert < stride * (across - 1) + along) return LAPSUM_ERR_LAYOUT;
+  ProductArgs a = product_args(*dw, rows, offsets);
+  a.a = next ? xs : dys;
+  a.b = next ? dys : xs;
+  a.am = 1;
+  a.ak = next ? xs_stride : dys_stride;
+  a.bk = next ? dys_stride : xs_stride;
+  a.bn = 1;
+  a.c = dw->w;
+  a.ce = dw->stride_expert;
+  a.cm = stride;
+  a.m = (int)across;
+  a.n = (int)along;
+  (void)hipGetLastError();
+  return done(launch_product_weights(a, dw->dtype, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t lapsum_beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int32_t k) {
+  return check_beams(LAPSUM_F32, batch, beams, vocab, k) == LAPSUM_OK ? beam_bytes(batch, beams, vocab) : 0;
+}
+
+lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batch, int64_t beams, int64_t vocab,
+                                 int64_t row_stride, const float *scores, const uint8_t *ended, int32_t end_token,
+                                 int32_t k, float *scores_out, int32_t *parents, int32_t *tokens, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  lapsum_status st = check_beams(dtype, batch, beams, vocab, k);
+  if (st != LAPSUM_OK) return st;
+  if (row_stride < vocab) return LAPSUM_ERR_LAYOUT;
+  if (ended && (end_token < 0 || end_token >= vocab)) return LAPSUM_ERR_OPTION;
+  if (!logits || !scores || !scores_out || !parents || !tokens) return LAPSUM_ERR_NULL;
+  st = check_workspace(workspace, workspace_bytes, beam_bytes(batch, beams, vocab));
+  if (st != LAPSUM_OK) return st;
+  BeamArgs a{};
+  a.logits = logits;
+  a.batch = batch;
+  a.stride = row_stride;
+  a.beams = (int)beams;
+  a.vocab = (int)vocab;
+  a.k = k;
+  beam_parts(beams, vocab, a.chunk, a.chunks);
+  a.scores = scores;
+  a.ended = ended;
+  a.end_token = end_token;
+  a.scores_out = scores_out;
+  a.parents = parents;
+  a.tokens = tokens;
+  a.parts = static_cast<float2 *>(workspace);
+  (void)hipGetLastError();
+  return done(launch_beam_select(a, dtype, reinterpret_cast<hipStream_t>(stream)));
+}
+
+lapsum_status lapsum_cache_reorder(const lapsum_cache *cache, int64_t beams, const int32_t *parents,
+                                   const int32_t *lengths, float *account, int32_t *positions, int32_t *lengths_out,
+                                   void *stream) {
+  lapsum_status st = check_cache(cache);
+  if (st != LAPSUM_OK) return st;
+  if (beams < 1 || beams > LAPSUM_MAX_BEAMS || cache->batch % beams != 0) return LAPSUM_ERR_SHAPE;
+  // entries are written: no two of them may share memory
+  if (!apart(*cache, cache->k_stride_batch, cache->k_stride_head, cache->k_stride_entry) ||
+      !apart(*cache, cache->v_stride_batch, cache->v_stride_head, cache->v_stride_entry))
+    return LAPSUM_ERR_LAYOUT;
+  if (!parents || !lengths || !lengths_out) return LAPSUM_ERR_NULL;
+  if (lengths_out == lengths) return LAPSUM_ERR_LAYOUT;
+  st = check_cache_pointers(cache);
+  if (st != LAPSUM_OK) return st;
+  ReorderArgs a{};
+  a.k = cache->k;
+  a.v = cache->v;
+  a.kb = cache->k_stride_batch;
+  a.kh = cache->k_stride_head;
+  a.ke = cache->k_stride_entry;
+  a.vb = cache->v_stride_batch;
+  a.vh = cache->v_stride_head;
+  a.ve = cache->v_stride_entry;
+  a.searches = cache->batch / beams;
+  a.heads = cache->heads;
+  a.capacity = cache->capacity;
+  a.beams = (int)beams;
+  a.width = cache->width;
+  a.parents = parents;
+  a.lengths = lengths;
+  a.account = account;
+  a.positions = positions;
+  a.lengths_out = lengths_out;
+  (void)hipGetLastError();
+  return done(launch_reorder(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

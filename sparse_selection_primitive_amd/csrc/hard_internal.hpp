@@ -98,4 +98,48 @@ struct EvictArgs {
 size_t evict_workspace(int64_t batch, int64_t heads, int64_t capacity, int64_t keep);
 hipError_t launch_evict(const EvictArgs &a, hipStream_t s);
 
+
+// product.hip: C = A B for every expert, of its own rows.  An element of A is at m * am + k * ak,
+// of B at e * be + k * bk + n * bn, of C at m * cm + n, where rows are counted through all experts.
+struct ProductArgs {
+  const void *a, *b;
+  void *c;
+  int64_t am, ak, be, bk, bn, ce, cm;
+  int64_t rows;             // of all experts and none
+  int m, n, k;              // sizes; the one that the rows take the place of is not used
+  int experts;
+  const int32_t *offsets;   // [experts + 1]
+};
+hipError_t launch_product_rows(const ProductArgs &a, int dtype, hipStream_t s);     // the rows are m: ys, dxs
+hipError_t launch_product_weights(const ProductArgs &a, int dtype, hipStream_t s);  // the rows are k: dw
+
+// beams.hip
+struct BeamArgs {
+  const void *logits;
+  int64_t batch, stride;
+  int beams, vocab, k;
+  int chunk, chunks;        // tokens of a part, parts of a row
+  const float *scores;
+  const uint8_t *ended;     // or NULL
+  int end_token;
+  float *scores_out;
+  int32_t *parents, *tokens;
+  float2 *parts;            // [batch * beams][chunks]: maximum, sum of e^(x - maximum)
+};
+void beam_parts(int64_t beams, int64_t vocab, int &chunk, int &chunks);
+hipError_t launch_beam_select(const BeamArgs &a, int dtype, hipStream_t s);
+
+// reorder.hip
+struct ReorderArgs {
+  void *k, *v;
+  int64_t kb, kh, ke, vb, vh, ve;
+  int64_t searches, heads, capacity;
+  int beams, width;
+  const int32_t *parents, *lengths;
+  float *account;           // or NULL
+  int32_t *positions;       // or NULL
+  int32_t *lengths_out;
+};
+hipError_t launch_reorder(const ReorderArgs &a, hipStream_t s);
+
 }  // namespace lapsum

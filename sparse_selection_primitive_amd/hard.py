@@ -8,10 +8,20 @@ Routing of tokens to experts and back, with gradients:
     y = combine_forward(ys, slot, weights)           # ys: the experts' outputs, in the rows of xs
     route / dispatch / combine                       # the same, differentiable
 
+The experts' products in between, with gradients:
+
+    ys = expert_product_forward(xs, w, offsets)      # w [experts, inputs, outputs]
+    expert_product                                   # the same, differentiable
+
 A cache that keeps the entries which received the most attention:
 
     out = cache_attend(q, k, v, lengths, account)    # adds each entry's weight to account
     kept, lengths = cache_evict(k, v, account, positions, lengths, keep, next_position=n, recent=256)
+
+A beam search's step, and the caches that follow its beams:
+
+    scores, parents, tokens = beam_select(logits, scores, k, ended=ended, end_token=2)
+    lengths = cache_reorder(k, v, parents, lengths, account, positions)
 
 As in the rest of the package this only marshals arguments; the formulas and
 what happens to masked, infinite and missing values stand in
@@ -37,9 +47,12 @@ _native = None
 _NATIVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
 _NATIVE_CALLS = ["route_forward", "route_backward", "dispatch_plan_workspace_bytes", "dispatch_plan",
                  "dispatch_forward", "dispatch_backward", "combine_forward", "combine_backward",
-                 "cache_attend_workspace_bytes", "cache_attend", "cache_evict_workspace_bytes", "cache_evict"]
+                 "cache_attend_workspace_bytes", "cache_attend", "cache_evict_workspace_bytes", "cache_evict",
+                 "expert_product_forward", "expert_product_backward_rows", "expert_product_backward_weights",
+                 "beam_select_workspace_bytes", "beam_select", "cache_reorder"]
 SCORES = {"softmax": 0, "sigmoid": 1}
-MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS = 1024, 32, 64
+MAX_EXPERTS, MAX_CHOICES, MAX_GROUPS, MAX_BEAMS = 1024, 32, 64, 64
+MAX_EXPERT_STRIDE = 1 << 21
 
 
 class RouteOptions(ctypes.Structure):
@@ -55,9 +68,16 @@ class Cache(ctypes.Structure):
                 ("v_stride_head", ctypes.c_int64), ("v_stride_entry", ctypes.c_int64)]
 
 
+class Experts(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("experts", ctypes.c_int64), ("inputs", ctypes.c_int64), ("outputs", ctypes.c_int64),
+                ("stride_expert", ctypes.c_int64), ("stride_input", ctypes.c_int64),
+                ("stride_output", ctypes.c_int64)]
+
+
 def declare(lib):
     i32, i64, vp, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
-    opt, cache = ctypes.POINTER(RouteOptions), ctypes.POINTER(Cache)
+    opt, cache, experts = ctypes.POINTER(RouteOptions), ctypes.POINTER(Cache), ctypes.POINTER(Experts)
     for name, res, args in [
         ("route_forward", ctypes.c_int, [vp, i32, i64, i64, i64, vp, opt, vp, vp, vp]),
         ("route_backward", ctypes.c_int, [vp, vp, i32, i64, i64, i64, vp, opt, vp, vp]),
@@ -71,6 +91,12 @@ def declare(lib):
         ("cache_attend", ctypes.c_int, [vp, cache, vp, i64, i64, ctypes.c_float, vp, vp, vp, vp, size, vp]),
         ("cache_evict_workspace_bytes", size, [cache, i64]),
         ("cache_evict", ctypes.c_int, [cache, vp, vp, vp, i64, vp, i32, i32, vp, vp, vp, vp, vp, size, vp]),
+        ("expert_product_forward", ctypes.c_int, [vp, i64, i64, experts, vp, vp, vp]),
+        ("expert_product_backward_rows", ctypes.c_int, [vp, i64, i64, experts, vp, vp, vp]),
+        ("expert_product_backward_weights", ctypes.c_int, [vp, i64, vp, i64, i64, vp, experts, vp]),
+        ("beam_select_workspace_bytes", size, [i64, i64, i64, i32]),
+        ("beam_select", ctypes.c_int, [vp, i32, i64, i64, i64, i64, vp, vp, i32, i32, vp, vp, vp, vp, size, vp]),
+        ("cache_reorder", ctypes.c_int, [cache, i64, vp, vp, vp, vp, vp, vp]),
     ]:
         f = getattr(lib, "lapsum_" + name)
         f.restype, f.argtypes = res, args
@@ -399,10 +425,132 @@ def combine(ys, weights, slot, offsets):
     return _differentiable()[2].apply(ys, weights, slot, offsets)
 
 
+# ---------------------------------------------------------- experts' products
+def _matrices(w, name):
+    """w [experts, inputs, outputs] as the library's: stored [inputs, outputs] or [outputs, inputs], or copied."""
+    experts, inputs, outputs = w.shape
+    se, si, so = w.stride()
+    if inputs == 1 and so == 1:
+        si = outputs  # the stride of a size of one is any
+    if outputs == 1 and si == 1:
+        so = inputs
+    if not ((so == 1 and outputs <= si <= MAX_EXPERT_STRIDE) or (si == 1 and inputs <= so <= MAX_EXPERT_STRIDE)):
+        w = w.contiguous()
+        se, si, so = inputs * outputs, outputs, 1
+    return w, Experts(w.data_ptr(), _dtype(w, name, (BF16, F16)), 0, experts, inputs, outputs, se, si, so)
+
+
+def _expert_rows(x, name, w, width):
+    """[rows, width] of the matrices' type with contiguous rows: (x, row stride)."""
+    _gpu(x, name, 2, w.device)
+    if x.dtype != w.dtype or x.shape[1] != width:
+        raise LapsumError(f"{name} must be {w.dtype} [rows, {width}]")
+    x, _, _, stride = _rows(x, name)
+    if stride > MAX_EXPERT_STRIDE:
+        x, stride = x.contiguous(), width
+    return x, stride
+
+
+def _expert_offsets(offsets, w):
+    offsets = _offsets_of(offsets, w.device)
+    if offsets.numel() != w.shape[0] + 1:
+        raise LapsumError(f"offsets must have {w.shape[0] + 1} elements for {w.shape[0]} experts")
+    return offsets
+
+
+def expert_product_forward(xs, w, offsets, *, out=None):
+    """ys [rows, outputs]: rows in expert order times their expert's matrix, ys[r] = xs[r] @ w[e] for the rows
+    offsets[e]:offsets[e + 1].  w [experts, inputs, outputs] bf16 or fp16, stored so or with inputs and outputs changed
+    over (a transposed view).  Rows of no expert give 0."""
+    if _native is not None and out is None:
+        done = _native.expert_product_forward(xs, w, offsets)
+        if done is not None:
+            return done
+    _gpu(w, "w", 3)
+    _dtype(w, "w", (BF16, F16))
+    xs, stride = _expert_rows(xs, "xs", w, w.shape[1])
+    offsets = _expert_offsets(offsets, w)
+    ys = _out(out, "ys", w.dtype, (xs.shape[0], w.shape[2]), w.device)
+    if ys.numel() == 0 or w.shape[1] == 0:
+        return ys.zero_()
+    w, experts = _matrices(w, "w")
+    _call(w.device, "lapsum_expert_product_forward", xs.data_ptr(), stride, xs.shape[0], experts, offsets.data_ptr(),
+          ys.data_ptr())
+    _written(out)
+    return ys
+
+
+def expert_product_backward_rows(dys, w, offsets, *, out=None):
+    """dxs [rows, inputs]: dxs[r] = dys[r] @ w[e].T."""
+    if _native is not None and out is None:
+        done = _native.expert_product_backward_rows(dys, w, offsets)
+        if done is not None:
+            return done
+    _gpu(w, "w", 3)
+    _dtype(w, "w", (BF16, F16))
+    dys, stride = _expert_rows(dys, "dys", w, w.shape[2])
+    offsets = _expert_offsets(offsets, w)
+    dxs = _out(out, "dxs", w.dtype, (dys.shape[0], w.shape[1]), w.device)
+    if dxs.numel() == 0 or w.shape[2] == 0:
+        return dxs.zero_()
+    w, experts = _matrices(w, "w")
+    _call(w.device, "lapsum_expert_product_backward_rows", dys.data_ptr(), stride, dys.shape[0], experts,
+          offsets.data_ptr(), dxs.data_ptr())
+    _written(out)
+    return dxs
+
+
+def expert_product_backward_weights(dys, xs, w, offsets, *, out=None):
+    """dw [experts, inputs, outputs]: dw[e] = xs[rows of e].T @ dys[rows of e], of w's type and stored as w is (w's
+    values are not read).  out: a tensor stored [inputs, outputs] or [outputs, inputs]."""
+    if _native is not None and out is None:
+        done = _native.expert_product_backward_weights(dys, xs, w, offsets)
+        if done is not None:
+            return done
+    _gpu(w, "w", 3)
+    _dtype(w, "w", (BF16, F16))
+    xs, xs_stride = _expert_rows(xs, "xs", w, w.shape[1])
+    dys, dys_stride = _expert_rows(dys, "dys", w, w.shape[2])
+    if xs.shape[0] != dys.shape[0]:
+        raise LapsumError("xs and dys must have the same rows")
+    offsets = _expert_offsets(offsets, w)
+    if out is None:
+        n, m = w.shape[1:]
+        swapped = w.stride(1) == 1 and w.stride(2) != 1 and n > 1
+        dw = torch.empty((w.shape[0], m, n) if swapped else w.shape, dtype=w.dtype, device=w.device)
+        dw = dw.transpose(1, 2) if swapped else dw
+    else:
+        dw = _gpu(out, "dw", 3, w.device)
+        if dw.dtype != w.dtype or dw.shape != w.shape:
+            raise LapsumError(f"dw must be {w.dtype} {list(w.shape)}")
+    if dw.numel() == 0 or xs.shape[0] == 0:
+        return dw.zero_()
+    same, experts = _matrices(dw, "dw")
+    if same is not dw:
+        raise LapsumError("dw must be stored [inputs, outputs] or [outputs, inputs]")
+    _call(w.device, "lapsum_expert_product_backward_weights", xs.data_ptr(), xs_stride, dys.data_ptr(), dys_stride,
+          xs.shape[0], offsets.data_ptr(), experts)
+    _written(out)
+    return dw
+
+
+def expert_product_backward(dys, xs, w, offsets, *, out=None):
+    """dxs [rows, inputs] and dw [experts, inputs, outputs]: the gradients of expert_product_forward."""
+    dxs, dw = (None, None) if out is None else out
+    return (expert_product_backward_rows(dys, w, offsets, out=dxs),
+            expert_product_backward_weights(dys, xs, w, offsets, out=dw))
+
+
+def expert_product(xs, w, offsets):
+    """Differentiable expert_product_forward: gradients reach the rows and the matrices."""
+    _gpu(xs, "xs", 2)
+    return _differentiable()[3].apply(xs, w, offsets)
+
+
 # ---------------------------------------------------------- differentiable
 @functools.lru_cache(maxsize=None)
 def _differentiable():
-    """The autograd functions of route, dispatch and combine, made once torch is bound (a class made by each call takes
+    """The autograd functions of route, dispatch, combine and the experts' products, made once torch is bound (a class made by each call takes
     longer than the call, and as a cycle keeps what it closes over until the collector runs)."""
     once = torch.autograd.function.once_differentiable
 
@@ -449,7 +597,22 @@ def _differentiable():
             ys, weights, slot, offsets = ctx.saved_tensors
             return (*combine_backward(dy, ys, slot, weights, offsets), None, None)
 
-    return Route, Dispatch, Combine
+    class ExpertProduct(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, xs, w, offsets):
+            ys = expert_product_forward(xs, w, offsets)
+            ctx.save_for_backward(xs, w, offsets)
+            return ys
+
+        @staticmethod
+        @once
+        def backward(ctx, dys):
+            xs, w, offsets = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            return (expert_product_backward_rows(dys, w, offsets) if need[0] else None,
+                    expert_product_backward_weights(dys, xs, w, offsets) if need[1] else None, None)
+
+    return Route, Dispatch, Combine, ExpertProduct
 
 
 # ------------------------------------------------------------------ cache
@@ -568,3 +731,85 @@ def cache_evict(k, v, account, positions, lengths, keep, *, next_position=None, 
     _written(k, v, account_out, positions_out)
     del ws
     return kept, lengths_out
+
+
+def cache_reorder(k, v, parents, lengths, account=None, positions=None):
+    """The caches of a beam search follow its beams: with parents int32 [searches, beams] (of beam_select), cache
+    b * beams + j becomes what b * beams + parents[b, j] was, in place: keys and values [searches * beams, heads,
+    capacity, width], account and positions [searches * beams, heads, capacity], the entries below the parent's length.
+    A parent outside the beams (-1) leaves its cache as it is, with length 0.
+
+    Returns the new lengths (a new tensor)."""
+    if _native is not None:
+        done = _native.cache_reorder(k, v, parents, lengths, account, positions)
+        if done is not None:
+            return done
+    cache = _cache_of(k, v)
+    dev, shape = k.device, k.shape[:3]
+    _gpu(parents, "parents", 2, dev)
+    searches, beams = parents.shape
+    if searches * beams != shape[0] or beams > MAX_BEAMS:
+        raise LapsumError(f"parents must be [searches, beams] of the {shape[0]} caches, {MAX_BEAMS} beams at most")
+    parents = _array(parents, "parents", torch.int32, parents.shape, dev)
+    lengths = _array(lengths, "lengths", torch.int32, (shape[0],), dev)
+    # written in place: they have to be usable as they are
+    if account is not None:
+        account = _out(account, "account", torch.float32, shape, dev)
+    if positions is not None:
+        positions = _out(positions, "positions", torch.int32, shape, dev)
+    after = torch.empty_like(lengths)
+    if k.numel() == 0:
+        there = (parents >= 0) & (parents < beams)
+        return torch.where(there, lengths.view(searches, beams).clamp(0, shape[2]).gather(
+            1, parents.long().clamp(0, max(beams - 1, 0))), 0).flatten() if shape[0] else after
+    _call(dev, "lapsum_cache_reorder", cache, beams, parents.data_ptr(), lengths.data_ptr(),
+          None if account is None else account.data_ptr(), None if positions is None else positions.data_ptr(),
+          after.data_ptr())
+    _written(k, v, account, positions)
+    return after
+
+
+# ------------------------------------------------------------ beam search
+@functools.lru_cache(maxsize=1024)
+def _beam_bytes(batch, beams, vocab, k):
+    return int(load_library().lapsum_beam_select_workspace_bytes(batch, beams, vocab, k))
+
+
+def beam_select(logits, scores, k=None, *, ended=None, end_token=None):
+    """scores fp32, parents int32 and tokens int32, all [batch, k]: the k best continuations of each search, over its
+    beams and the vocabulary, by scores[b, i] + log_softmax(logits[b, i])[token], in descending order (equal ones by
+    beam, then token).  logits [batch, beams, vocab] fp32, bf16 or fp16; scores fp32 [batch, beams], the beams' log
+    probabilities (-inf: no beam); k: the number of beams by default.  ended: bool [batch, beams], beams that offer
+    end_token alone, at their own score.  Places that no continuation is left for hold -inf, -1 and -1.  No gradient."""
+    if _native is not None:
+        done = _native.beam_select(logits, scores, k, ended, end_token)
+        if done is not None:
+            return done
+    code = _dtype(_gpu(logits, "logits", 3), "logits")
+    batch, beams, vocab = logits.shape
+    dev = logits.device
+    k = _size(beams if k is None else k, "k", MAX_BEAMS)
+    if beams < 1 or vocab < 1:
+        raise LapsumError("logits must hold at least one beam and one token")
+    scores = _array(scores, "scores", torch.float32, (batch, beams), dev)
+    if ended is not None:
+        ended = _array(ended, "ended", torch.bool, (batch, beams), dev)
+        if end_token is None or not 0 <= int(end_token) < vocab:
+            raise LapsumError("ended beams need an end_token of the vocabulary")
+    # rows at one distance, whatever it is; others are copied
+    sb, si, sv = logits.stride()
+    if (sv != 1 and vocab > 1) or (beams > 1 and si < vocab) or (batch > 1 and sb != (si if beams > 1 else sb) * beams) \
+            or (beams == 1 and batch > 1 and sb < vocab):
+        logits = logits.contiguous()
+        sb, si = beams * vocab, vocab
+    stride = si if beams > 1 else (sb if batch > 1 else vocab)
+    out = (torch.empty((batch, k), dtype=torch.float32, device=dev),
+           torch.empty((batch, k), dtype=torch.int32, device=dev), torch.empty((batch, k), dtype=torch.int32, device=dev))
+    if batch == 0:
+        return out
+    ws, wptr, wlen = _workspace(_beam_bytes(batch, beams, vocab, k), dev)
+    _call(dev, "lapsum_beam_select", logits.data_ptr(), code, batch, beams, vocab, stride, scores.data_ptr(),
+          None if ended is None else ended.data_ptr(), 0 if ended is None else int(end_token), k, out[0].data_ptr(),
+          out[1].data_ptr(), out[2].data_ptr(), wptr, wlen)
+    del ws
+    return out
