@@ -36,10 +36,10 @@ struct RowTile {
   int expert;      // -1: no expert's
   int first, end;  // rows of the tile
 };
-// The index-th of the tiles of `size` rows; every wave finds it by itself.  False: there are no more.
-LDEV bool find_rows(const ProductArgs &p, int size, int index, RowTile &t) {
+// The tiles of `size` rows up to and with this lane's ranges; every wave counts them by itself.
+LDEV int count_row_tiles(const ProductArgs &p, int size, int &mine) {
   const int lane = lane_id(), ranges = p.experts + 2, per = (ranges + 63) / 64;
-  int mine = 0;
+  mine = 0;
   for (int i = 0; i < per; ++i) {
     const int g = lane * per + i;
     if (g >= ranges) break;
@@ -52,6 +52,11 @@ LDEV bool find_rows(const ProductArgs &p, int size, int index, RowTile &t) {
     const int x = __shfl_up(upto, d, 64);
     if (lane >= d) upto += x;
   }
+  return upto;
+}
+// The index-th of them.  False: there are no more.
+LDEV bool find_row_tile(const ProductArgs &p, int size, int index, int upto, int mine, RowTile &t) {
+  const int ranges = p.experts + 2, per = (ranges + 63) / 64;
   if (index >= read_lane(upto, 63)) return false;
   const int at = __builtin_ctzll(__ballot(upto > index));
   int left = index - read_lane(upto - mine, at);
@@ -95,7 +100,9 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
     k1 = offset_of(p, e + 1);
   } else {
     RowTile t;
-    if (grid_row() > 0x7FFFFFFF || !find_rows(p, kAny, (int)grid_row(), t)) return;
+    int mine;
+    const int upto = count_row_tiles(p, kAny, mine);
+    if (!find_row_tile(p, kAny, (int)grid_row(), upto, mine, t)) return;
     e = t.expert;
     m0 = t.first;
     m1 = t.end;
@@ -139,14 +146,275 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
   }
 }
 
+// ------------------------------------------------------------- 16 bytes at a time
+// A window of memory that loads are held to: what lies past its end reads as zero.
+using window_t = __amdgpu_buffer_rsrc_t;
+LDEV window_t window_of(const void *first, int64_t bytes) {
+  const int64_t most = 0x7FFFFFF0;
+  bytes = bytes < 0 ? 0 : (bytes < most ? bytes : most);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
+
+// 64 x 16 bytes from the lanes' offsets to consecutive places of LDS from `to` on (bytes).  Written out, since the compiler
+// would have every later read of LDS wait for it; whoever reads waits by arrived().
+LDEV void load_to_lds(window_t w, uint32_t to, uint32_t offset) {
+  uint32_t m0;  // the compiler's; the place goes there
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(to), "v"(offset), "s"(w)
+               : "memory");
+}
+LDEV uint32_t lds_at(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+constexpr int kDepth = 64;  // of a step: elements of the sum
+
+// One factor's side of a tile: SIZE places along C by kDepth of the sum, in LDS, brought there by WAVES waves.
+//
+// NEXT: the sum's elements lie next to each other in memory.  Places are rows of 128 bytes, whose 16-byte chunks
+// change places by the row (SHIFT says by which of its bits), so that lanes that read one chunk of several rows
+// use different banks.
+// Otherwise places lie next to each other: LDS holds kDepth rows of SIZE.
+template <class T, int SIZE, bool NEXT, int WAVES, int SHIFT>
+struct Side {
+  static constexpr int kLoads = SIZE * kDepth * 2 / 1024 / WAVES;
+  const char *at;     // of the step
+  int64_t advance, bytes;  // per step; of the window from `at`
+  uint32_t offset[kLoads];
+  int chunk;          // NEXT: the lane's chunk of the step's sum (of even loads; odd ones have it ^ 4 where SHIFT is 3)
+
+  // first: the element at the tile's first place and the sum's first element; `stride` between rows of memory;
+  // `places` of the tile and `sum` elements are there
+  LDEV void start(const T *first, int64_t stride, int64_t places, int64_t sum) {
+    const int lane = lane_id(), wave = threadIdx.x / 64;
+    at = reinterpret_cast<const char *>(first);
+    if (NEXT) {
+      advance = kDepth * 2;
+      bytes = ((places - 1) * stride + sum) * 2;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = (i * WAVES + wave) * 8 + lane / 8;
+        offset[i] = (uint32_t)(row * stride * 2) + (uint32_t)(((lane % 8) ^ ((row >> SHIFT) & 7)) * 16);
+      }
+      chunk = (lane % 8) ^ (((wave * 8 + lane / 8) >> SHIFT) & 7);
+    } else {
+      constexpr int kPer = SIZE / 8;  // chunks of a row
+      advance = kDepth * stride * 2;
+      bytes = ((sum - 1) * stride + places) * 2;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int x = (i * WAVES + wave) * 64 + lane;
+        offset[i] = (uint32_t)(x / kPer * stride * 2) + (uint32_t)(x % kPer * 16);
+      }
+    }
+  }
+  // the step's part, of which `left` elements of the sum are there, to LDS
+  LDEV void load(uint32_t lds, int left) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const window_t w = window_of(at, bytes);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint32_t o = offset[i];
+      if (NEXT) {
+        const int c = SHIFT == 3 && (i * WAVES) % 8 != 0 ? chunk ^ ((i * WAVES) & 7) : chunk;
+        o |= c * 8 < left ? 0u : kNowhere;
+      }
+      load_to_lds(w, lds + (i * WAVES + wave) * 1024, o);
+    }
+    at += advance;
+    bytes -= advance;
+  }
+};
+
+// two 16-bit elements, the low or the high ones of two words
+LDEV uint32_t pair_low(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+LDEV uint32_t pair_high(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// Operands of matrix instructions for 128 places (first + 8 * lane % 16 + i for operand i) and the half `h` of a step, from
+// rows of places: eight rows of the sum by eight places a lane, turned over in registers.
+template <class T, int SIZE>
+LDEV void turned(const T *lds, int first, int h, pack_t<T> (&f)[8]) {
+  const int lane = lane_id();
+  const T *p = lds + (h * 32 + lane / 16 * 8) * SIZE + first + lane % 16 * 8;
+  uint4 w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4 *>(p + j * SIZE);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t *a = reinterpret_cast<const uint32_t *>(&w[2 * j]), *b = reinterpret_cast<const uint32_t *>(&w[2 * j + 1]);
+      d[j] = i % 2 == 0 ? pair_low(a[i / 2], b[i / 2]) : pair_high(a[i / 2], b[i / 2]);
+    }
+    f[i] = __builtin_bit_cast(pack_t<T>, uint4{d[0], d[1], d[2], d[3]});
+  }
+}
+
+template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT>
+struct Tile {
+  static constexpr int kWaves = WAVES_M * WAVES_N, kM = WM * WAVES_M, kN = 128 * WAVES_N, kFrags = WM / 16;
+  using A = Side<T, kM, A_NEXT, kWaves, 0>;
+  using B = Side<T, kN, B_NEXT, kWaves, 3>;
+  f32x4 c[kFrags][8];
+
+  LDEV void step(const T *la, const T *lb) {
+    const int lane = lane_id(), wave = threadIdx.x / 64, wm = wave / WAVES_N, wn = wave % WAVES_N;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      pack_t<T> fa[kFrags], fb[8];
+      if constexpr (A_NEXT) {
+        const T *p = la + (wm * WM + lane % 16) * kDepth + (((h * 4 + lane / 16) ^ (lane % 8)) * 8);
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i) fa[i] = load_pack(p + i * 16 * kDepth);
+      } else {
+        turned<T, kM>(la, wm * WM, h, fa);
+      }
+      if constexpr (B_NEXT) {
+        const T *p = lb + (wn * 128 + lane % 16 * 8) * kDepth + (((h * 4 + lane / 16) ^ (lane % 8)) * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) fb[i] = load_pack(p + i * kDepth);
+      } else {
+        turned<T, kN>(lb, wn * 128, h, fb);
+      }
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[i][j] = mfma(fa[i], fb[j], c[i][j]);
+    }
+  }
+  // places [0, m) x [0, n) of the tile
+  LDEV void store(T *out, int64_t stride, int m, int n) const {
+    const int lane = lane_id(), wave = threadIdx.x / 64, wm = wave / WAVES_N, wn = wave % WAVES_N;
+    const int col = wn * 128 + lane % 16 * 8;
+    if (col >= n) return;
+#pragma unroll
+    for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int in = lane / 16 * 4 + r, row = wm * WM + (A_NEXT ? i * 16 + in : in * 8 + i);
+        pack_t<T> v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (T)c[i][j][r];
+        if (row < m) store_pack(out + row * stride + col, v);
+      }
+  }
+};
+
+LDEV void arrived() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+// Workgroups go round the eight dies; each die takes a run of tiles that share factors.
+LDEV int64_t tile_of_workgroup(int64_t total) {
+  const int64_t each = (total + 7) / 8, i = blockIdx.x;
+  const int64_t t = i % 8 * each + i / 8;
+  return i / 8 < each && t < total ? t : -1;
+}
+
+template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
+__global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 1) void product_tile_kernel(ProductArgs p) {
+  using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
+  constexpr int kA = Work::kM * kDepth, kStage = kA + Work::kN * kDepth;
+  __shared__ T lds[2 * kStage];
+  lds_poison(lds);
+  const int tiles_n = (p.n + Work::kN - 1) / Work::kN;
+  const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
+  T *out = static_cast<T *>(p.c);
+  int m, n0, sum;  // places of the tile, its first column, elements of the sum
+  if constexpr (SUM_ROWS) {
+    const int tiles_m = (p.m + Work::kM - 1) / Work::kM;
+    const int64_t t = tile_of_workgroup((int64_t)tiles_m * tiles_n * p.experts);
+    if (t < 0) return;
+    const int e = (int)(t / (tiles_m * tiles_n)), in = (int)(t % (tiles_m * tiles_n)), m0 = in % tiles_m * Work::kM;
+    n0 = in / tiles_m * Work::kN;
+    const int k0 = offset_of(p, e), k1 = offset_of(p, e + 1);
+    sum = k1 - k0;
+    m = p.m - m0;
+    a += k0 * p.ak + m0;
+    b += k0 * p.bk + n0;
+    out += e * p.ce + m0 * p.cm + n0;
+  } else {
+    int mine;
+    const int upto = count_row_tiles(p, Work::kM, mine), rows = read_lane(upto, 63);
+    const int64_t t = tile_of_workgroup((int64_t)rows * tiles_n);
+    if (t < 0) return;
+    // kGroup tiles of rows go through the columns together, so that each column of a matrix is read once for them
+    constexpr int kGroup = 8;
+    const int64_t group = t / (kGroup * tiles_n);
+    const int first = (int)group * kGroup, g = rows - first < kGroup ? rows - first : kGroup;
+    const int in = (int)(t - group * kGroup * tiles_n);
+    RowTile r;
+    if (!find_row_tile(p, Work::kM, first + in % g, upto, mine, r)) return;
+    n0 = in / g * Work::kN;
+    m = r.end - r.first;
+    sum = r.expert < 0 ? 0 : p.k;
+    a += r.first * p.am;
+    b += (r.expert < 0 ? 0 : r.expert) * p.be + n0 * p.bn;
+    out += r.first * p.cm + n0;
+  }
+  const int n = p.n - n0;
+  Work w;
+#pragma unroll
+  for (int i = 0; i < Work::kFrags; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w.c[i][j] = f32x4{};
+  if (sum > 0) {
+    typename Work::A sa;
+    typename Work::B sb;
+    sa.start(a, A_NEXT ? p.am : p.ak, m < Work::kM ? m : Work::kM, sum);
+    sb.start(b, B_NEXT ? p.bn : p.bk, n < Work::kN ? n : Work::kN, sum);
+    const uint32_t at = lds_at(lds);
+    sa.load(at, sum);
+    sb.load(at + kA * 2, sum);
+    int stage = 0;
+#pragma unroll 1
+    for (; sum > 0; sum -= kDepth) {
+      arrived();
+      const T *now = lds + stage;
+      stage = kStage - stage;
+      if (sum > kDepth) {
+        sa.load(at + stage * 2, sum - kDepth);
+        sb.load(at + (stage + kA) * 2, sum - kDepth);
+      }
+      w.step(now, now + kA);
+    }
+  }
+  w.store(out, p.cm, m, n);
+}
+
+template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
+hipError_t tiles(const ProductArgs &p, hipStream_t s) {
+  using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
+  const int64_t nt = (p.n + Work::kN - 1) / Work::kN;
+  const int64_t mt = SUM_ROWS ? (int64_t)((p.m + Work::kM - 1) / Work::kM) * p.experts : most_row_tiles(p, Work::kM);
+  const int64_t groups = (nt * mt + 7) / 8 * 8;
+  if (groups > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+  product_tile_kernel<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT, SUM_ROWS>
+      <<<dim3((unsigned)groups), dim3(64 * WAVES_M * WAVES_N), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+bool whole(const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; }
+bool whole(int64_t n) { return n % 8 == 0; }
+
 template <class T>
 hipError_t rows_of(const ProductArgs &p, hipStream_t s) {
+  if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.am) && whole(p.be) && whole(p.bk == 1 ? p.bn : p.bk) &&
+      whole(p.cm) && whole(p.n) && whole(p.k))
+    return p.bk == 1 ? tiles<T, 128, 2, 2, true, true, false>(p, s) : tiles<T, 128, 2, 2, true, false, false>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   product_any_kernel<T, false><<<rows_grid(nt, most_row_tiles(p, kAny)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
 template <class T>
 hipError_t weights_of(const ProductArgs &p, hipStream_t s) {
+  if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.ak) && whole(p.bk) && whole(p.ce) && whole(p.cm) &&
+      whole(p.m) && whole(p.n))
+    return tiles<T, 128, 2, 2, false, false, true>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   const int64_t mt = (p.m + kAny - 1) / kAny;
   product_any_kernel<T, true><<<rows_grid(nt, mt * p.experts), dim3(256), 0, s>>>(p);
