@@ -169,21 +169,23 @@ LDEV uint32_t lds_at(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
 }
 
-constexpr int kDepth = 64;  // of a step: elements of the sum
+constexpr int kDepth = 32;  // of a step: elements of the sum
+constexpr int kStages = 4;
 
 // One factor's side of a tile: SIZE places along C by kDepth of the sum, in LDS, brought there by WAVES waves.
 //
-// NEXT: the sum's elements lie next to each other in memory.  Places are rows of 128 bytes, whose 16-byte chunks
-// change places by the row (SHIFT says by which of its bits), so that lanes that read one chunk of several rows
-// use different banks.
+// NEXT: the sum's elements lie next to each other in memory.  LDS holds rows of one place, 64 bytes, whose 16-byte
+// chunks change places by the row, so that eight lanes that read one chunk of neighbouring rows meet all
+// banks.  SPREAD: rows 16 i + j hold places 8 j + i of each 128, so that what a lane reads from rows 16 apart are
+// neighbouring places.
 // Otherwise places lie next to each other: LDS holds kDepth rows of SIZE.
-template <class T, int SIZE, bool NEXT, int WAVES, int SHIFT>
+template <class T, int SIZE, bool NEXT, bool SPREAD, int WAVES>
 struct Side {
   static constexpr int kLoads = SIZE * kDepth * 2 / 1024 / WAVES;
-  const char *at;     // of the step
+  const char *at;          // of the step
   int64_t advance, bytes;  // per step; of the window from `at`
   uint32_t offset[kLoads];
-  int chunk;          // NEXT: the lane's chunk of the step's sum (of even loads; odd ones have it ^ 4 where SHIFT is 3)
+  int chunk;               // NEXT: the lane's chunk of the step's sum
 
   // first: the element at the tile's first place and the sum's first element; `stride` between rows of memory;
   // `places` of the tile and `sum` elements are there
@@ -193,12 +195,13 @@ struct Side {
     if (NEXT) {
       advance = kDepth * 2;
       bytes = ((places - 1) * stride + sum) * 2;
+      chunk = lane % 4 ^ (lane / 8 & 3);  // the same for all loads: their rows are 16 apart
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int row = (i * WAVES + wave) * 8 + lane / 8;
-        offset[i] = (uint32_t)(row * stride * 2) + (uint32_t)(((lane % 8) ^ ((row >> SHIFT) & 7)) * 16);
+        const int row = (i * WAVES + wave) * 16 + lane / 4;
+        const int place = SPREAD ? row / 128 * 128 + row % 16 * 8 + row / 16 % 8 : row;
+        offset[i] = (uint32_t)(place * stride * 2) + (uint32_t)(chunk * 16);
       }
-      chunk = (lane % 8) ^ (((wave * 8 + lane / 8) >> SHIFT) & 7);
     } else {
       constexpr int kPer = SIZE / 8;  // chunks of a row
       advance = kDepth * stride * 2;
@@ -210,19 +213,13 @@ struct Side {
       }
     }
   }
-  // the step's part, of which `left` elements of the sum are there, to LDS
+  // the step's part, of which `left` elements of the sum are there (none or fewer: zeros), to LDS
   LDEV void load(uint32_t lds, int left) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const window_t w = window_of(at, bytes);
+    const uint32_t none = NEXT && chunk * 8 >= left ? kNowhere : 0u;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      uint32_t o = offset[i];
-      if (NEXT) {
-        const int c = SHIFT == 3 && (i * WAVES) % 8 != 0 ? chunk ^ ((i * WAVES) & 7) : chunk;
-        o |= c * 8 < left ? 0u : kNowhere;
-      }
-      load_to_lds(w, lds + (i * WAVES + wave) * 1024, o);
-    }
+    for (int i = 0; i < kLoads; ++i) load_to_lds(w, lds + (i * WAVES + wave) * 1024, offset[i] | none);
     at += advance;
     bytes -= advance;
   }
@@ -232,57 +229,69 @@ struct Side {
 LDEV uint32_t pair_low(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 LDEV uint32_t pair_high(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
-// Operands of matrix instructions for 128 places (first + 8 * lane % 16 + i for operand i) and the half `h` of a step, from
-// rows of places: eight rows of the sum by eight places a lane, turned over in registers.
-template <class T, int SIZE>
-LDEV void turned(const T *lds, int first, int h, pack_t<T> (&f)[8]) {
-  const int lane = lane_id();
-  const T *p = lds + (h * 32 + lane / 16 * 8) * SIZE + first + lane % 16 * 8;
-  uint4 w[8];
+// What a lane holds of one side's step for N matrix instructions: with NEXT the operands themselves (SPREAD or not, by
+// what LDS holds); otherwise eight rows of the sum by N neighbouring places (first + N * lane % 16 + i for
+// operand i), which operand() turns over.
+template <class T, int SIZE, bool NEXT, int N>
+struct Held {
+  static constexpr int kWords = N / 2;  // of N places
+  uint32_t w[NEXT ? N : 8][NEXT ? 4 : kWords];
+  LDEV void read(const T *lds, int first) {
+    const int lane = lane_id();
+    if constexpr (NEXT) {
+      const T *p = lds + (first + lane % 16) * kDepth + ((lane / 16) ^ (lane / 2 & 3)) * 8;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint4 *>(p + j * SIZE);
+      for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(w[i]) = *reinterpret_cast<const uint4 *>(p + i * 16 * kDepth);
+    } else {
+      const T *p = lds + lane / 16 * 8 * SIZE + first + lane % 16 * N;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (N == 8)
+          *reinterpret_cast<uint4 *>(w[i]) = *reinterpret_cast<const uint4 *>(p + i * SIZE);
+        else
+          *reinterpret_cast<uint2 *>(w[i]) = *reinterpret_cast<const uint2 *>(p + i * SIZE);
+      }
+    }
+  }
+  LDEV pack_t<T> operand(int i) const {
     uint32_t d[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t *a = reinterpret_cast<const uint32_t *>(&w[2 * j]), *b = reinterpret_cast<const uint32_t *>(&w[2 * j + 1]);
-      d[j] = i % 2 == 0 ? pair_low(a[i / 2], b[i / 2]) : pair_high(a[i / 2], b[i / 2]);
+      if constexpr (NEXT)
+        d[j] = w[i][j];
+      else
+        d[j] = i % 2 == 0 ? pair_low(w[2 * j][i / 2], w[2 * j + 1][i / 2]) : pair_high(w[2 * j][i / 2], w[2 * j + 1][i / 2]);
     }
-    f[i] = __builtin_bit_cast(pack_t<T>, uint4{d[0], d[1], d[2], d[3]});
+    return __builtin_bit_cast(pack_t<T>, uint4{d[0], d[1], d[2], d[3]});
   }
-}
+};
 
 template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT>
 struct Tile {
   static constexpr int kWaves = WAVES_M * WAVES_N, kM = WM * WAVES_M, kN = 128 * WAVES_N, kFrags = WM / 16;
-  using A = Side<T, kM, A_NEXT, kWaves, 0>;
-  using B = Side<T, kN, B_NEXT, kWaves, 3>;
+  using A = Side<T, kM, A_NEXT, false, kWaves>;
+  using B = Side<T, kN, B_NEXT, true, kWaves>;
+  static constexpr int kLoads = A::kLoads + B::kLoads;  // of a wave and step
+  struct Operands {
+    Held<T, kM, A_NEXT, kFrags> a;
+    Held<T, kN, B_NEXT, 8> b;
+    LDEV void read(const T *la, const T *lb) {
+      const int wave = threadIdx.x / 64;
+      a.read(la, wave / WAVES_N * WM);
+      b.read(lb, wave % WAVES_N * 128);
+    }
+  };
   f32x4 c[kFrags][8];
 
-  LDEV void step(const T *la, const T *lb) {
-    const int lane = lane_id(), wave = threadIdx.x / 64, wm = wave / WAVES_N, wn = wave % WAVES_N;
+  LDEV void step(const Operands &x) {
+    pack_t<T> fa[kFrags];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      pack_t<T> fa[kFrags], fb[8];
-      if constexpr (A_NEXT) {
-        const T *p = la + (wm * WM + lane % 16) * kDepth + (((h * 4 + lane / 16) ^ (lane % 8)) * 8);
+    for (int i = 0; i < kFrags; ++i) fa[i] = x.a.operand(i);
 #pragma unroll
-        for (int i = 0; i < kFrags; ++i) fa[i] = load_pack(p + i * 16 * kDepth);
-      } else {
-        turned<T, kM>(la, wm * WM, h, fa);
-      }
-      if constexpr (B_NEXT) {
-        const T *p = lb + (wn * 128 + lane % 16 * 8) * kDepth + (((h * 4 + lane / 16) ^ (lane % 8)) * 8);
+    for (int j = 0; j < 8; ++j) {
+      const pack_t<T> fb = x.b.operand(j);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) fb[i] = load_pack(p + i * kDepth);
-      } else {
-        turned<T, kN>(lb, wn * 128, h, fb);
-      }
-#pragma unroll
-      for (int i = 0; i < kFrags; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[i][j] = mfma(fa[i], fb[j], c[i][j]);
+      for (int i = 0; i < kFrags; ++i) c[i][j] = mfma(fa[i], fb, c[i][j]);
     }
   }
   // places [0, m) x [0, n) of the tile
@@ -294,7 +303,7 @@ struct Tile {
     for (int i = 0; i < kFrags; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int in = lane / 16 * 4 + r, row = wm * WM + (A_NEXT ? i * 16 + in : in * 8 + i);
+        const int in = lane / 16 * 4 + r, row = wm * WM + (A_NEXT ? i * 16 + in : in * kFrags + i);
         pack_t<T> v;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = (T)c[i][j][r];
@@ -303,9 +312,10 @@ struct Tile {
   }
 };
 
+// All but the last LOADS loads to LDS of every wave are there, and what every wave has read from LDS is in its registers.
+template <int LOADS>
 LDEV void arrived() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
 }
 
 // Workgroups go round the eight dies; each die takes a run of tiles that share factors.
@@ -316,10 +326,10 @@ LDEV int64_t tile_of_workgroup(int64_t total) {
 }
 
 template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
-__global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 1) void product_tile_kernel(ProductArgs p) {
+__global__ __launch_bounds__(64 * WAVES_M *WAVES_N, WAVES_M *WAVES_N / 4) void product_tile_kernel(ProductArgs p) {
   using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
   constexpr int kA = Work::kM * kDepth, kStage = kA + Work::kN * kDepth;
-  __shared__ T lds[2 * kStage];
+  __shared__ T lds[kStages * kStage];
   lds_poison(lds);
   const int tiles_n = (p.n + Work::kN - 1) / Work::kN;
   const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
@@ -368,20 +378,40 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 1) void product_tile_kernel(
     sa.start(a, A_NEXT ? p.am : p.ak, m < Work::kM ? m : Work::kM, sum);
     sb.start(b, B_NEXT ? p.bn : p.bk, n < Work::kN ? n : Work::kN, sum);
     const uint32_t at = lds_at(lds);
-    sa.load(at, sum);
-    sb.load(at + kA * 2, sum);
-    int stage = 0;
-#pragma unroll 1
-    for (; sum > 0; sum -= kDepth) {
-      arrived();
-      const T *now = lds + stage;
-      stage = kStage - stage;
-      if (sum > kDepth) {
-        sa.load(at + stage * 2, sum - kDepth);
-        sb.load(at + (stage + kA) * 2, sum - kDepth);
+    // Step t computes on what the step before has read from LDS, reads what the next one computes on, and asks for
+    // what is kStages steps away, whose place step t's own part has left.  Past the end zeros are asked for, so that
+    // as many loads are under way in every step.
+    int to = 0, from = 0, asked = sum;
+    const auto load = [&] {
+      sa.load(at + to * 2, asked);
+      sb.load(at + (to + kA) * 2, asked);
+      asked -= kDepth;
+      to = to == (kStages - 1) * kStage ? 0 : to + kStage;
+    };
+    const auto step = [&](const typename Work::Operands &now, typename Work::Operands &next) {
+      arrived<(kStages - 2) * Work::kLoads>();
+      load();
+      from = from == (kStages - 1) * kStage ? 0 : from + kStage;
+      next.read(lds + from, lds + from + kA);
+      w.step(now);
+#pragma unroll
+      for (int i = 0; i < 8 + Work::kFrags; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read of LDS,
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // then matrix instructions
       }
-      w.step(now, now + kA);
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) load();
+    typename Work::Operands x, y;
+    arrived<(kStages - 1) * Work::kLoads>();
+    x.read(lds, lds + kA);
+#pragma unroll 1
+    for (; sum > 0; sum -= 2 * kDepth) {
+      step(x, y);
+      step(y, x);
     }
+    // no load may reach LDS that is another workgroup's
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
   w.store(out, p.cm, m, n);
 }
@@ -405,7 +435,7 @@ template <class T>
 hipError_t rows_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.am) && whole(p.be) && whole(p.bk == 1 ? p.bn : p.bk) &&
       whole(p.cm) && whole(p.n) && whole(p.k))
-    return p.bk == 1 ? tiles<T, 128, 2, 2, true, true, false>(p, s) : tiles<T, 128, 2, 2, true, false, false>(p, s);
+    return p.bk == 1 ? tiles<T, 64, 4, 2, true, true, false>(p, s) : tiles<T, 64, 4, 2, true, false, false>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   product_any_kernel<T, false><<<rows_grid(nt, most_row_tiles(p, kAny)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
@@ -414,7 +444,7 @@ template <class T>
 hipError_t weights_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.ak) && whole(p.bk) && whole(p.ce) && whole(p.cm) &&
       whole(p.m) && whole(p.n))
-    return tiles<T, 128, 2, 2, false, false, true>(p, s);
+    return tiles<T, 64, 4, 2, false, false, true>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   const int64_t mt = (p.m + kAny - 1) / kAny;
   product_any_kernel<T, true><<<rows_grid(nt, mt * p.experts), dim3(256), 0, s>>>(p);
