@@ -147,13 +147,8 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
 }
 
 // ------------------------------------------------------------- 16 bytes at a time
-// A window of memory that loads are held to: what lies past its end reads as zero.
+// A window of memory that loads are held to: what lies past its end reads as zero.  Steps of a tile lie within 2^31 bytes.
 using window_t = __amdgpu_buffer_rsrc_t;
-LDEV window_t window_of(const void *first, int64_t bytes) {
-  const int64_t most = 0x7FFFFFF0;
-  bytes = bytes < 0 ? 0 : (bytes < most ? bytes : most);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(first), 0, (int)bytes, 0x00020000);
-}
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
 
 // 64 x 16 bytes from the lanes' offsets to consecutive places of LDS from `to` on (bytes).  Written out, since the compiler
@@ -182,47 +177,53 @@ constexpr int kStages = 4;
 template <class T, int SIZE, bool NEXT, bool SPREAD, int WAVES>
 struct Side {
   static constexpr int kLoads = SIZE * kDepth * 2 / 1024 / WAVES;
-  const char *at;          // of the step
-  int64_t advance, bytes;  // per step; of the window from `at`
+  const char *at;     // of the step
+  int64_t advance;    // bytes from step to step
+  int whole, rest;    // bytes of the window of a whole step and of the last one, where that is not whole
+  uint32_t to;        // LDS of this wave's first load, of the first stage
   uint32_t offset[kLoads];
-  int chunk;               // NEXT: the lane's chunk of the step's sum
+  int chunk;          // NEXT: the lane's chunk of the step's sum
 
   // first: the element at the tile's first place and the sum's first element; `stride` between rows of memory;
   // `places` of the tile and `sum` elements are there
-  LDEV void start(const T *first, int64_t stride, int64_t places, int64_t sum) {
-    const int lane = lane_id(), wave = threadIdx.x / 64;
+  LDEV void start(const T *first, int64_t stride, int places, int sum, uint32_t lds) {
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     at = reinterpret_cast<const char *>(first);
+    to = lds + wave * 1024;
+    const int left = sum % kDepth, step = (int)stride;
     if (NEXT) {
       advance = kDepth * 2;
-      bytes = ((places - 1) * stride + sum) * 2;
+      whole = ((places - 1) * step + kDepth) * 2;
+      rest = ((places - 1) * step + left) * 2;
       chunk = lane % 4 ^ (lane / 8 & 3);  // the same for all loads: their rows are 16 apart
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int row = (i * WAVES + wave) * 16 + lane / 4;
         const int place = SPREAD ? row / 128 * 128 + row % 16 * 8 + row / 16 % 8 : row;
-        offset[i] = (uint32_t)(place * stride * 2) + (uint32_t)(chunk * 16);
+        offset[i] = (uint32_t)(place * step * 2) + (uint32_t)(chunk * 16);
       }
     } else {
       constexpr int kPer = SIZE / 8;  // chunks of a row
       advance = kDepth * stride * 2;
-      bytes = ((sum - 1) * stride + places) * 2;
+      whole = ((kDepth - 1) * step + places) * 2;
+      rest = ((left - 1) * step + places) * 2;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int x = (i * WAVES + wave) * 64 + lane;
-        offset[i] = (uint32_t)(x / kPer * stride * 2) + (uint32_t)(x % kPer * 16);
+        offset[i] = (uint32_t)(x / kPer * step * 2) + (uint32_t)(x % kPer * 16);
       }
     }
   }
-  // the step's part, of which `left` elements of the sum are there (none or fewer: zeros), to LDS
-  LDEV void load(uint32_t lds, int left) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const window_t w = window_of(at, bytes);
-    const uint32_t none = NEXT && chunk * 8 >= left ? kNowhere : 0u;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load_to_lds(w, lds + (i * WAVES + wave) * 1024, offset[i] | none);
+  // The step's part, of which `left` elements of the sum are there (none or fewer: zeros), to LDS: load `i` of this wave.
+  window_t window;
+  uint32_t none;
+  LDEV void begin(int left) {
+    const int bytes = left >= kDepth ? whole : (left > 0 ? rest : 0);
+    window = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, bytes, 0x00020000);
+    none = NEXT && chunk * 8 >= left ? kNowhere : 0u;
     at += advance;
-    bytes -= advance;
   }
+  LDEV void load(int i, uint32_t stage) const { load_to_lds(window, to + stage + i * (WAVES * 1024), offset[i] | none); }
 };
 
 // two 16-bit elements, the low or the high ones of two words
@@ -234,24 +235,20 @@ LDEV uint32_t pair_high(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b
 // operand i), which operand() turns over.
 template <class T, int SIZE, bool NEXT, int N>
 struct Held {
-  static constexpr int kWords = N / 2;  // of N places
-  uint32_t w[NEXT ? N : 8][NEXT ? 4 : kWords];
-  LDEV void read(const T *lds, int first) {
+  static constexpr int kReads = NEXT ? N : 8;
+  uint32_t w[kReads][NEXT ? 4 : N / 2];
+  // where this lane reads from, in elements from the side's part of a stage
+  LDEV static int place(int first) {
     const int lane = lane_id();
-    if constexpr (NEXT) {
-      const T *p = lds + (first + lane % 16) * kDepth + ((lane / 16) ^ (lane / 2 & 3)) * 8;
-#pragma unroll
-      for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(w[i]) = *reinterpret_cast<const uint4 *>(p + i * 16 * kDepth);
-    } else {
-      const T *p = lds + lane / 16 * 8 * SIZE + first + lane % 16 * N;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (N == 8)
-          *reinterpret_cast<uint4 *>(w[i]) = *reinterpret_cast<const uint4 *>(p + i * SIZE);
-        else
-          *reinterpret_cast<uint2 *>(w[i]) = *reinterpret_cast<const uint2 *>(p + i * SIZE);
-      }
-    }
+    return NEXT ? (first + lane % 16) * kDepth + ((lane / 16) ^ (lane / 2 & 3)) * 8
+                : lane / 16 * 8 * SIZE + first + lane % 16 * N;
+  }
+  LDEV void read(int i, const T *from) {
+    const T *p = from + i * (NEXT ? 16 * kDepth : SIZE);
+    if constexpr (NEXT || N == 8)
+      *reinterpret_cast<uint4 *>(w[i]) = *reinterpret_cast<const uint4 *>(p);
+    else
+      *reinterpret_cast<uint2 *>(w[i]) = *reinterpret_cast<const uint2 *>(p);
   }
   LDEV pack_t<T> operand(int i) const {
     uint32_t d[4];
@@ -275,23 +272,27 @@ struct Tile {
   struct Operands {
     Held<T, kM, A_NEXT, kFrags> a;
     Held<T, kN, B_NEXT, 8> b;
-    LDEV void read(const T *la, const T *lb) {
-      const int wave = threadIdx.x / 64;
-      a.read(la, wave / WAVES_N * WM);
-      b.read(lb, wave % WAVES_N * 128);
-    }
   };
+  static constexpr int kReadsA = decltype(Operands::a)::kReads;
   f32x4 c[kFrags][8];
 
-  LDEV void step(const Operands &x) {
+  // The products of a step, column by column, and between them what `between(j)` does: the columns stay in order, so
+  // that neither loads nor reads of LDS hold up the matrix instructions.
+  template <class F>
+  LDEV void step(const Operands &x, const F &between) {
     pack_t<T> fa[kFrags];
 #pragma unroll
     for (int i = 0; i < kFrags; ++i) fa[i] = x.a.operand(i);
+    pack_t<T> fb = x.b.operand(0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const pack_t<T> fb = x.b.operand(j);
+      between(j);
+      pack_t<T> next = fb;
+      if (j < 7) next = x.b.operand(j + 1);
 #pragma unroll
       for (int i = 0; i < kFrags; ++i) c[i][j] = mfma(fa[i], fb, c[i][j]);
+      fb = next;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   // places [0, m) x [0, n) of the tile
@@ -375,36 +376,57 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, WAVES_M *WAVES_N / 4) void p
   if (sum > 0) {
     typename Work::A sa;
     typename Work::B sb;
-    sa.start(a, A_NEXT ? p.am : p.ak, m < Work::kM ? m : Work::kM, sum);
-    sb.start(b, B_NEXT ? p.bn : p.bk, n < Work::kN ? n : Work::kN, sum);
-    const uint32_t at = lds_at(lds);
+    sa.start(a, A_NEXT ? p.am : p.ak, m < Work::kM ? m : Work::kM, sum, lds_at(lds));
+    sb.start(b, B_NEXT ? p.bn : p.bk, n < Work::kN ? n : Work::kN, sum, lds_at(lds + kA));
     // Step t computes on what the step before has read from LDS, reads what the next one computes on, and asks for
     // what is kStages steps away, whose place step t's own part has left.  Past the end zeros are asked for, so that
     // as many loads are under way in every step.
     int to = 0, from = 0, asked = sum;
-    const auto load = [&] {
-      sa.load(at + to * 2, asked);
-      sb.load(at + (to + kA) * 2, asked);
+    const int wave = threadIdx.x / 64;
+    const int place_a = decltype(Work::Operands::a)::place(wave / WAVES_N * WM);
+    const int place_b = kA + decltype(Work::Operands::b)::place(wave % WAVES_N * 128);
+    const auto begin = [&] {
+      sa.begin(asked);
+      sb.begin(asked);
       asked -= kDepth;
-      to = to == (kStages - 1) * kStage ? 0 : to + kStage;
     };
+    const auto load = [&](int i) {
+      if (i < Work::A::kLoads)
+        sa.load(i, to * 2);
+      else
+        sb.load(i - Work::A::kLoads, to * 2);
+    };
+    const auto after = [&](int stage) { return stage == (kStages - 1) * kStage ? 0 : stage + kStage; };
     const auto step = [&](const typename Work::Operands &now, typename Work::Operands &next) {
       arrived<(kStages - 2) * Work::kLoads>();
-      load();
-      from = from == (kStages - 1) * kStage ? 0 : from + kStage;
-      next.read(lds + from, lds + from + kA);
-      w.step(now);
+      from = after(from);
+      const T *pa = lds + from + place_a, *pb = lds + from + place_b;
+      w.step(now, [&](int j) {
 #pragma unroll
-      for (int i = 0; i < 8 + Work::kFrags; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read of LDS,
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);  // then matrix instructions
-      }
+        for (int i = j * Work::kReadsA / 8; i < (j + 1) * Work::kReadsA / 8; ++i) next.a.read(i, pa);
+        next.b.read(j, pb);
+#pragma unroll
+        for (int i = (j * Work::kLoads + 7) / 8; i < ((j + 1) * Work::kLoads + 7) / 8; ++i) load(i);
+        if (j == 7) {
+          begin();  // the next step's
+          to = after(to);
+        }
+      });
     };
 #pragma unroll 1
-    for (int i = 0; i < kStages; ++i) load();
+    for (int s = 0; s < kStages; ++s) {
+      begin();
+#pragma unroll
+      for (int i = 0; i < Work::kLoads; ++i) load(i);
+      to = after(to);
+    }
+    begin();
     typename Work::Operands x, y;
     arrived<(kStages - 1) * Work::kLoads>();
-    x.read(lds, lds + kA);
+#pragma unroll
+    for (int i = 0; i < Work::kReadsA; ++i) x.a.read(i, lds + place_a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.b.read(i, lds + place_b);
 #pragma unroll 1
     for (; sum > 0; sum -= 2 * kDepth) {
       step(x, y);
