@@ -36,46 +36,65 @@ struct RowTile {
   int expert;      // -1: no expert's
   int first, end;  // rows of the tile
 };
-// The tiles of `size` rows up to and with this lane's ranges; every wave counts them by itself.
-LDEV int count_row_tiles(const ProductArgs &p, int size, int &mine) {
-  const int lane = lane_id(), ranges = p.experts + 2, per = (ranges + 63) / 64;
-  mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int g = lane * per + i;
-    if (g >= ranges) break;
-    const int a = range_begin(p, g), b = range_begin(p, g + 1);
-    mine += b > a ? (b - a + size - 1) / size : 0;
-  }
-  int upto = mine;
+// The tiles of `size` rows, counted through the ranges in order: lanes take `per` neighbouring ranges each.  Every wave counts
+// by itself.  The bounds of up to kBounds ranges a lane are asked for at once and stay in its registers; of
+// more (from 511 experts on) they are read again.
+struct RowTiles {
+  static constexpr int kBounds = 8;
+  int bound[kBounds + 1];
+  int per, mine, upto;  // ranges of a lane; tiles of this lane's and up to them
+
+  static LDEV int tiles_of(int a, int b, int size) { return b > a ? (b - a + size - 1) / size : 0; }
+  LDEV void count(const ProductArgs &p, int size) {
+    const int ranges = p.experts + 2, first = lane_id() * (per = (ranges + 63) / 64);
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int x = __shfl_up(upto, d, 64);
-    if (lane >= d) upto += x;
+    for (int i = 0; i <= kBounds; ++i) {
+      const int g = first + (i < per ? i : per);
+      bound[i] = range_begin(p, g < ranges ? g : ranges);
+    }
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i < kBounds; ++i) mine += tiles_of(bound[i], bound[i + 1], size);
+    for (int i = kBounds; i < per; ++i) {
+      const int g = first + i;
+      if (g < ranges) mine += tiles_of(range_begin(p, g), range_begin(p, g + 1), size);
+    }
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int x = __shfl_up(upto, d, 64);
+      if (lane_id() >= d) upto += x;
+    }
   }
-  return upto;
-}
-// The index-th of them.  False: there are no more.
-LDEV bool find_row_tile(const ProductArgs &p, int size, int index, int upto, int mine, RowTile &t) {
-  const int ranges = p.experts + 2, per = (ranges + 63) / 64;
-  if (index >= read_lane(upto, 63)) return false;
-  const int at = __builtin_ctzll(__ballot(upto > index));
-  int left = index - read_lane(upto - mine, at);
-  for (int i = 0; i < per; ++i) {
-    const int g = at * per + i;
-    if (g >= ranges) break;
-    const int a = range_begin(p, g), b = range_begin(p, g + 1), n = b > a ? (b - a + size - 1) / size : 0;
-    if (left < n) {
+  LDEV int total() const { return read_lane(upto, 63); }
+  // the index-th of them; false: there are no more
+  LDEV bool find(const ProductArgs &p, int size, int index, RowTile &t) const {
+    if (index >= total()) return false;
+    const int at = __builtin_ctzll(__ballot(upto > index)), first = at * per;
+    int left = index - read_lane(upto - mine, at);
+    const auto here = [&](int g, int a, int b) {
+      const int n = tiles_of(a, b, size);
+      if (left >= n) {
+        left -= n;
+        return false;
+      }
       t.expert = g >= 1 && g <= p.experts ? g - 1 : -1;
       t.first = a + left * size;
       t.end = t.first + size < b ? t.first + size : b;
       return true;
-    }
-    left -= n;
+    };
+#pragma unroll
+    for (int i = 0; i < kBounds; ++i)
+      if (i < per && here(first + i, read_lane(bound[i], at), read_lane(bound[i + 1], at))) return true;
+    for (int i = kBounds; i < per; ++i)
+      if (here(first + i, range_begin(p, first + i), range_begin(p, first + i + 1))) return true;
+    return false;
   }
-  return false;
+};
+// as many tiles as there can be: a range that has rows adds one to those that are full
+int64_t most_row_tiles(const ProductArgs &p, int size) {
+  return p.rows / size + (p.rows < p.experts + 2 ? p.rows : p.experts + 2);
 }
-// as many tiles as there can be
-int64_t most_row_tiles(const ProductArgs &p, int size) { return p.rows / size + p.experts + 2; }
 
 // ------------------------------------------------------------------ any layout
 // A tile of 64 x 64, its factors brought to LDS an element at a time: for sizes, strides and pointers that are no
@@ -100,9 +119,9 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
     k1 = offset_of(p, e + 1);
   } else {
     RowTile t;
-    int mine;
-    const int upto = count_row_tiles(p, kAny, mine);
-    if (!find_row_tile(p, kAny, (int)grid_row(), upto, mine, t)) return;
+    RowTiles all;
+    all.count(p, kAny);
+    if (!all.find(p, kAny, (int)grid_row(), t)) return;
     e = t.expert;
     m0 = t.first;
     m1 = t.end;
@@ -165,7 +184,6 @@ LDEV uint32_t lds_at(const void *p) {
 }
 
 constexpr int kDepth = 32;  // of a step: elements of the sum
-constexpr int kStages = 4;
 
 // One factor's side of a tile: SIZE places along C by kDepth of the sum, in LDS, brought there by WAVES waves.
 //
@@ -320,14 +338,13 @@ LDEV void arrived() {
 }
 
 // Workgroups go round the eight dies; each die takes a run of tiles that share factors.
-LDEV int64_t tile_of_workgroup(int64_t total) {
-  const int64_t each = (total + 7) / 8, i = blockIdx.x;
-  const int64_t t = i % 8 * each + i / 8;
-  return i / 8 < each && t < total ? t : -1;
+LDEV int tile_of_workgroup(int total) {
+  const int each = (total + 7) / 8, i = blockIdx.x / 8, t = blockIdx.x % 8 * each + i;
+  return i < each && t < total ? t : -1;
 }
 
-template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
-__global__ __launch_bounds__(64 * WAVES_M *WAVES_N, WAVES_M *WAVES_N / 4) void product_tile_kernel(ProductArgs p) {
+template <class T, int WM, int WAVES_M, int WAVES_N, int kStages, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
+__global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 2) void product_tile_kernel(ProductArgs p) {
   using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
   constexpr int kA = Work::kM * kDepth, kStage = kA + Work::kN * kDepth;
   __shared__ T lds[kStages * kStage];
@@ -338,9 +355,9 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, WAVES_M *WAVES_N / 4) void p
   int m, n0, sum;  // places of the tile, its first column, elements of the sum
   if constexpr (SUM_ROWS) {
     const int tiles_m = (p.m + Work::kM - 1) / Work::kM;
-    const int64_t t = tile_of_workgroup((int64_t)tiles_m * tiles_n * p.experts);
+    const int t = tile_of_workgroup(tiles_m * tiles_n * p.experts);
     if (t < 0) return;
-    const int e = (int)(t / (tiles_m * tiles_n)), in = (int)(t % (tiles_m * tiles_n)), m0 = in % tiles_m * Work::kM;
+    const int e = t / (tiles_m * tiles_n), in = t % (tiles_m * tiles_n), m0 = in % tiles_m * Work::kM;
     n0 = in / tiles_m * Work::kN;
     const int k0 = offset_of(p, e), k1 = offset_of(p, e + 1);
     sum = k1 - k0;
@@ -349,17 +366,16 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, WAVES_M *WAVES_N / 4) void p
     b += k0 * p.bk + n0;
     out += e * p.ce + m0 * p.cm + n0;
   } else {
-    int mine;
-    const int upto = count_row_tiles(p, Work::kM, mine), rows = read_lane(upto, 63);
-    const int64_t t = tile_of_workgroup((int64_t)rows * tiles_n);
+    RowTiles all;
+    all.count(p, Work::kM);
+    const int rows = all.total(), t = tile_of_workgroup(rows * tiles_n);
     if (t < 0) return;
     // kGroup tiles of rows go through the columns together, so that each column of a matrix is read once for them
     constexpr int kGroup = 8;
-    const int64_t group = t / (kGroup * tiles_n);
-    const int first = (int)group * kGroup, g = rows - first < kGroup ? rows - first : kGroup;
-    const int in = (int)(t - group * kGroup * tiles_n);
+    const int first = t / (kGroup * tiles_n) * kGroup, g = rows - first < kGroup ? rows - first : kGroup;
+    const int in = t - first * tiles_n;
     RowTile r;
-    if (!find_row_tile(p, Work::kM, first + in % g, upto, mine, r)) return;
+    if (!all.find(p, Work::kM, first + in % g, r)) return;
     n0 = in / g * Work::kN;
     m = r.end - r.first;
     sum = r.expert < 0 ? 0 : p.k;
@@ -438,15 +454,127 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, WAVES_M *WAVES_N / 4) void p
   w.store(out, p.cm, m, n);
 }
 
-template <class T, int WM, int WAVES_M, int WAVES_N, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
+template <class T, int WM, int WAVES_M, int WAVES_N, int STAGES, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
 hipError_t tiles(const ProductArgs &p, hipStream_t s) {
   using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
   const int64_t nt = (p.n + Work::kN - 1) / Work::kN;
   const int64_t mt = SUM_ROWS ? (int64_t)((p.m + Work::kM - 1) / Work::kM) * p.experts : most_row_tiles(p, Work::kM);
   const int64_t groups = (nt * mt + 7) / 8 * 8;
   if (groups > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
-  product_tile_kernel<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT, SUM_ROWS>
+  product_tile_kernel<T, WM, WAVES_M, WAVES_N, STAGES, A_NEXT, B_NEXT, SUM_ROWS>
       <<<dim3((unsigned)groups), dim3(64 * WAVES_M * WAVES_N), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ few rows
+// 16 MT rows by 16 NT columns a workgroup, whose waves share the sum: a matrix goes from memory to the operands'
+// registers, without LDS, as much of it under way as the registers hold, and the waves' sums are added at the end.
+constexpr int kFewDepth = 4;  // steps of 32 that are asked for at once
+
+template <class T, int MT, int NT, int WAVES, bool B_NEXT>
+__global__ __launch_bounds__(64 * WAVES) void product_few_kernel(ProductArgs p) {
+  constexpr int M = 16 * MT, N = 16 * NT, kWords = B_NEXT ? 4 : NT / 2;
+  __shared__ float sums[WAVES][M][N];
+  lds_poison(sums);
+  RowTile r;
+  RowTiles all;
+  all.count(p, M);
+  if (!all.find(p, M, (int)grid_row(), r)) return;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int n0 = blockIdx.x * N, m = r.end - r.first, n = p.n - n0 < N ? p.n - n0 : N;
+  f32x4 c[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) c[i][j] = f32x4{};
+  if (r.expert >= 0) {
+    const T *a = static_cast<const T *>(p.a) + r.first * p.am;
+    const T *b = static_cast<const T *>(p.b) + r.expert * p.be + n0 * p.bn;
+    const int sa = (int)p.am, sb = (int)(B_NEXT ? p.bn : p.bk);
+    // this lane's place in a step: of A the row lane % 16 and eight elements, of B as in Held
+    const uint32_t oa = (uint32_t)(lane % 16 * sa * 2 + lane / 16 * 16);
+    const uint32_t ob = (uint32_t)(B_NEXT ? lane % 16 * NT * sb * 2 + lane / 16 * 16
+                                          : lane / 16 * 8 * sb * 2 + lane % 16 * NT * 2);
+    // steps go round the waves, kFewDepth neighbouring ones each
+#pragma unroll 1
+    for (int k0 = wave * kFewDepth * 32; k0 < p.k; k0 += WAVES * kFewDepth * 32) {
+      uint4 fa[kFewDepth][MT];
+      uint32_t fb[kFewDepth][B_NEXT ? NT : 8][kWords];
+#pragma unroll
+      for (int d = 0; d < kFewDepth; ++d) {
+        const int k = k0 + d * 32, left = p.k - k < 32 ? p.k - k : 32;  // may be none
+        const uint32_t none = lane / 16 * 8 >= left ? kNowhere : 0u;
+        const window_t wb = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<T *>(b + (int64_t)k * (B_NEXT ? 1 : sb)), 0,
+            left <= 0 ? 0 : (B_NEXT ? ((n - 1) * sb + left) * 2 : ((left - 1) * sb + n) * 2), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < (B_NEXT ? NT : 8); ++i) {
+          const uint32_t o = ob + (uint32_t)(i * sb * 2);
+          if constexpr (B_NEXT)
+            *reinterpret_cast<uint4 *>(fb[d][i]) =
+                __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wb, (int)(o | none), 0, 0));
+          else if constexpr (NT == 8)
+            *reinterpret_cast<uint4 *>(fb[d][i]) =
+                __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(wb, (int)o, 0, 0));
+          else
+            *reinterpret_cast<uint2 *>(fb[d][i]) =
+                __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(wb, (int)o, 0, 0));
+        }
+        const window_t wa = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(a + k), 0,
+                                                              left <= 0 ? 0 : ((m - 1) * sa + left) * 2, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          fa[d][i] = __builtin_bit_cast(
+              uint4, __builtin_amdgcn_raw_buffer_load_b128(wa, (int)((oa + (uint32_t)(i * 16 * sa * 2)) | none), 0, 0));
+      }
+#pragma unroll
+      for (int d = 0; d < kFewDepth; ++d)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (B_NEXT)
+              w[q] = fb[d][j][q];
+            else
+              w[q] = j % 2 == 0 ? pair_low(fb[d][2 * q][j / 2], fb[d][2 * q + 1][j / 2])
+                                : pair_high(fb[d][2 * q][j / 2], fb[d][2 * q + 1][j / 2]);
+          }
+          const pack_t<T> f = __builtin_bit_cast(pack_t<T>, uint4{w[0], w[1], w[2], w[3]});
+#pragma unroll
+          for (int i = 0; i < MT; ++i) c[i][j] = mfma(__builtin_bit_cast(pack_t<T>, fa[d][i]), f, c[i][j]);
+        }
+    }
+  }
+  // lane l has the rows l / 16 * 4 + 0 .. 3 and the columns l % 16 * NT + 0 .. NT - 1 of each 16 rows
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) sums[wave][i * 16 + lane / 16 * 4 + q][lane % 16 * NT + j] = c[i][j][q];
+  __syncthreads();
+  T *out = static_cast<T *>(p.c) + r.first * p.cm + n0;
+  for (int x = threadIdx.x; x < M * N / 2; x += 64 * WAVES) {
+    const int row = x / (N / 2), col = x % (N / 2) * 2;
+    if (row >= m || col >= n) continue;
+    float2 s = {0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const float2 y = *reinterpret_cast<const float2 *>(&sums[w][row][col]);
+      s.x += y.x;
+      s.y += y.y;
+    }
+    typedef T pair_t __attribute__((ext_vector_type(2)));
+    *reinterpret_cast<pair_t *>(out + row * p.cm + col) = pair_t{(T)s.x, (T)s.y};
+  }
+}
+
+template <class T, int MT, int NT, int WAVES, bool B_NEXT>
+hipError_t few(const ProductArgs &p, hipStream_t s) {
+  const unsigned nt = (unsigned)((p.n + 16 * NT - 1) / (16 * NT));
+  product_few_kernel<T, MT, NT, WAVES, B_NEXT>
+      <<<rows_grid(nt, most_row_tiles(p, 16 * MT)), dim3(64 * WAVES), 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -457,7 +585,7 @@ template <class T>
 hipError_t rows_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.am) && whole(p.be) && whole(p.bk == 1 ? p.bn : p.bk) &&
       whole(p.cm) && whole(p.n) && whole(p.k))
-    return p.bk == 1 ? tiles<T, 64, 4, 2, true, true, false>(p, s) : tiles<T, 64, 4, 2, true, false, false>(p, s);
+    return p.rows <= 256 ? (p.bk == 1 ? few<T, 1, 4, 8, true>(p, s) : few<T, 1, 4, 8, false>(p, s)) : p.bk == 1 ? tiles<T, 64, 2, 2, 3, true, true, false>(p, s) : tiles<T, 64, 2, 2, 3, true, false, false>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   product_any_kernel<T, false><<<rows_grid(nt, most_row_tiles(p, kAny)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
@@ -466,7 +594,7 @@ template <class T>
 hipError_t weights_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.ak) && whole(p.bk) && whole(p.ce) && whole(p.cm) &&
       whole(p.m) && whole(p.n))
-    return tiles<T, 64, 4, 2, false, false, true>(p, s);
+    return tiles<T, 64, 2, 2, 3, false, false, true>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   const int64_t mt = (p.m + kAny - 1) / kAny;
   product_any_kernel<T, true><<<rows_grid(nt, mt * p.experts), dim3(256), 0, s>>>(p);
