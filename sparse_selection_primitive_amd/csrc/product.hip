@@ -6,6 +6,8 @@
 // what is summed over.  How many rows an expert has is known on the device only, so a workgroup finds its
 // expert and rows from the offsets: tiles are counted through the experts in order, one wave's lanes a
 // few experts each.
+#include <cmath>
+
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
 
@@ -581,11 +583,54 @@ hipError_t few(const ProductArgs &p, hipStream_t s) {
 bool whole(const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; }
 bool whole(int64_t n) { return n % 8 == 0; }
 
+// Which kernel takes the rows: by how long each would take, as far as the host knows sizes (not how the rows are
+// spread: experts that rows meet by chance have x rows each, x / size + 1/2 tiles).  Figures of bf16, in us.
+//  - 16 rows a workgroup: a start, then what its tiles draw through the caches.  4 experts of 2048 x 1024 with 12
+//    rows each: 9.4 (tiles of 128 x 256: 28), with 400 48 (30); 32 experts of 1024 x 4096 with a row each 27 (33), with
+//    24 68 (46).
+//  - 32 rows: a longer start, the caches' draw halved.  4 experts of 1024 x 4096, 96 rows each: 14.8 (16 rows 25.5,
+//    tiles 18.0); 256 experts of 2048 x 1024 with 24 rows 230 (tiles 205).
+//  - 128 x 256: 0.42 a step where every workgroup has a compute unit to itself, else a round of 512; or the matrices' way
+//    from memory.
+//  - 256 x 256: a round of 256 takes as long, and less is loaded: 8 experts of 4096 x 14336 with 2048 rows 1710 for
+//    1830, 64 experts of 2056 x 1416 with 469 rows (as many rounds of both) 328 for 366, 256 experts of 2048 x 1024 with
+//    256 (six rounds for five) 509 for 443.
+enum Kind { kFew16, kFew32, kTile128, kTile256 };
+Kind tile_kind(double tiles128, double tiles256) {
+  return tiles128 > 256 && std::ceil(tiles256 / 256) <= std::ceil(tiles128 / 512) ? kTile256 : kTile128;
+}
+Kind rows_kind(const ProductArgs &p) {
+  const double rows = (double)p.rows, met = p.experts * (1.0 - std::exp(-rows / p.experts)), x = rows / met;
+  const auto tiles = [&](int size) { return met * std::fmax(1.0, x / size + 0.5); };
+  const double matrix = (double)p.k * p.n * 2e-6, columns = std::ceil(p.n / 256.0), tiles128 = tiles(128) * columns;
+  const double few16 = 4.5 + tiles(16) * matrix / 6;
+  const double few32 = 6 + std::fmax(tiles(32) * matrix / 11, met * matrix / 4.5);
+  const double step = tiles128 <= 256 ? 0.42 : 0.95 * std::ceil(tiles128 / 512);
+  const double tile = 3 + std::fmax(step * p.k / 32, met * matrix / 5.2);
+  if (few16 <= few32 && few16 < tile) return kFew16;
+  if (few32 < tile) return kFew32;
+  return tile_kind(tiles128, tiles(256) * columns);
+}
+
+template <class T, bool B_NEXT>
+hipError_t rows_in(const ProductArgs &p, hipStream_t s) {
+  switch (rows_kind(p)) {
+    case kFew16:
+      if constexpr (B_NEXT)
+        return few<T, 1, 2, 8, true>(p, s);
+      else  // wide rows of a matrix where there are workgroups enough (192 rows to 256 experts of 2048 x 1024: 72, else 80)
+        return most_row_tiles(p, 16) * p.n >= 1024 * 128 ? few<T, 1, 8, 4, false>(p, s) : few<T, 1, 4, 8, false>(p, s);
+    case kFew32: return few<T, 2, 4, 4, B_NEXT>(p, s);
+    case kTile128: return tiles<T, 64, 2, 2, 3, true, B_NEXT, false>(p, s);
+    case kTile256: return tiles<T, 64, 4, 2, 4, true, B_NEXT, false>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
 template <class T>
 hipError_t rows_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.am) && whole(p.be) && whole(p.bk == 1 ? p.bn : p.bk) &&
       whole(p.cm) && whole(p.n) && whole(p.k))
-    return p.rows <= 256 ? (p.bk == 1 ? few<T, 1, 4, 8, true>(p, s) : few<T, 1, 4, 8, false>(p, s)) : p.bk == 1 ? tiles<T, 64, 2, 2, 3, true, true, false>(p, s) : tiles<T, 64, 2, 2, 3, true, false, false>(p, s);
+    return p.bk == 1 ? rows_in<T, true>(p, s) : rows_in<T, false>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   product_any_kernel<T, false><<<rows_grid(nt, most_row_tiles(p, kAny)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
@@ -594,7 +639,10 @@ template <class T>
 hipError_t weights_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.ak) && whole(p.bk) && whole(p.ce) && whole(p.cm) &&
       whole(p.m) && whole(p.n))
-    return tiles<T, 64, 2, 2, 3, false, false, true>(p, s);
+    return tile_kind(std::ceil(p.m / 128.0) * std::ceil(p.n / 256.0) * p.experts,
+                     std::ceil(p.m / 256.0) * std::ceil(p.n / 256.0) * p.experts) == kTile256
+               ? tiles<T, 64, 4, 2, 4, false, false, true>(p, s)
+               : tiles<T, 64, 2, 2, 3, false, false, true>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
   const int64_t mt = (p.m + kAny - 1) / kAny;
   product_any_kernel<T, true><<<rows_grid(nt, mt * p.experts), dim3(256), 0, s>>>(p);
