@@ -12,108 +12,105 @@
 namespace lapsum {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // (a struct of four would go through memory)
+
 LDEV int clamped(int64_t n, int64_t capacity) { return (int)(n < 0 ? 0 : (n > capacity ? capacity : n)); }
 
-// One column: what the beams hold at `at` elements of a V, `stride` (bytes) between beams.
+// The beams of a search, one a lane: whose cache each takes over, and how many entries it has.  Asked with all lanes.
+struct Family {
+  int parent, length;  // parent -1: none, or itself
+  // the beams that take p's cache over
+  LDEV uint64_t takers(int p) const { return __ballot(parent == p); }
+  // its entries, none where nobody takes it
+  LDEV int reach(int p) const { return takers(p) != 0 ? read_lane(length, p) : 0; }
+};
+
+// One column: what the beams hold at `at`, `stride` bytes from beam to beam, of entry `entry`.
 template <int NB, class V>
 struct Column {
   V held[NB];
-  template <class S>
-  LDEV void take(const S &sh, const char *at, int64_t stride, int entry) {
-#pragma unroll
-    for (int p = 0; p < NB; ++p)
-      if (entry < sh.reach(p)) held[p] = *reinterpret_cast<const V *>(at + p * stride);
-  }
-  template <class S>
-  LDEV void give(const S &sh, char *at, int64_t stride, int entry) const {
+  LDEV void take(const Family &f, const char *at, int64_t stride, int entry) {
 #pragma unroll
     for (int p = 0; p < NB; ++p) {
-      if (entry >= sh.reach(p)) continue;
-      for (uint64_t left = sh.takers(p); left != 0; left &= left - 1)
-        *reinterpret_cast<V *>(at + __builtin_ctzll(left) * stride) = held[p];
+      const int reach = f.reach(p);
+      if (entry < reach) held[p] = *reinterpret_cast<const V *>(at + p * stride);
     }
   }
-};
-
-// which beams take each beam's cache over, and how many entries (0 where none does)
-template <int NB>
-struct Family {
-  uint64_t mask[NB];
-  int length[NB];
-  LDEV int reach(int p) const { return __builtin_amdgcn_readfirstlane(length[p]); }
-  LDEV uint64_t takers(int p) const {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)mask[p]);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(mask[p] >> 32));
-    return (uint64_t)hi << 32 | lo;
-  }
-};
-
-template <int NB, class V>
-__global__ __launch_bounds__(256) void reorder_kernel(ReorderArgs a, int tile) {
-  __shared__ Family<NB> sh;
-  lds_poison(sh);
-  const int64_t b = grid_row() / a.heads, h = grid_row() % a.heads;
-  if (b >= a.searches) return;
-  const int lane = lane_id(), beams = a.beams;
-  int parent = -1, length = 0;
-  if (lane < beams) {
-    parent = a.parents[b * beams + lane];
-    length = clamped(a.lengths[b * beams + lane], a.capacity);
-  }
-  if (parent < 0 || parent >= beams) parent = -1;
-  const int theirs = __shfl(length, parent < 0 ? 0 : parent, 64);
-  if (blockIdx.x == 0 && h == 0 && threadIdx.x < beams) a.lengths_out[b * beams + lane] = parent < 0 ? 0 : theirs;
-  if (threadIdx.x < 64) {
-#pragma unroll 1
+  LDEV void give(const Family &f, char *at, int64_t stride, int entry) const {
+#pragma unroll
     for (int p = 0; p < NB; ++p) {
-      const uint64_t m = __ballot(lane < beams && parent == p && lane != p);
-      if (lane == 0) {
-        sh.mask[p] = m;
-        sh.length[p] = m != 0 ? read_lane(length, p) : 0;
+      const int reach = f.reach(p);
+      for (uint64_t left = f.takers(p); left != 0; left &= left - 1) {
+        const int j = __builtin_ctzll(left);
+        if (entry < reach) *reinterpret_cast<V *>(at + j * stride) = held[p];
       }
     }
   }
-  __syncthreads();
-  int most = 0;
+};
+
+constexpr int kNoEntry = 0x7FFFFFFF;
+
+// Workgroups of `tile` entries, 256 columns of V, then (blockIdx.x from `tiles` on) of 256 entries' accounts and positions.
+template <int NB, class V>
+__global__ __launch_bounds__(256) void reorder_kernel(ReorderArgs a, int tile, int tiles) {
+  const uint32_t row = (uint32_t)grid_row(), heads = (uint32_t)a.heads;  // at most 2^24
+  const int64_t b = row / heads, h = row % heads;
+  if (b >= a.searches) return;
+  const int lane = lane_id(), beams = a.beams;
+  Family f{-1, 0};
+  if (lane < beams) {
+    f.parent = a.parents[b * beams + lane];
+    f.length = clamped(a.lengths[b * beams + lane], a.capacity);
+  }
+  const bool there = f.parent >= 0 && f.parent < beams;
+  const int theirs = __shfl(f.length, there ? f.parent : 0, 64);
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x < beams) a.lengths_out[b * beams + lane] = there ? theirs : 0;
+  if (!there || f.parent == lane) f.parent = -1;
+  int most = 0;  // entries of the longest cache that is taken over
 #pragma unroll
-  for (int p = 0; p < NB; ++p) most = sh.reach(p) > most ? sh.reach(p) : most;
-  const int64_t e0 = (int64_t)blockIdx.x * tile;
-  if (e0 >= most) return;
-  const int entries = most - (int)e0 < tile ? most - (int)e0 : tile;
-  const int per = a.width * 2 / (int)sizeof(V);  // columns of an entry
-  char *k = static_cast<char *>(a.k) + (b * beams * a.kb + h * a.kh + e0 * a.ke) * 2;
-  char *v = static_cast<char *>(a.v) + (b * beams * a.vb + h * a.vh + e0 * a.ve) * 2;
-  for (int u = threadIdx.x; u < entries * per; u += 256) {
-    const int e = u / per, c = (u - e * per) * (int)sizeof(V);
-    Column<NB, V> x;
-    char *at = k + e * a.ke * 2 + c;
-    x.take(sh, at, a.kb * 2, (int)e0 + e);
-    x.give(sh, at, a.kb * 2, (int)e0 + e);
-    at = v + e * a.ve * 2 + c;
-    x.take(sh, at, a.vb * 2, (int)e0 + e);
-    x.give(sh, at, a.vb * 2, (int)e0 + e);
+  for (int p = 0; p < NB; ++p) {
+    const int reach = f.reach(p);
+    most = reach > most ? reach : most;
   }
-  const int64_t first = (b * beams * a.heads + h) * a.capacity + e0, beam = a.heads * a.capacity * 4;
-  for (int e = threadIdx.x; e < entries; e += 256) {
-    Column<NB, uint32_t> x;
-    if (a.account != nullptr) {
-      char *at = reinterpret_cast<char *>(a.account + first + e);
-      x.take(sh, at, beam, (int)e0 + e);
-      x.give(sh, at, beam, (int)e0 + e);
+  if ((int)blockIdx.x < tiles) {
+    const int64_t e0 = (int64_t)blockIdx.x * tile;
+    if (e0 >= most) return;
+    const int per = a.width * 2 / (int)sizeof(V);  // columns of an entry
+    const int e = threadIdx.x / per, entry = e < tile ? (int)e0 + e : kNoEntry, c = (threadIdx.x - e * per) * (int)sizeof(V);
+    char *k = static_cast<char *>(a.k) + (b * beams * a.kb + h * a.kh + (e0 + e) * a.ke) * 2 + c;
+    char *v = static_cast<char *>(a.v) + (b * beams * a.vb + h * a.vh + (e0 + e) * a.ve) * 2 + c;
+    Column<NB, V> x, y;
+    x.take(f, k, a.kb * 2, entry);
+    if constexpr (NB <= 8) {  // both at once where the registers hold them
+      y.take(f, v, a.vb * 2, entry);
+      x.give(f, k, a.kb * 2, entry);
+      y.give(f, v, a.vb * 2, entry);
+    } else {
+      x.give(f, k, a.kb * 2, entry);
+      y.take(f, v, a.vb * 2, entry);
+      y.give(f, v, a.vb * 2, entry);
     }
-    if (a.positions != nullptr) {
-      char *at = reinterpret_cast<char *>(a.positions + first + e);
-      x.take(sh, at, beam, (int)e0 + e);
-      x.give(sh, at, beam, (int)e0 + e);
-    }
+    return;
   }
+  const int64_t e0 = (int64_t)(blockIdx.x - tiles) * 256 + threadIdx.x;
+  if (e0 - threadIdx.x >= most) return;
+  const int entry = e0 < most ? (int)e0 : kNoEntry;
+  const int64_t first = ((b * beams * a.heads + h) * a.capacity + e0) * 4, beam = a.heads * a.capacity * 4;
+  char *account = reinterpret_cast<char *>(a.account) + first, *positions = reinterpret_cast<char *>(a.positions) + first;
+  Column<NB, uint32_t> x, y;
+  if (a.account != nullptr) x.take(f, account, beam, entry);
+  if (a.positions != nullptr) y.take(f, positions, beam, entry);
+  if (a.account != nullptr) x.give(f, account, beam, entry);
+  if (a.positions != nullptr) y.give(f, positions, beam, entry);
 }
 
 template <int NB, class V>
 hipError_t reorder(const ReorderArgs &a, hipStream_t s) {
-  const int64_t rows = a.searches * a.heads;
-  const int tile = 32;
-  reorder_kernel<NB, V><<<rows_grid((unsigned)((a.capacity + tile - 1) / tile), rows), dim3(256), 0, s>>>(a, tile);
+  const int per = a.width * 2 / (int)sizeof(V), tile = 256 / per;
+  const int64_t tiles = (a.capacity + tile - 1) / tile;
+  const int64_t extra = a.account != nullptr || a.positions != nullptr ? (a.capacity + 255) / 256 : 0;
+  if (tiles + extra > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+  reorder_kernel<NB, V><<<rows_grid((unsigned)(tiles + extra), a.searches * a.heads), dim3(256), 0, s>>>(a, tile, (int)tiles);
   return hipGetLastError();
 }
 
@@ -121,9 +118,9 @@ hipError_t reorder(const ReorderArgs &a, hipStream_t s) {
 
 hipError_t launch_reorder(const ReorderArgs &a, hipStream_t s) {
   // a thread's registers hold the column: 16 bytes of up to 16 beams, 4 of up to 64
-  if (a.beams <= 4) return reorder<4, uint4>(a, s);
-  if (a.beams <= 8) return reorder<8, uint4>(a, s);
-  if (a.beams <= 16) return reorder<16, uint4>(a, s);
+  if (a.beams <= 4) return reorder<4, u32x4>(a, s);
+  if (a.beams <= 8) return reorder<8, u32x4>(a, s);
+  if (a.beams <= 16) return reorder<16, u32x4>(a, s);
   return reorder<64, uint32_t>(a, s);
 }
 
