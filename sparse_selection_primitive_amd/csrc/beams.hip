@@ -2,8 +2,8 @@
 //
 // score(i, v) = scores[i] + (x - M) - log S with M = max_u x[i, u] and S = sum_u e^(x[i, u] - M).
 //
-// First launch: rows are cut into parts of 512 tokens (16 lanes a part); each leaves its maximum and
-// its sum of e^(x - maximum).  That is the one pass over the logits, and no selection takes part in it.
+// First launch: rows are cut into parts of 512 tokens (16 lanes a part); each leaves its maximum, and each
+// workgroup its sum of e^(x - maximum).  That is the one pass over the logits, and no selection takes part in it.
 // Second launch, a workgroup a search: the sums give every beam's log S, so the parts' maxima become scores.  All of
 // the k best continuations lie in the k best parts (by score, then by place): a part
 // that is not among them has k parts before it, each with a continuation before all of its own.  So only
@@ -63,12 +63,13 @@ __global__ __launch_bounds__(256) void beam_parts_kernel(BeamArgs a) {
   constexpr int N = Pack<T>::N, L = kPart / (16 * N);
   const int64_t row = grid_row();
   if (row >= a.batch * a.beams || (a.ended != nullptr && a.ended[row] != 0)) return;
-  const int part = blockIdx.x * 16 + threadIdx.x / 16, lane = threadIdx.x % 16;
-  if (part >= a.chunks) return;
+  const int part = blockIdx.x * kBeamGroup + threadIdx.x / 16, lane = threadIdx.x % 16;
+  __shared__ float2 sums[256 / 64];
+  lds_poison(sums);
   const T *x = static_cast<const T *>(a.logits) + row * a.stride;
   float m = -INFINITY, s = 0.0f;
   const int64_t begin = (int64_t)part * a.chunk;
-  for (int64_t t0 = begin; t0 < begin + a.chunk && t0 < a.vocab; t0 += kPart) {
+  for (int64_t t0 = begin; t0 < begin + a.chunk && t0 < a.vocab; t0 += kPart) {  // none behind the last part
     float v[L][N];
 #pragma unroll
     for (int i = 0; i < L; ++i) {
@@ -107,7 +108,16 @@ __global__ __launch_bounds__(256) void beam_parts_kernel(BeamArgs a) {
   join_lanes<2>(m, s);
   join_lanes<4>(m, s);
   join_lanes<8>(m, s);
-  if (lane == 0) a.parts[row * a.chunks + part] = float2{m, s};
+  if (lane == 0 && part < a.chunks) a.tops[row * a.chunks + part] = m;
+  join_lanes<16>(m, s);
+  join_lanes<32>(m, s);
+  if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = float2{m, s};
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 256 / 64; ++w) join(m, s, sums[w].x, sums[w].y);
+    a.sums[row * ((a.chunks + kBeamGroup - 1) / kBeamGroup) + blockIdx.x] = float2{m, s};
+  }
 }
 
 // --------------------------------------------------------------- selection
@@ -140,6 +150,13 @@ LDEV double score_of(const Shared &sh, int beam, float x) {
   return s > kNone ? s : kNone;  // NaN is none
 }
 
+LDEV int row_sum(int v) {  // over 16 lanes
+  v += (int)xor_lanes<1>((uint32_t)v);
+  v += (int)xor_lanes<2>((uint32_t)v);
+  v += (int)xor_lanes<7>((uint32_t)v);
+  return v + (int)xor_lanes<15>((uint32_t)v);
+}
+
 // The k first of the listed candidates in their order, each ranked by how many come before it.
 LDEV void rank_listed(Shared &sh, int n, int k) {
   for (int i = threadIdx.x; i < k; i += kThreads) {
@@ -147,11 +164,12 @@ LDEV void rank_listed(Shared &sh, int n, int k) {
     sh.best_place[i] = -1;
   }
   __syncthreads();
-  if ((int)threadIdx.x < n) {
-    const Best me{sh.score[threadIdx.x], sh.place[threadIdx.x]};
+  for (int e = threadIdx.x / 16; e < n; e += kRows) {  // 16 lanes each
+    const Best me{sh.score[e], sh.place[e]};
     int rank = 0;
-    for (int i = 0; i < n; ++i) rank += Best{sh.score[i], sh.place[i]}.before(me) ? 1 : 0;
-    if (rank < k) {
+    for (int i = threadIdx.x % 16; i < n; i += 16) rank += Best{sh.score[i], sh.place[i]}.before(me) ? 1 : 0;
+    rank = row_sum(rank);
+    if (rank < k && threadIdx.x % 16 == 0) {
       sh.best_score[rank] = me.score;
       sh.best_place[rank] = me.place;
     }
@@ -223,15 +241,25 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
   const int64_t search = grid_row();
   if (search >= a.batch) return;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const float2 *parts = a.parts + search * a.beams * a.chunks;
+  const int all = a.beams * a.chunks, groups = (a.chunks + kBeamGroup - 1) / kBeamGroup;
+  const float *tops = a.tops + search * a.beams * a.chunks;
+  const float2 *sums = a.sums + search * a.beams * groups;
 
+  // this thread's parts, asked for before the sums are joined
+  constexpr int kMine = kMostParts / kThreads;
+  float mine_top[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int i = j * kThreads + threadIdx.x;
+    if (i < all) mine_top[j] = tops[i];  // of an ended beam whatever is there: not looked at
+  }
   for (int i = wave; i < a.beams; i += kThreads / 64) {
     const float score = a.scores[search * a.beams + i];
     const bool ended = a.ended != nullptr && a.ended[search * a.beams + i] != 0;
     float m = -INFINITY, s = 0.0f;
     if (!ended) {
-      for (int c = lane; c < a.chunks; c += 64) {
-        const float2 x = parts[i * a.chunks + c];
+      for (int c = lane; c < groups; c += 64) {
+        const float2 x = sums[i * groups + c];
         join(m, s, x.x, x.y);
       }
       join_lanes<1>(m, s);
@@ -244,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
     if (lane == 0) {
       const bool finite = score > -INFINITY && score < INFINITY;
       const bool none = !finite || (!ended && !(s > 0.0f));  // a NaN sum, or nothing above -inf
-      sh.base[i] = none ? kNone : (ended ? (double)score : (double)score - log((double)s));
+      sh.base[i] = none ? kNone : (ended ? (double)score : (double)score - log_pos((double)s));
       sh.top[i] = ended || none ? 0.0f : m;
       sh.done[i] = ended;
     }
@@ -253,15 +281,22 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
   __syncthreads();
 
   // the best parts
-  const int all = a.beams * a.chunks, end_part = a.ended != nullptr ? a.end_token / a.chunk : 0;
-  const auto each_part = [&](const auto &f) {
-    for (int i = threadIdx.x; i < all; i += kThreads) {
-      const int beam = i / a.chunks;
-      if (sh.done[beam])
-        f(Best{i - beam * a.chunks == end_part ? sh.base[beam] : kNone, i});
-      else
-        f(Best{score_of(sh, beam, parts[i].x), i});
+  double mine_score[kMine];
+  const int end_part = a.ended != nullptr ? a.end_token / a.chunk : 0;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int i = j * kThreads + threadIdx.x;
+    mine_score[j] = kNone;
+    if (i < all) {
+      const int beam = (int)((uint64_t)i * a.chunk_magic >> 32);
+      mine_score[j] = !sh.done[beam] ? score_of(sh, beam, mine_top[j])
+                                     : (i - beam * a.chunks == end_part ? sh.base[beam] : kNone);
     }
+  }
+  const auto each_part = [&](const auto &f) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j)
+      if (mine_score[j] > kNone) f(Best{mine_score[j], j * kThreads + (int)threadIdx.x});
   };
   // the k-th best of the rows of 16 lanes' best: k candidates are at least that
   double mine = kNone;
@@ -277,10 +312,7 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
       const Best o{sh.row_best[first + i], first + i};
       before += o.before(Best{mine, row}) ? 1 : 0;
     }
-    before += (int)xor_lanes<1>((uint32_t)before);
-    before += (int)xor_lanes<2>((uint32_t)before);
-    before += (int)xor_lanes<7>((uint32_t)before);
-    before += (int)xor_lanes<15>((uint32_t)before);
+    before = row_sum(before);
     if (before == a.k - 1 && threadIdx.x % 16 == 0) sh.least = mine;
   }
   __syncthreads();
@@ -293,12 +325,13 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
     sh.listed = 0;
   }
   __syncthreads();
-  const int units = a.chunk / N;
+  const int shift = __builtin_ctz(a.chunk / N);
   const auto each_token = [&](const auto &f) {
-    for (int u = threadIdx.x; u < a.k * units; u += kThreads) {
-      const int part = chosen[u / units];
+    for (int u = threadIdx.x; u < a.k << shift; u += kThreads) {
+      const int part = chosen[u >> shift];
       if (part < 0) continue;
-      const int beam = part / a.chunks, t = (part - beam * a.chunks) * a.chunk + u % units * N;
+      const int beam = (int)((uint64_t)part * a.chunk_magic >> 32);
+      const int t = (part - beam * a.chunks) * a.chunk + (u & ((1 << shift) - 1)) * N;
       if (sh.done[beam]) {
         if (a.end_token >= t && a.end_token < t + N) f(Best{sh.base[beam], beam * a.vocab + a.end_token});
         continue;
@@ -322,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
 
 template <class T>
 hipError_t beams(const BeamArgs &a, hipStream_t s) {
-  beam_parts_kernel<T><<<rows_grid((unsigned)((a.chunks + 15) / 16), a.batch * a.beams), dim3(256), 0, s>>>(a);
+  beam_parts_kernel<T><<<rows_grid((unsigned)((a.chunks + kBeamGroup - 1) / kBeamGroup), a.batch * a.beams), dim3(256), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   beam_select_kernel<T><<<rows_grid(1, a.batch), dim3(kThreads), 0, s>>>(a);

@@ -174,10 +174,13 @@ lapsum_status check_beams(int32_t dtype, int64_t batch, int64_t beams, int64_t v
     return LAPSUM_ERR_SHAPE;
   return k < 1 || k > LAPSUM_MAX_BEAMS ? LAPSUM_ERR_OPTION : LAPSUM_OK;
 }
+// the parts' maxima, then the groups' sums
+size_t beam_tops_bytes(int64_t rows, int chunks) { return aligned_up((size_t)rows * (size_t)chunks * sizeof(float)); }
 size_t beam_bytes(int64_t batch, int64_t beams, int64_t vocab) {
   int chunk, chunks;
   beam_parts(beams, vocab, chunk, chunks);
-  return aligned_up((size_t)(batch * beams) * (size_t)chunks * sizeof(float2));
+  const size_t groups = (size_t)(chunks + kBeamGroup - 1) / kBeamGroup;
+  return beam_tops_bytes(batch * beams, chunks) + aligned_up((size_t)(batch * beams) * groups * sizeof(float2));
 }
 
 size_t attend_bytes(const AttendPlan &p) {
@@ -493,7 +496,9 @@ lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batc
   a.scores_out = scores_out;
   a.parents = parents;
   a.tokens = tokens;
-  a.parts = static_cast<float2 *>(workspace);
+  a.chunk_magic = (((uint64_t)1 << 32) + (uint64_t)a.chunks - 1) / (uint64_t)a.chunks;
+  a.tops = static_cast<float *>(workspace);
+  a.sums = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + beam_tops_bytes(batch * beams, a.chunks));
   (void)hipGetLastError();
   return done(launch_beam_select(a, dtype, reinterpret_cast<hipStream_t>(stream)));
 }

@@ -124,8 +124,11 @@ struct BeamArgs {
   int end_token;
   float *scores_out;
   int32_t *parents, *tokens;
-  float2 *parts;            // [batch * beams][chunks]: maximum, sum of e^(x - maximum)
+  uint64_t chunk_magic;     // ceil(2^32 / chunks): i / chunks = i * magic >> 32 for all parts of a search
+  float *tops;              // [batch * beams][chunks]: maximum of a part
+  float2 *sums;             // [batch * beams][groups]: maximum and sum of e^(x - maximum) of kBeamGroup parts
 };
+constexpr int kBeamGroup = 16;
 void beam_parts(int64_t beams, int64_t vocab, int &chunk, int &chunks);
 hipError_t launch_beam_select(const BeamArgs &a, int dtype, hipStream_t s);
 

@@ -12,7 +12,9 @@
 namespace lapsum {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));  // (a struct of four would go through memory)
+// (structs of as many would go through memory)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 LDEV int clamped(int64_t n, int64_t capacity) { return (int)(n < 0 ? 0 : (n > capacity ? capacity : n)); }
 
@@ -49,10 +51,13 @@ struct Column {
 };
 
 constexpr int kNoEntry = 0x7FFFFFFF;
+constexpr int64_t kMostGroups = 1 << 20;  // of a search and head; beyond, workgroups take several parts
 
-// Workgroups of `tile` entries, 256 columns of V, then (blockIdx.x from `tiles` on) of 256 entries' accounts and positions.
+// Workgroups of twice `tile` entries' keys or values (in turn; 256 columns of V are a tile), then, blockIdx.x from `parts`
+// on, of 256 entries' accounts and positions.  Keys and values of one tile by one workgroup: 16 searches of 4 beams with up to
+// 8192 entries 430 us, by two of two tiles 370 (short caches the same, 7.0), of 8 tiles 377 (12.5), with streamed accesses 366 to 372.
 template <int NB, class V>
-__global__ __launch_bounds__(256) void reorder_kernel(ReorderArgs a, int tile, int tiles) {
+__global__ __launch_bounds__(256) void reorder_kernel(ReorderArgs a, int tile, int64_t parts) {
   const uint32_t row = (uint32_t)grid_row(), heads = (uint32_t)a.heads;  // at most 2^24
   const int64_t b = row / heads, h = row % heads;
   if (b >= a.searches) return;
@@ -72,56 +77,60 @@ __global__ __launch_bounds__(256) void reorder_kernel(ReorderArgs a, int tile, i
     const int reach = f.reach(p);
     most = reach > most ? reach : most;
   }
-  if ((int)blockIdx.x < tiles) {
-    const int64_t e0 = (int64_t)blockIdx.x * tile;
-    if (e0 >= most) return;
+  for (int64_t part = blockIdx.x; part < parts; part += gridDim.x) {
+    const int64_t e0 = part / 2 * (2 * tile);
+    if (e0 >= most) break;
+    const bool values = part % 2 != 0;
+    const int64_t beam = (values ? a.vb : a.kb) * 2, head = (values ? a.vh : a.kh) * 2, step = (values ? a.ve : a.ke) * 2;
     const int per = a.width * 2 / (int)sizeof(V);  // columns of an entry
-    const int e = threadIdx.x / per, entry = e < tile ? (int)e0 + e : kNoEntry, c = (threadIdx.x - e * per) * (int)sizeof(V);
-    char *k = static_cast<char *>(a.k) + (b * beams * a.kb + h * a.kh + (e0 + e) * a.ke) * 2 + c;
-    char *v = static_cast<char *>(a.v) + (b * beams * a.vb + h * a.vh + (e0 + e) * a.ve) * 2 + c;
+    const int e = threadIdx.x / per, c = (threadIdx.x - e * per) * (int)sizeof(V);
+    char *at = static_cast<char *>(values ? a.v : a.k) + b * beams * beam + h * head + (e0 + e) * step + c;
+    char *then = at + tile * step;
+    const int entry = e < tile ? (int)e0 + e : kNoEntry, second = e < tile ? (int)e0 + tile + e : kNoEntry;
     Column<NB, V> x, y;
-    x.take(f, k, a.kb * 2, entry);
-    if constexpr (NB <= 8) {  // both at once where the registers hold them
-      y.take(f, v, a.vb * 2, entry);
-      x.give(f, k, a.kb * 2, entry);
-      y.give(f, v, a.vb * 2, entry);
-    } else {
-      x.give(f, k, a.kb * 2, entry);
-      y.take(f, v, a.vb * 2, entry);
-      y.give(f, v, a.vb * 2, entry);
-    }
-    return;
+    x.take(f, at, beam, entry);
+    constexpr bool kBoth = NB * sizeof(V) <= 128;  // where the registers hold both tiles' columns
+    if (kBoth) y.take(f, then, beam, second);
+    x.give(f, at, beam, entry);
+    if (!kBoth) y.take(f, then, beam, second);
+    y.give(f, then, beam, second);
   }
-  const int64_t e0 = (int64_t)(blockIdx.x - tiles) * 256 + threadIdx.x;
-  if (e0 - threadIdx.x >= most) return;
-  const int entry = e0 < most ? (int)e0 : kNoEntry;
-  const int64_t first = ((b * beams * a.heads + h) * a.capacity + e0) * 4, beam = a.heads * a.capacity * 4;
-  char *account = reinterpret_cast<char *>(a.account) + first, *positions = reinterpret_cast<char *>(a.positions) + first;
-  Column<NB, uint32_t> x, y;
-  if (a.account != nullptr) x.take(f, account, beam, entry);
-  if (a.positions != nullptr) y.take(f, positions, beam, entry);
-  if (a.account != nullptr) x.give(f, account, beam, entry);
-  if (a.positions != nullptr) y.give(f, positions, beam, entry);
+  if (a.account == nullptr && a.positions == nullptr) return;
+  // the workgroups behind those of the keys and values, or where there are none (very long caches), all
+  const int64_t before = (int64_t)gridDim.x > parts ? parts : 0;
+  for (int64_t part = (int64_t)blockIdx.x - before; part >= 0; part += gridDim.x - before) {
+    const int64_t e0 = part * 256 + threadIdx.x;
+    if (part * 256 >= most) break;
+    const int entry = e0 < most ? (int)e0 : kNoEntry;
+    const int64_t first = ((b * beams * a.heads + h) * a.capacity + e0) * 4, beam = a.heads * a.capacity * 4;
+    char *account = reinterpret_cast<char *>(a.account) + first, *positions = reinterpret_cast<char *>(a.positions) + first;
+    Column<NB, uint32_t> x, y;
+    if (a.account != nullptr) x.take(f, account, beam, entry);
+    if (a.positions != nullptr) y.take(f, positions, beam, entry);
+    if (a.account != nullptr) x.give(f, account, beam, entry);
+    if (a.positions != nullptr) y.give(f, positions, beam, entry);
+  }
 }
 
 template <int NB, class V>
 hipError_t reorder(const ReorderArgs &a, hipStream_t s) {
   const int per = a.width * 2 / (int)sizeof(V), tile = 256 / per;
-  const int64_t tiles = (a.capacity + tile - 1) / tile;
+  const int64_t parts = (a.capacity + 2 * tile - 1) / (2 * tile) * 2;
   const int64_t extra = a.account != nullptr || a.positions != nullptr ? (a.capacity + 255) / 256 : 0;
-  if (tiles + extra > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
-  reorder_kernel<NB, V><<<rows_grid((unsigned)(tiles + extra), a.searches * a.heads), dim3(256), 0, s>>>(a, tile, (int)tiles);
+  const int64_t groups = parts + extra <= kMostGroups ? parts + extra : kMostGroups;
+  reorder_kernel<NB, V><<<rows_grid((unsigned)groups, a.searches * a.heads), dim3(256), 0, s>>>(a, tile, parts);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_reorder(const ReorderArgs &a, hipStream_t s) {
-  // a thread's registers hold the column: 16 bytes of up to 16 beams, 4 of up to 64
+  // a thread's registers hold the column: 16 bytes of up to 16 beams, 8 of up to 64
   if (a.beams <= 4) return reorder<4, u32x4>(a, s);
   if (a.beams <= 8) return reorder<8, u32x4>(a, s);
   if (a.beams <= 16) return reorder<16, u32x4>(a, s);
-  return reorder<64, uint32_t>(a, s);
+  if (a.beams <= 32) return reorder<32, u32x2>(a, s);
+  return reorder<64, u32x2>(a, s);
 }
 
 }  // namespace lapsum
