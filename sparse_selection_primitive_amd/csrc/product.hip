@@ -7,6 +7,7 @@
 // expert and rows from the offsets: tiles are counted through the experts in order, one wave's lanes a
 // few experts each.
 #include <cmath>
+#include <type_traits>
 
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
@@ -199,51 +200,58 @@ struct Side {
   static constexpr int kLoads = SIZE * kDepth * 2 / 1024 / WAVES;
   const char *at;     // of the step
   int64_t advance;    // bytes from step to step
+  int step;           // elements between rows of memory
   int whole, rest;    // bytes of the window of a whole step and of the last one, where that is not whole
   uint32_t to;        // LDS of this wave's first load, of the first stage
-  uint32_t offset[kLoads];
+  uint32_t offset;    // of this lane's part of the wave's first load
   int chunk;          // NEXT: the lane's chunk of the step's sum
 
-  // first: the element at the tile's first place and the sum's first element; `stride` between rows of memory;
-  // `places` of the tile and `sum` elements are there
-  LDEV void start(const T *first, int64_t stride, int places, int sum, uint32_t lds) {
+  // rows of memory between the wave's first load and load `i`
+  static constexpr int rows_to(int i) {
+    if (!NEXT) return i * (WAVES * 64 / (SIZE / 8));
+    if (!SPREAD) return i * WAVES * 16;
+    return i * WAVES / 8 * 128 + i * WAVES % 8;  // 16 rows a wave, 8 such to 128 places
+  }
+  LDEV void start(int64_t stride, uint32_t lds) {
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    at = reinterpret_cast<const char *>(first);
     to = lds + wave * 1024;
-    const int left = sum % kDepth, step = (int)stride;
+    step = (int)stride;
+    at = nullptr;
+    whole = rest = 0;
     if (NEXT) {
       advance = kDepth * 2;
-      whole = ((places - 1) * step + kDepth) * 2;
-      rest = ((places - 1) * step + left) * 2;
       chunk = lane % 4 ^ (lane / 8 & 3);  // the same for all loads: their rows are 16 apart
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int row = (i * WAVES + wave) * 16 + lane / 4;
-        const int place = SPREAD ? row / 128 * 128 + row % 16 * 8 + row / 16 % 8 : row;
-        offset[i] = (uint32_t)(place * step * 2) + (uint32_t)(chunk * 16);
-      }
+      static_assert(!NEXT || !SPREAD || 8 % WAVES == 0, "the places of a wave's loads");
+      const int place = SPREAD ? lane / 4 * 8 + wave : wave * 16 + lane / 4;
+      offset = (uint32_t)(place * step * 2) + (uint32_t)(chunk * 16);
     } else {
       constexpr int kPer = SIZE / 8;  // chunks of a row
+      static_assert(NEXT || WAVES * 64 % kPer == 0, "a wave's loads are whole rows apart");
+      const int x = wave * 64 + lane;
       advance = kDepth * stride * 2;
-      whole = ((kDepth - 1) * step + places) * 2;
-      rest = ((left - 1) * step + places) * 2;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int x = (i * WAVES + wave) * 64 + lane;
-        offset[i] = (uint32_t)(x / kPer * step * 2) + (uint32_t)(x % kPer * 16);
-      }
+      offset = (uint32_t)(x / kPer * step * 2) + (uint32_t)(x % kPer * 16);
     }
+  }
+  // To a tile: the element at its first place and the sum's first element; places and elements of the sum that are there.
+  LDEV void aim(const T *first, int places, int sum) {
+    at = reinterpret_cast<const char *>(first);
+    places = places < SIZE ? places : SIZE;
+    const int left = sum % kDepth;
+    whole = NEXT ? ((places - 1) * step + kDepth) * 2 : ((kDepth - 1) * step + places) * 2;
+    rest = NEXT ? ((places - 1) * step + left) * 2 : ((left - 1) * step + places) * 2;
   }
   // The step's part, of which `left` elements of the sum are there (none or fewer: zeros), to LDS: load `i` of this wave.
   window_t window;
-  uint32_t none;
+  uint32_t from;
   LDEV void begin(int left) {
     const int bytes = left >= kDepth ? whole : (left > 0 ? rest : 0);
     window = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, bytes, 0x00020000);
-    none = NEXT && chunk * 8 >= left ? kNowhere : 0u;
+    from = NEXT && chunk * 8 >= left ? kNowhere : offset;
     at += advance;
   }
-  LDEV void load(int i, uint32_t stage) const { load_to_lds(window, to + stage + i * (WAVES * 1024), offset[i] | none); }
+  LDEV void load(int i, uint32_t stage) const {
+    load_to_lds(window, to + stage + i * (WAVES * 1024), from + (uint32_t)(rows_to(i) * step * 2));
+  }
 };
 
 // two 16-bit elements, the low or the high ones of two words
@@ -315,11 +323,15 @@ struct Tile {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // places [0, m) x [0, n) of the tile
+  // Places [0, m) x [0, n) of the tile.  Always kStores stores of a wave, so that they can be counted.
+  static constexpr int kStores = kFrags * 4;
   LDEV void store(T *out, int64_t stride, int m, int n) const {
     const int lane = lane_id(), wave = threadIdx.x / 64, wm = wave / WAVES_N, wn = wave % WAVES_N;
-    const int col = wn * 128 + lane % 16 * 8;
-    if (col >= n) return;
+    const int col = wn * 128 + lane % 16 * 8, step = (int)stride;
+    m = m < kM ? m : kM;
+    n = n < kN ? n : kN;
+    const window_t window = __builtin_amdgcn_make_buffer_rsrc(out, 0, ((m - 1) * step + n) * 2, 0x00020000);
+    const uint32_t none = col < n ? 0u : kNowhere;
 #pragma unroll
     for (int i = 0; i < kFrags; ++i)
 #pragma unroll
@@ -328,8 +340,16 @@ struct Tile {
         pack_t<T> v;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = (T)c[i][j][r];
-        if (row < m) store_pack(out + row * stride + col, v);
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), window,
+                                               (int)((uint32_t)(row * step * 2 + col * 2) | none), 0, 0);
       }
+  }
+  LDEV void clear() {
+#pragma unroll
+    for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[i][j] = f32x4{};
   }
 };
 
@@ -339,121 +359,201 @@ LDEV void arrived() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
 }
 
-// Workgroups go round the eight dies; each die takes a run of tiles that share factors.
-LDEV int tile_of_workgroup(int total) {
-  const int each = (total + 7) / 8, i = blockIdx.x / 8, t = blockIdx.x % 8 * each + i;
-  return i < each && t < total ? t : -1;
-}
+// Tiles of rows counted through the ranges, in LDS: before[g] of them come before range g.
+struct RowTable {
+  int before[LAPSUM_MAX_EXPERTS + 3];
+  LDEV int total(const ProductArgs &p) const { return __builtin_amdgcn_readfirstlane(before[p.experts + 2]); }
+  LDEV void fill(const ProductArgs &p, int size) {
+    if (threadIdx.x < 64) {
+      RowTiles all;
+      all.count(p, size);
+      const int ranges = p.experts + 2, first = lane_id() * all.per;
+      int at = all.upto - all.mine;
+#pragma unroll
+      for (int i = 0; i < RowTiles::kBounds; ++i)
+        if (i < all.per && first + i < ranges) {
+          before[first + i] = at;
+          at += RowTiles::tiles_of(all.bound[i], all.bound[i + 1], size);
+        }
+      for (int i = RowTiles::kBounds; i < all.per && first + i < ranges; ++i) {
+        before[first + i] = at;
+        at += RowTiles::tiles_of(range_begin(p, first + i), range_begin(p, first + i + 1), size);
+      }
+      if (lane_id() == 63) before[ranges] = all.upto;
+    }
+    __syncthreads();
+  }
+  // the index-th tile of `size` rows; index below total().  Every lane of the wave asks.
+  LDEV RowTile find(const ProductArgs &p, int size, int index) const {
+    const int ranges = p.experts + 2, per = (ranges + 63) / 64, lane = lane_id();
+    const auto end = [&](int g) { return before[g + 1 < ranges ? g + 1 : ranges]; };
+    const int part = __builtin_ctzll(__ballot(end(lane * per + per - 1) > index)) * per;
+    // per is at most 17
+    const int g = part + __builtin_ctzll(__ballot(lane >= per || end(part + lane) > index));
+    const int a = __builtin_amdgcn_readfirstlane(range_begin(p, g));
+    const int b = __builtin_amdgcn_readfirstlane(range_begin(p, g + 1));
+    RowTile t;
+    t.expert = g >= 1 && g <= p.experts ? g - 1 : -1;
+    t.first = a + (index - __builtin_amdgcn_readfirstlane(before[g])) * size;
+    t.end = t.first + size < b ? t.first + size : b;
+    return t;
+  }
+};
 
+template <class T>
+struct TilePlace {
+  const T *a, *b;
+  T *out;
+  int m, n, sum;  // places that are there (or more than the tile holds), elements of the sum
+};
+
+// Workgroups stay, as many as there is room for, and take tile after tile, so that a tile's first loads are under way
+// while the last one is still multiplied and stored.  They go round the eight dies; each die takes a run of tiles,
+// which share factors.
+//
+// What loads is ahead of what multiplies by kStages steps, in whatever tile that is; tiles have an even number of steps
+// (the last may be zeros), so that the two sets of operands change places evenly.
 template <class T, int WM, int WAVES_M, int WAVES_N, int kStages, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
 __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 2) void product_tile_kernel(ProductArgs p) {
   using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
   constexpr int kA = Work::kM * kDepth, kStage = kA + Work::kN * kDepth;
   __shared__ T lds[kStages * kStage];
   lds_poison(lds);
-  const int tiles_n = (p.n + Work::kN - 1) / Work::kN;
-  const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
-  T *out = static_cast<T *>(p.c);
-  int m, n0, sum;  // places of the tile, its first column, elements of the sum
+  const int tiles_n = (p.n + Work::kN - 1) / Work::kN, tiles_m = SUM_ROWS ? (p.m + Work::kM - 1) / Work::kM : 0;
+  int total;
+  __shared__ std::conditional_t<SUM_ROWS, int, RowTable> table;
+  lds_poison(table);
   if constexpr (SUM_ROWS) {
-    const int tiles_m = (p.m + Work::kM - 1) / Work::kM;
-    const int t = tile_of_workgroup(tiles_m * tiles_n * p.experts);
-    if (t < 0) return;
-    const int e = t / (tiles_m * tiles_n), in = t % (tiles_m * tiles_n), m0 = in % tiles_m * Work::kM;
-    n0 = in / tiles_m * Work::kN;
-    const int k0 = offset_of(p, e), k1 = offset_of(p, e + 1);
-    sum = k1 - k0;
-    m = p.m - m0;
-    a += k0 * p.ak + m0;
-    b += k0 * p.bk + n0;
-    out += e * p.ce + m0 * p.cm + n0;
+    total = tiles_m * tiles_n * p.experts;
   } else {
-    RowTiles all;
-    all.count(p, Work::kM);
-    const int rows = all.total(), t = tile_of_workgroup(rows * tiles_n);
-    if (t < 0) return;
-    // kGroup tiles of rows go through the columns together, so that each column of a matrix is read once for them
-    constexpr int kGroup = 8;
-    const int first = t / (kGroup * tiles_n) * kGroup, g = rows - first < kGroup ? rows - first : kGroup;
-    const int in = t - first * tiles_n;
-    RowTile r;
-    if (!all.find(p, Work::kM, first + in % g, r)) return;
-    n0 = in / g * Work::kN;
-    m = r.end - r.first;
-    sum = r.expert < 0 ? 0 : p.k;
-    a += r.first * p.am;
-    b += (r.expert < 0 ? 0 : r.expert) * p.be + n0 * p.bn;
-    out += r.first * p.cm + n0;
+    table.fill(p, Work::kM);
+    total = table.total(p) * tiles_n;
   }
-  const int n = p.n - n0;
-  Work w;
-#pragma unroll
-  for (int i = 0; i < Work::kFrags; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w.c[i][j] = f32x4{};
-  if (sum > 0) {
-    typename Work::A sa;
-    typename Work::B sb;
-    sa.start(a, A_NEXT ? p.am : p.ak, m < Work::kM ? m : Work::kM, sum, lds_at(lds));
-    sb.start(b, B_NEXT ? p.bn : p.bk, n < Work::kN ? n : Work::kN, sum, lds_at(lds + kA));
-    // Step t computes on what the step before has read from LDS, reads what the next one computes on, and asks for
-    // what is kStages steps away, whose place step t's own part has left.  Past the end zeros are asked for, so that
-    // as many loads are under way in every step.
-    int to = 0, from = 0, asked = sum;
-    const int wave = threadIdx.x / 64;
-    const int place_a = decltype(Work::Operands::a)::place(wave / WAVES_N * WM);
-    const int place_b = kA + decltype(Work::Operands::b)::place(wave % WAVES_N * 128);
-    const auto begin = [&] {
-      sa.begin(asked);
-      sb.begin(asked);
-      asked -= kDepth;
-    };
-    const auto load = [&](int i) {
-      if (i < Work::A::kLoads)
-        sa.load(i, to * 2);
-      else
-        sb.load(i - Work::A::kLoads, to * 2);
-    };
-    const auto after = [&](int stage) { return stage == (kStages - 1) * kStage ? 0 : stage + kStage; };
-    const auto step = [&](const typename Work::Operands &now, typename Work::Operands &next) {
-      arrived<(kStages - 2) * Work::kLoads>();
-      from = after(from);
-      const T *pa = lds + from + place_a, *pb = lds + from + place_b;
-      w.step(now, [&](int j) {
-#pragma unroll
-        for (int i = j * Work::kReadsA / 8; i < (j + 1) * Work::kReadsA / 8; ++i) next.a.read(i, pa);
-        next.b.read(j, pb);
-#pragma unroll
-        for (int i = (j * Work::kLoads + 7) / 8; i < ((j + 1) * Work::kLoads + 7) / 8; ++i) load(i);
-        if (j == 7) {
-          begin();  // the next step's
-          to = after(to);
-        }
-      });
-    };
-#pragma unroll 1
-    for (int s = 0; s < kStages; ++s) {
-      begin();
-#pragma unroll
-      for (int i = 0; i < Work::kLoads; ++i) load(i);
-      to = after(to);
+  const int each = (total + 7) / 8, round = gridDim.x / 8;
+  // this workgroup's index-th tile
+  const auto place = [&](int index, TilePlace<T> &x) {
+    const int i = index * round + (int)blockIdx.x / 8, t = (int)blockIdx.x % 8 * each + i;
+    if (i >= each || t >= total) return false;
+    x.a = static_cast<const T *>(p.a);
+    x.b = static_cast<const T *>(p.b);
+    x.out = static_cast<T *>(p.c);
+    int n0;
+    if constexpr (SUM_ROWS) {
+      const int e = t / (tiles_m * tiles_n), in = t % (tiles_m * tiles_n), m0 = in % tiles_m * Work::kM;
+      n0 = in / tiles_m * Work::kN;
+      const int k0 = offset_of(p, e), k1 = offset_of(p, e + 1);
+      x.sum = k1 - k0;
+      x.m = p.m - m0;
+      x.a += k0 * p.ak + m0;
+      x.b += k0 * p.bk + n0;
+      x.out += e * p.ce + m0 * p.cm + n0;
+    } else {
+      // kGroup tiles of rows go through the columns together, so that each column of a matrix is read once for them
+      constexpr int kGroup = 8;
+      const int rows = total / tiles_n, first = t / (kGroup * tiles_n) * kGroup;
+      const int g = rows - first < kGroup ? rows - first : kGroup, in = t - first * tiles_n;
+      const RowTile r = table.find(p, Work::kM, first + in % g);
+      n0 = in / g * Work::kN;
+      x.m = r.end - r.first;
+      x.sum = r.expert < 0 ? 0 : p.k;
+      x.a += r.first * p.am;
+      x.b += (r.expert < 0 ? 0 : r.expert) * p.be + n0 * p.bn;
+      x.out += r.first * p.cm + n0;
     }
-    begin();
-    typename Work::Operands x, y;
-    arrived<(kStages - 1) * Work::kLoads>();
+    x.n = p.n - n0;
+    return true;
+  };
+
+  TilePlace<T> now;
+  if (!place(0, now)) return;
+  typename Work::A sa;
+  typename Work::B sb;
+  sa.start(A_NEXT ? p.am : p.ak, lds_at(lds));
+  sb.start(B_NEXT ? p.bn : p.bk, lds_at(lds + kA));
+  int ahead = 0, asked = 0;  // the next tile to load; what is left of the sum of the one that is loaded
+  int to = 0, from = 0, fresh = 0;
+  const int wave = threadIdx.x / 64;
+  const int place_a = decltype(Work::Operands::a)::place(wave / WAVES_N * WM);
+  const int place_b = kA + decltype(Work::Operands::b)::place(wave % WAVES_N * 128);
+  bool more = true, half = false;  // half: a tile's second step of two is next
+  const auto begin = [&] {
+    if (asked <= 0 && !half && more) {
+      TilePlace<T> x;
+      do {
+        more = place(ahead++, x);
+      } while (more && x.sum <= 0);
+      if (more) {
+        sa.aim(x.a, x.m, x.sum);
+        sb.aim(x.b, x.n, x.sum);
+        asked = x.sum;
+      }
+    }
+    sa.begin(asked);
+    sb.begin(asked);
+    asked -= kDepth;
+    half = !half;
+  };
+  const auto load = [&](int i) {
+    if (i < Work::A::kLoads)
+      sa.load(i, to * 2);
+    else
+      sb.load(i - Work::A::kLoads, to * 2);
+  };
+  const auto after = [&](int stage) { return stage == (kStages - 1) * kStage ? 0 : stage + kStage; };
+  Work w;
+  // Step t computes on what the step before has read from LDS, reads what the next one computes on, and asks for
+  // what is kStages steps away, whose place step t's own part has left.  Past the end zeros are asked for, so that
+  // as many loads are under way in every step.
+  const auto step = [&](const typename Work::Operands &now, typename Work::Operands &next) {
+    // stores count as loads do, for as long as loads from before them are waited for
+    if (fresh > 0) {
+      --fresh;
+      arrived<(kStages - 2) * Work::kLoads + Work::kStores>();
+    } else {
+      arrived<(kStages - 2) * Work::kLoads>();
+    }
+    from = after(from);
+    const T *pa = lds + from + place_a, *pb = lds + from + place_b;
+    w.step(now, [&](int j) {
 #pragma unroll
-    for (int i = 0; i < Work::kReadsA; ++i) x.a.read(i, lds + place_a);
+      for (int i = j * Work::kReadsA / 8; i < (j + 1) * Work::kReadsA / 8; ++i) next.a.read(i, pa);
+      next.b.read(j, pb);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x.b.read(i, lds + place_b);
+      for (int i = (j * Work::kLoads + 7) / 8; i < ((j + 1) * Work::kLoads + 7) / 8; ++i) load(i);
+      if (j == 7) {
+        begin();  // the next step's
+        to = after(to);
+      }
+    });
+  };
 #pragma unroll 1
-    for (; sum > 0; sum -= 2 * kDepth) {
+  for (int s = 0; s < kStages; ++s) {
+    begin();
+#pragma unroll
+    for (int i = 0; i < Work::kLoads; ++i) load(i);
+    to = after(to);
+  }
+  begin();
+  typename Work::Operands x, y;
+  arrived<(kStages - 1) * Work::kLoads>();
+#pragma unroll
+  for (int i = 0; i < Work::kReadsA; ++i) x.a.read(i, lds + place_a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x.b.read(i, lds + place_b);
+#pragma unroll 1
+  for (int index = 1;; ++index) {
+    w.clear();
+#pragma unroll 1
+    for (int sum = now.sum; sum > 0; sum -= 2 * kDepth) {
       step(x, y);
       step(y, x);
     }
-    // no load may reach LDS that is another workgroup's
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    w.store(now.out, p.cm, now.m, now.n);
+    fresh = kStages - 1;
+    if (!place(index, now)) break;
   }
-  w.store(out, p.cm, m, n);
+  // no load may reach LDS that is another workgroup's
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <class T, int WM, int WAVES_M, int WAVES_N, int STAGES, bool A_NEXT, bool B_NEXT, bool SUM_ROWS>
@@ -461,8 +561,9 @@ hipError_t tiles(const ProductArgs &p, hipStream_t s) {
   using Work = Tile<T, WM, WAVES_M, WAVES_N, A_NEXT, B_NEXT>;
   const int64_t nt = (p.n + Work::kN - 1) / Work::kN;
   const int64_t mt = SUM_ROWS ? (int64_t)((p.m + Work::kM - 1) / Work::kM) * p.experts : most_row_tiles(p, Work::kM);
-  const int64_t groups = (nt * mt + 7) / 8 * 8;
-  if (groups > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+  if (mt > 0x7FFFFFFF / nt) return hipErrorInvalidValue;  // more than memory holds
+  const int64_t room = 256 * 8 / (WAVES_M * WAVES_N);  // eight waves a compute unit
+  const int64_t groups = nt * mt < room ? (nt * mt + 7) / 8 * 8 : room;
   product_tile_kernel<T, WM, WAVES_M, WAVES_N, STAGES, A_NEXT, B_NEXT, SUM_ROWS>
       <<<dim3((unsigned)groups), dim3(64 * WAVES_M * WAVES_N), 0, s>>>(p);
   return hipGetLastError();
