@@ -171,6 +171,7 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs p) {
 // ------------------------------------------------------------- 16 bytes at a time
 // A window of memory that loads are held to: what lies past its end reads as zero.  Steps of a tile lie within 2^31 bytes.
 using window_t = __amdgpu_buffer_rsrc_t;
+constexpr int kStreamed = 2;  // not kept in the caches: the products are another's to read (3% of a training batch)
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
 
 // 64 x 16 bytes from the lanes' offsets to consecutive places of LDS from `to` on (bytes).  Written out, since the compiler
@@ -342,7 +343,7 @@ struct Tile {
         for (int j = 0; j < 8; ++j) v[j] = (T)c[i][j][r];
         typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), window,
-                                               (int)((uint32_t)(row * step * 2 + col * 2) | none), 0, 0);
+                                               (int)((uint32_t)(row * step * 2 + col * 2) | none), 0, kStreamed);
       }
   }
   LDEV void clear() {
@@ -693,12 +694,13 @@ bool whole(int64_t n) { return n % 8 == 0; }
 //    tiles 18.0); 256 experts of 2048 x 1024 with 24 rows 230 (tiles 205).
 //  - 128 x 256: 0.42 a step where every workgroup has a compute unit to itself, else a round of 512; or the matrices' way
 //    from memory.
-//  - 256 x 256: a round of 256 takes as long, and less is loaded: 8 experts of 4096 x 14336 with 2048 rows 1710 for
-//    1830, 64 experts of 2056 x 1416 with 469 rows (as many rounds of both) 328 for 366, 256 experts of 2048 x 1024 with
-//    256 (six rounds for five) 509 for 443.
+//  - 256 x 256 takes as long as 1.85 of those; where the sum lies next to each other in a matrix, so that its lines come in halves,
+//    1.6.  8 experts of 4096 x 14336 with 2048 rows 1740 for 1830, 256 experts of 2048 x 1024 with 256 510 for 443, of 1024
+//    x 2048, lines in halves, 440 for 489, 64 experts of 2056 x 1416 with 469 rows 328 for 366; their matrices' gradients
+//    468 for 515 (256) and 360 for 394 (64).
 enum Kind { kFew16, kFew32, kTile128, kTile256 };
-Kind tile_kind(double tiles128, double tiles256) {
-  return tiles128 > 256 && std::ceil(tiles256 / 256) <= std::ceil(tiles128 / 512) ? kTile256 : kTile128;
+Kind tile_kind(double tiles128, double tiles256, bool halves) {
+  return tiles128 > 256 && tiles256 * (halves ? 1.6 : 1.85) < tiles128 ? kTile256 : kTile128;
 }
 Kind rows_kind(const ProductArgs &p) {
   const double rows = (double)p.rows, met = p.experts * (1.0 - std::exp(-rows / p.experts)), x = rows / met;
@@ -710,7 +712,7 @@ Kind rows_kind(const ProductArgs &p) {
   const double tile = 3 + std::fmax(step * p.k / 32, met * matrix / 5.2);
   if (few16 <= few32 && few16 < tile) return kFew16;
   if (few32 < tile) return kFew32;
-  return tile_kind(tiles128, tiles(256) * columns);
+  return tile_kind(tiles128, tiles(256) * columns, p.bk == 1);
 }
 
 template <class T, bool B_NEXT>
@@ -741,7 +743,7 @@ hipError_t weights_of(const ProductArgs &p, hipStream_t s) {
   if (whole(p.a) && whole(p.b) && whole(p.c) && whole(p.ak) && whole(p.bk) && whole(p.ce) && whole(p.cm) &&
       whole(p.m) && whole(p.n))
     return tile_kind(std::ceil(p.m / 128.0) * std::ceil(p.n / 256.0) * p.experts,
-                     std::ceil(p.m / 256.0) * std::ceil(p.n / 256.0) * p.experts) == kTile256
+                     std::ceil(p.m / 256.0) * std::ceil(p.n / 256.0) * p.experts, false) == kTile256
                ? tiles<T, 64, 4, 2, 4, false, false, true>(p, s)
                : tiles<T, 64, 2, 2, 3, false, false, true>(p, s);
   const unsigned nt = (unsigned)((p.n + kAny - 1) / kAny);
