@@ -90,6 +90,36 @@ def test_many_rows(L, sizes, n, m, stored):
     check(L, *inputs(offsets[-1], n, m, offsets, "fp16", stored))
 
 
+def check_sample(L, xs, w, offsets, dys, experts):
+    """As check, for all rows of some experts: larger products than the CPU forms in time."""
+    got, bounds = L.expert_product_forward(xs, w, offsets), offsets.tolist()
+    dx, d = L.expert_product_backward(dys, xs, w, offsets)
+    for e in experts:
+        mine = slice(bounds[e], bounds[e + 1])
+        if mine.start == mine.stop:
+            assert (d[e] == 0).all()
+            continue
+        x, m, dy = xs[mine].double(), w[e].double(), dys[mine].double()
+        longest = max(1, mine.stop - mine.start)
+        for a, b, size, terms in ((got[mine], x @ m, x.abs() @ m.abs(), x.shape[1]),
+                                  (dx[mine], dy @ m.t(), dy.abs() @ m.t().abs(), dy.shape[1]),
+                                  (d[e], x.t() @ dy, x.t().abs() @ dy.abs(), longest)):
+            plain.check_product(a, (b.cpu(), size.cpu(), terms), f"expert {e}")
+
+
+@pytest.mark.parametrize("stored", ["in_out", "out_in"])
+def test_tiles_of_every_kind(L, stored):
+    """Sizes that go to each of the kernels: few rows of few and of many experts, some rows, tiles of 128 and of 256 rows; in
+    each the sum is no whole number of steps, and neither rows nor columns are of tiles."""
+    for experts, rows, n, m in ((3, 5, 200, 520), (200, 230, 200, 2056), (4, 300, 1032, 2056), (40, 2500, 1032, 1032),
+                                (70, 33000, 264, 1288), (5, 9000, 776, 1544)):
+        g = torch.Generator().manual_seed(rows)
+        p = torch.softmax(0.7 * torch.randn(experts, generator=g), 0)
+        sizes = torch.bincount(torch.multinomial(p, rows, replacement=True, generator=g), minlength=experts).tolist()
+        check_sample(L, *inputs(rows, n, m, offsets_of(sizes), "bf16", stored),
+                     sorted({0, 1, experts // 2, experts - 1, sizes.index(max(sizes)), sizes.index(min(sizes))}))
+
+
 @pytest.mark.parametrize("n,m", [(128, 256), (37, 50)])
 def test_rows_of_no_expert_are_zero(L, n, m):
     """Rows before the first expert's and behind the last one's (another device's, or dropped pairs): NaN there stays
