@@ -129,10 +129,17 @@ struct Best {
 };
 constexpr double kNone = -INFINITY;
 
+struct alignas(16) Beam {
+  double base;  // scores - log S; -inf: no continuation
+  float top;    // M
+  int done;     // ended
+  LDEV double score(float x) const {
+    const double s = base + (x == top ? 0.0 : (double)x - (double)top);
+    return s > kNone ? s : kNone;  // NaN is none
+  }
+};
 struct Shared {
-  double base[LAPSUM_MAX_BEAMS];  // scores - log S; -inf: no continuation
-  float top[LAPSUM_MAX_BEAMS];    // M
-  int done[LAPSUM_MAX_BEAMS];     // ended
+  Beam beam[LAPSUM_MAX_BEAMS];
   double row_best[kRows];
   double least;                   // no candidate below it is among the k best
   int listed;
@@ -143,12 +150,6 @@ struct Shared {
   double wave_score[kThreads / 64];
   int wave_place[kThreads / 64];
 };
-
-LDEV double score_of(const Shared &sh, int beam, float x) {
-  const float top = sh.top[beam];
-  const double s = sh.base[beam] + (x == top ? 0.0 : (double)x - (double)top);
-  return s > kNone ? s : kNone;  // NaN is none
-}
 
 LDEV int row_sum(int v) {  // over 16 lanes
   v += (int)xor_lanes<1>((uint32_t)v);
@@ -254,27 +255,25 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
     if (i < all) mine_top[j] = tops[i];  // of an ended beam whatever is there: not looked at
   }
   for (int i = wave; i < a.beams; i += kThreads / 64) {
+    // all asked for at once; what an ended beam's sums hold is not looked at
     const float score = a.scores[search * a.beams + i];
     const bool ended = a.ended != nullptr && a.ended[search * a.beams + i] != 0;
     float m = -INFINITY, s = 0.0f;
-    if (!ended) {
-      for (int c = lane; c < groups; c += 64) {
-        const float2 x = sums[i * groups + c];
-        join(m, s, x.x, x.y);
-      }
-      join_lanes<1>(m, s);
-      join_lanes<2>(m, s);
-      join_lanes<4>(m, s);
-      join_lanes<8>(m, s);
-      join_lanes<16>(m, s);
-      join_lanes<32>(m, s);
+    for (int c = lane; c < groups; c += 64) {
+      const float2 x = sums[i * groups + c];
+      join(m, s, x.x, x.y);
     }
+    join_lanes<1>(m, s);
+    join_lanes<2>(m, s);
+    join_lanes<4>(m, s);
+    join_lanes<8>(m, s);
+    join_lanes<16>(m, s);
+    join_lanes<32>(m, s);
     if (lane == 0) {
       const bool finite = score > -INFINITY && score < INFINITY;
       const bool none = !finite || (!ended && !(s > 0.0f));  // a NaN sum, or nothing above -inf
-      sh.base[i] = none ? kNone : (ended ? (double)score : (double)score - log_pos((double)s));
-      sh.top[i] = ended || none ? 0.0f : m;
-      sh.done[i] = ended;
+      sh.beam[i] = Beam{none ? kNone : (ended ? (double)score : (double)score - log_pos((double)s)),
+                        ended || none ? 0.0f : m, ended};
     }
   }
   if (threadIdx.x == 0) sh.listed = 0;
@@ -289,8 +288,8 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
     mine_score[j] = kNone;
     if (i < all) {
       const int beam = (int)((uint64_t)i * a.chunk_magic >> 32);
-      mine_score[j] = !sh.done[beam] ? score_of(sh, beam, mine_top[j])
-                                     : (i - beam * a.chunks == end_part ? sh.base[beam] : kNone);
+      const Beam x = sh.beam[beam];
+      mine_score[j] = !x.done ? x.score(mine_top[j]) : (i - beam * a.chunks == end_part ? x.base : kNone);
     }
   }
   const auto each_part = [&](const auto &f) {
@@ -332,15 +331,16 @@ __global__ __launch_bounds__(kThreads) void beam_select_kernel(BeamArgs a) {
       if (part < 0) continue;
       const int beam = (int)((uint64_t)part * a.chunk_magic >> 32);
       const int t = (part - beam * a.chunks) * a.chunk + (u & ((1 << shift) - 1)) * N;
-      if (sh.done[beam]) {
-        if (a.end_token >= t && a.end_token < t + N) f(Best{sh.base[beam], beam * a.vocab + a.end_token});
+      if (t >= a.vocab) continue;
+      const Beam y = sh.beam[beam];
+      if (y.done) {
+        if (a.end_token >= t && a.end_token < t + N) f(Best{y.base, beam * a.vocab + a.end_token});
         continue;
       }
-      if (t >= a.vocab) continue;
       float x[N];
       load_tokens(static_cast<const T *>(a.logits) + (search * a.beams + beam) * a.stride, t, a.vocab, x);
 #pragma unroll
-      for (int j = 0; j < N; ++j) f(Best{score_of(sh, beam, x[j]), beam * a.vocab + t + j});
+      for (int j = 0; j < N; ++j) f(Best{y.score(x[j]), beam * a.vocab + t + j});
     }
   };
   select(sh, a.k, each_token);
