@@ -468,7 +468,7 @@ lapsum_status lapsum_cache_evict(const lapsum_cache *cache, const float *account
  * [outputs, inputs]) and the other at least the size that it passes. */
 typedef struct lapsum_experts {
     void *w;       /* device */
-    int32_t dtype; /* LAPSUM_BF16 or LAPSUM_F16 */
+    int32_t dtype; /* lapsum_dtype */
     int32_t reserved;
     int64_t experts, inputs, outputs; /* inputs and outputs at most LAPSUM_MAX_EXPERT_WIDTH */
     int64_t stride_expert, stride_input, stride_output; /* elements */
@@ -486,11 +486,12 @@ typedef struct lapsum_experts {
  * another's, NaN and infinities included.
  *   xs      device [rows, inputs] of the matrices' type, rows `xs_stride` elements apart
  *   dys     device [rows, outputs], rows `dys_stride` elements apart
- *   ys, dxs device, contiguous;  dw: as w, its own layout, no two elements in one place
+ *   ys, dxs device, contiguous;  dw: as w, its own layout, no two elements in one place; none of them
+ *           in the memory of what the call reads (LAPSUM_ERR_LAYOUT)
  *   offsets device [experts + 1], taken into 0 .. rows; of offsets that do not ascend it is
  *           not defined which rows of ys and dxs are written
- * rows <= LAPSUM_MAX_PAIRS.  Sizes, strides and pointers that are multiples of 16 bytes
- * are the fast ones; any others (of whole elements) are taken too. */
+ * rows <= LAPSUM_MAX_PAIRS.  The fast ones are bf16 and fp16 with sizes, strides and pointers that are multiples of 16
+ * bytes; fp32 (products in fp32), and any others of whole elements, go through a simple kernel. */
 lapsum_status lapsum_expert_product_forward(const void *xs, int64_t xs_stride, int64_t rows, const lapsum_experts *w,
                                             const int32_t *offsets, void *ys, void *stream);
 lapsum_status lapsum_expert_product_backward_rows(const void *dys, int64_t dys_stride, int64_t rows,
@@ -512,7 +513,7 @@ lapsum_status lapsum_expert_product_backward_weights(const void *xs, int64_t xs_
  *   ended      device [batch, beams] bytes, or NULL: a beam whose byte is not 0 has one continuation,
  *              end_token (in 0 .. vocab - 1), at its own score; its logits are not read
  *   k          1 .. LAPSUM_MAX_BEAMS, also beyond `beams` (twice as many, say)
- *   scores_out device [batch, k] fp32;  parents, tokens device [batch, k] int32
+ *   scores_out device [batch, k] fp32, not scores itself (LAPSUM_ERR_LAYOUT);  parents, tokens device [batch, k] int32
  * Scores are compared in fp64 (the sum of exponentials is an fp32 sum) and rounded to fp32 once.  A
  * token whose logit is -inf is no continuation; logits of +inf share the
  * probability equally, the others have none.  A beam with a NaN among its logits, without a logit above -inf,
@@ -528,7 +529,7 @@ lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batc
  * sequence b * beams + parents[b, j] was, in place, without a second cache: the entries below the parent's
  * length, and with them the accounts and positions.  Entries at that length and behind stay as they are.
  *   cache    batch a multiple of beams (at most LAPSUM_MAX_BEAMS); no two entries may share memory
- *            (LAPSUM_ERR_LAYOUT), as for the eviction
+ *            (LAPSUM_ERR_LAYOUT), as for the eviction; v may be k (the same pointer and strides), else they share none
  *   parents  device [batch / beams, beams] int32; one outside 0 .. beams - 1 leaves its sequence
  *            as it is, with length 0
  *   lengths  device [batch] int32, taken as 0 .. capacity

@@ -369,7 +369,7 @@ PyObject *cache_evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 // [experts, inputs, outputs], stored so or with inputs and outputs changed over
 bool matrices(const at::Tensor *w, lapsum_experts &e) {
-  if (w == nullptr || w->dim() != 3 || dtype_of(*w) < LAPSUM_BF16) return false;
+  if (w == nullptr || w->dim() != 3 || dtype_of(*w) < 0) return false;
   e = lapsum_experts{w->data_ptr(), dtype_of(*w),   0,           w->size(0),  w->size(1),
                      w->size(2),    w->stride(0), w->stride(1), w->stride(2)};
   return (e.stride_output == 1 && e.stride_input >= e.outputs) || (e.stride_input == 1 && e.stride_output >= e.inputs);

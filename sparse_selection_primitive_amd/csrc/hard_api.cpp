@@ -143,7 +143,7 @@ lapsum_status check_attend(const lapsum_cache *c, int64_t news, int64_t q_heads)
 
 lapsum_status check_experts(const lapsum_experts *w, int64_t rows) {
   if (!w) return LAPSUM_ERR_NULL;
-  if (w->dtype != LAPSUM_BF16 && w->dtype != LAPSUM_F16) return LAPSUM_ERR_OPTION;
+  if (!known_dtype(w->dtype)) return LAPSUM_ERR_OPTION;
   if (w->experts < 1 || w->experts > LAPSUM_MAX_EXPERTS || w->inputs < 1 || w->inputs > LAPSUM_MAX_EXPERT_WIDTH ||
       w->outputs < 1 || w->outputs > LAPSUM_MAX_EXPERT_WIDTH || rows < 1 || rows > LAPSUM_MAX_PAIRS)
     return LAPSUM_ERR_SHAPE;
@@ -158,6 +158,22 @@ lapsum_status check_row_stride(int64_t stride, int64_t width) {
 }
 // whether a matrix' outputs lie next to each other (of one column or row both hold)
 bool outputs_next(const lapsum_experts &w) { return w.stride_output == 1 && w.stride_input >= w.outputs; }
+
+// Whether two stretches of memory meet.
+bool meet(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+int64_t type_bytes(int32_t dtype) { return dtype == LAPSUM_F32 ? 4 : 2; }
+int64_t rows_bytes(int64_t rows, int64_t width, int64_t stride, int32_t dtype) {
+  return ((rows - 1) * stride + width) * type_bytes(dtype);
+}
+int64_t experts_bytes(const lapsum_experts &w) {  // strides that no memory holds count as the most there is
+  const __int128 last = (__int128)(w.experts - 1) * w.stride_expert + (w.inputs - 1) * w.stride_input +
+                        (w.outputs - 1) * w.stride_output + 1;
+  const __int128 bytes = last * type_bytes(w.dtype), most = (__int128)1 << 62;
+  return (int64_t)(bytes < most ? bytes : most);
+}
 
 ProductArgs product_args(const lapsum_experts &w, int64_t rows, const int32_t *offsets) {
   ProductArgs a{};
@@ -408,6 +424,9 @@ lapsum_status lapsum_expert_product_forward(const void *xs, int64_t xs_stride, i
   st = check_row_stride(xs_stride, w->inputs);
   if (st != LAPSUM_OK) return st;
   if (!xs || !w->w || !offsets || !ys) return LAPSUM_ERR_NULL;
+  const int64_t out = rows_bytes(rows, w->outputs, w->outputs, w->dtype);
+  if (meet(ys, out, xs, rows_bytes(rows, w->inputs, xs_stride, w->dtype)) || meet(ys, out, w->w, experts_bytes(*w)))
+    return LAPSUM_ERR_LAYOUT;
   ProductArgs a = product_args(*w, rows, offsets);
   a.a = xs;
   a.am = xs_stride;
@@ -451,6 +470,10 @@ lapsum_status lapsum_expert_product_backward_weights(const void *xs, int64_t xs_
   const int64_t across = next ? dw->inputs : dw->outputs, along = next ? dw->outputs : dw->inputs;
   const int64_t stride = next ? dw->stride_input : dw->stride_output;
   if (dw->experts > 1 && dw->stride_expert < stride * (across - 1) + along) return LAPSUM_ERR_LAYOUT;
+  const int64_t out = experts_bytes(*dw);
+  if (meet(dw->w, out, xs, rows_bytes(rows, dw->inputs, xs_stride, dw->dtype)) ||
+      meet(dw->w, out, dys, rows_bytes(rows, dw->outputs, dys_stride, dw->dtype)))
+    return LAPSUM_ERR_LAYOUT;
   ProductArgs a = product_args(*dw, rows, offsets);
   a.a = next ? xs : dys;
   a.b = next ? dys : xs;
@@ -480,6 +503,7 @@ lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batc
   if (row_stride < vocab) return LAPSUM_ERR_LAYOUT;
   if (ended && (end_token < 0 || end_token >= vocab)) return LAPSUM_ERR_OPTION;
   if (!logits || !scores || !scores_out || !parents || !tokens) return LAPSUM_ERR_NULL;
+  if (scores_out == scores) return LAPSUM_ERR_LAYOUT;  // of several searches one is read when another is written
   st = check_workspace(workspace, workspace_bytes, beam_bytes(batch, beams, vocab));
   if (st != LAPSUM_OK) return st;
   BeamArgs a{};
@@ -518,6 +542,9 @@ lapsum_status lapsum_cache_reorder(const lapsum_cache *cache, int64_t beams, con
   st = check_cache_pointers(cache);
   if (st != LAPSUM_OK) return st;
   ReorderArgs a{};
+  // keys that are the values as well move once
+  a.one = cache->k == cache->v && cache->k_stride_batch == cache->v_stride_batch &&
+          cache->k_stride_head == cache->v_stride_head && cache->k_stride_entry == cache->v_stride_entry;
   a.k = cache->k;
   a.v = cache->v;
   a.kb = cache->k_stride_batch;

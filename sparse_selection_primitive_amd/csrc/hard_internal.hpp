@@ -138,6 +138,7 @@ struct ReorderArgs {
   int64_t kb, kh, ke, vb, vh, ve;
   int64_t searches, heads, capacity;
   int beams, width;
+  bool one;                 // v is k
   const int32_t *parents, *lengths;
   float *account;           // or NULL
   int32_t *positions;       // or NULL

@@ -81,6 +81,7 @@ __global__ __launch_bounds__(256) void reorder_kernel(ReorderArgs a, int tile, i
     const int64_t e0 = part / 2 * (2 * tile);
     if (e0 >= most) break;
     const bool values = part % 2 != 0;
+    if (values && a.one) continue;
     const int64_t beam = (values ? a.vb : a.kb) * 2, head = (values ? a.vh : a.kh) * 2, step = (values ? a.ve : a.ke) * 2;
     const int per = a.width * 2 / (int)sizeof(V);  // columns of an entry
     const int e = threadIdx.x / per, c = (threadIdx.x - e * per) * (int)sizeof(V);

@@ -117,6 +117,8 @@ def _bind():
         spec = importlib.util.spec_from_file_location(__package__ + "._binding", _NATIVE_PATH)
         native = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(native)
+        if not all(hasattr(native, name) or name.endswith("_bytes") for name in _NATIVE_CALLS):
+            return  # built before these calls were there
         native.bind(*[ctypes.cast(getattr(lib, "lapsum_" + name), ctypes.c_void_p).value for name in _NATIVE_CALLS])
         native.on_failure(_check)
         _native = native
@@ -437,7 +439,7 @@ def _matrices(w, name):
     if not ((so == 1 and outputs <= si <= MAX_EXPERT_STRIDE) or (si == 1 and inputs <= so <= MAX_EXPERT_STRIDE)):
         w = w.contiguous()
         se, si, so = inputs * outputs, outputs, 1
-    return w, Experts(w.data_ptr(), _dtype(w, name, (BF16, F16)), 0, experts, inputs, outputs, se, si, so)
+    return w, Experts(w.data_ptr(), _dtype(w, name), 0, experts, inputs, outputs, se, si, so)
 
 
 def _expert_rows(x, name, w, width):
@@ -460,18 +462,18 @@ def _expert_offsets(offsets, w):
 
 def expert_product_forward(xs, w, offsets, *, out=None):
     """ys [rows, outputs]: rows in expert order times their expert's matrix, ys[r] = xs[r] @ w[e] for the rows
-    offsets[e]:offsets[e + 1].  w [experts, inputs, outputs] bf16 or fp16, stored so or with inputs and outputs changed
+    offsets[e]:offsets[e + 1].  w [experts, inputs, outputs] bf16, fp16 or fp32 (slower), stored so or with inputs and outputs changed
     over (a transposed view).  Rows of no expert give 0."""
     if _native is not None and out is None:
         done = _native.expert_product_forward(xs, w, offsets)
         if done is not None:
             return done
     _gpu(w, "w", 3)
-    _dtype(w, "w", (BF16, F16))
+    _dtype(w, "w")
     xs, stride = _expert_rows(xs, "xs", w, w.shape[1])
     offsets = _expert_offsets(offsets, w)
     ys = _out(out, "ys", w.dtype, (xs.shape[0], w.shape[2]), w.device)
-    if ys.numel() == 0 or w.shape[1] == 0:
+    if ys.numel() == 0 or w.numel() == 0:
         return ys.zero_()
     w, experts = _matrices(w, "w")
     _call(w.device, "lapsum_expert_product_forward", xs.data_ptr(), stride, xs.shape[0], experts, offsets.data_ptr(),
@@ -487,11 +489,11 @@ def expert_product_backward_rows(dys, w, offsets, *, out=None):
         if done is not None:
             return done
     _gpu(w, "w", 3)
-    _dtype(w, "w", (BF16, F16))
+    _dtype(w, "w")
     dys, stride = _expert_rows(dys, "dys", w, w.shape[2])
     offsets = _expert_offsets(offsets, w)
     dxs = _out(out, "dxs", w.dtype, (dys.shape[0], w.shape[1]), w.device)
-    if dxs.numel() == 0 or w.shape[2] == 0:
+    if dxs.numel() == 0 or w.numel() == 0:
         return dxs.zero_()
     w, experts = _matrices(w, "w")
     _call(w.device, "lapsum_expert_product_backward_rows", dys.data_ptr(), stride, dys.shape[0], experts,
@@ -508,7 +510,7 @@ def expert_product_backward_weights(dys, xs, w, offsets, *, out=None):
         if done is not None:
             return done
     _gpu(w, "w", 3)
-    _dtype(w, "w", (BF16, F16))
+    _dtype(w, "w")
     xs, xs_stride = _expert_rows(xs, "xs", w, w.shape[1])
     dys, dys_stride = _expert_rows(dys, "dys", w, w.shape[2])
     if xs.shape[0] != dys.shape[0]:

@@ -5,7 +5,7 @@ import math
 import torch
 
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
-LEAST = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}  # half of the smallest step
+LEAST = {torch.float32: 2.0 ** -149, torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}  # half of the smallest step
 
 
 def ranges(offsets, rows):
@@ -30,8 +30,9 @@ def products(xs, w, offsets, dys=None):
 
 
 def check_product(got, want, what=""):
-    """An fp32 sum of n products (exact in fp32) errs by at most n steps of 2^-23 of the sum of their magnitudes: n - 1
-    additions that may round or cut each step; its one rounding to the type by half a step."""
+    """An fp32 sum of n products (exact in fp32, or added without a rounding of their own) errs by at most n steps of 2^-23
+    of the sum of their magnitudes: n additions that may round or cut each step; its one rounding to the type by half a
+    step."""
     ref, size, n = want
     bound = HALF[got.dtype] * ref.abs() + LEAST[got.dtype] + (1 + HALF[got.dtype]) * n * 2.0 ** -23 * size
     err = (got.double().cpu() - ref).abs()

@@ -70,6 +70,15 @@ def test_constant_rows(L, vocab, value):
         assert (parents == -1).all() and (tokens == -1).all() and (s == -math.inf).all()
 
 
+def test_constant_rows_of_many_beams(L):
+    """More equal parts than the list holds."""
+    logits = torch.zeros(1, 64, 20000, device="cuda").bfloat16()
+    scores = torch.zeros(1, 64, device="cuda")
+    scores[0, :5] = -1.0
+    _, parents, tokens = check(L, logits, scores, 20)
+    assert parents.tolist() == [[5] * 20] and tokens.tolist() == [list(range(20))]
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_many_ties(L, dtype):
     g = torch.Generator().manual_seed(1)

@@ -80,6 +80,20 @@ def test_layouts(L):
     check(L, dict(k=both[..., 0, :], v=both[..., 1, :]), parents, lengths)
 
 
+@pytest.mark.parametrize("name", ["account", "positions"])
+def test_one_of_the_arrays(L, name):
+    s = state(4, 2, 300, 64)
+    check(L, {n: s[n] for n in ("k", "v", name)}, i32([[1, 1, 3, 2]]), i32([300, 290, 5, 257]))
+
+
+@pytest.mark.parametrize("beams", [3, 12, 20])
+def test_keys_that_are_the_values(L, beams):
+    k = torch.randn(beams, 2, 70, 64, device="cuda").bfloat16()
+    want, after = plain.reorder(dict(k=k), i32([[(i + 1) % beams for i in range(beams)]]), i32([70] * beams))
+    got = L.cache_reorder(k, k, i32([[(i + 1) % beams for i in range(beams)]]), i32([70] * beams))
+    assert got.tolist() == after.tolist() and torch.equal(k, want["k"])
+
+
 def test_twice_in_a_row_and_versions(L):
     s, lengths = state(4, 2, 50, 64), i32([50, 40, 30, 20])
     versions = {n: x._version for n, x in s.items()}

@@ -6,7 +6,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import search_plain as plain  # noqa: E402
 
-TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 
 
 @pytest.fixture(scope="module")
@@ -52,7 +52,7 @@ def offsets_of(sizes, first=0):
     return out
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("stored", ["in_out", "out_in"])
 @pytest.mark.parametrize("n,m", [(64, 64), (128, 256), (264, 136), (8, 512), (520, 8), (72, 1032)])
 def test_ragged(L, n, m, stored, dtype):
@@ -60,11 +60,12 @@ def test_ragged(L, n, m, stored, dtype):
     check(L, *inputs(offsets[-1], n, m, offsets, dtype, stored))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("stored", ["in_out", "out_in"])
 @pytest.mark.parametrize("n,m", [(1, 1), (1, 70), (33, 1), (7, 13), (65, 127), (100, 36), (131, 260)])
-def test_sizes_of_no_whole_16_bytes(L, n, m, stored):
+def test_sizes_of_no_whole_16_bytes(L, n, m, stored, dtype):
     offsets = offsets_of(RAGGED)
-    check(L, *inputs(offsets[-1], n, m, offsets, "bf16", stored))
+    check(L, *inputs(offsets[-1], n, m, offsets, dtype, stored))
 
 
 @pytest.mark.parametrize("stored", ["in_out", "out_in"])
@@ -138,11 +139,12 @@ def test_rows_of_no_expert_are_zero(L, n, m):
     assert (d[1] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("stored", ["in_out", "out_in"])
 @pytest.mark.parametrize("n,m,rows", [(128, 256, 5), (120, 200, 40), (264, 136, 400), (37, 50, 20)])
-def test_nothing_reaches_another_expert(L, n, m, rows, stored):
+def test_nothing_reaches_another_expert(L, n, m, rows, stored, dtype):
     """NaN and infinities of one expert's rows and matrix stay with it, tails of rows and sums included."""
-    xs, w, offsets, dys = inputs(3 * rows, n, m, [0, rows, 2 * rows, 3 * rows], "bf16", stored)
+    xs, w, offsets, dys = inputs(3 * rows, n, m, [0, rows, 2 * rows, 3 * rows], dtype, stored)
     xs[:rows], dys[2 * rows:], w[0], w[2] = float("nan"), float("inf"), float("nan"), float("inf")
     mine = slice(rows, 2 * rows)
     one = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
@@ -219,12 +221,17 @@ def test_nothing_to_do(L):
     assert dx.shape == (0, 16) and dw.shape == w.shape and (dw == 0).all()
     x, w = torch.zeros(5, 0, device="cuda").bfloat16(), torch.ones(3, 0, 24, device="cuda").bfloat16()
     assert (L.expert_product_forward(x, w, o) == 0).all() and L.expert_product_forward(x, w, o).shape == (5, 24)
+    none, first = torch.ones(0, 16, 24, device="cuda").bfloat16(), o[:1]  # no expert at all: the rows are nobody's
+    x, dy = torch.ones(5, 16, device="cuda").bfloat16(), torch.ones(5, 24, device="cuda").bfloat16()
+    assert (L.expert_product_forward(x, none, first) == 0).all()
+    dx, dw = L.expert_product_backward(dy, x, none, first)
+    assert (dx == 0).all() and dw.shape == (0, 16, 24)
 
 
 def test_refusals(L):
     xs, w, offsets, dys = inputs(20, 16, 24, [0, 10, 20], "bf16")
     for bad in (lambda: L.expert_product_forward(xs.float(), w, offsets), lambda: L.expert_product_forward(xs, w.float(), offsets),
-                lambda: L.expert_product_forward(xs.float(), w.float(), offsets), lambda: L.expert_product_forward(xs.half(), w, offsets),
+                lambda: L.expert_product_forward(xs.double(), w.double(), offsets), lambda: L.expert_product_forward(xs.half(), w, offsets),
                 lambda: L.expert_product_forward(dys, w, offsets), lambda: L.expert_product_forward(xs, w[0], offsets),
                 lambda: L.expert_product_forward(xs, w, offsets[:2]), lambda: L.expert_product_forward(xs, w, offsets.long()),
                 lambda: L.expert_product_forward(xs, w, offsets.cpu()), lambda: L.expert_product_forward(xs, w, offsets, out=xs),
@@ -233,6 +240,22 @@ def test_refusals(L):
                 lambda: L.expert_product(xs.cpu(), w, offsets)):
         with pytest.raises(L.LapsumError):
             bad()
+
+
+def test_outputs_in_the_memory_of_inputs_are_refused(L):
+    memory = torch.zeros(4000, device="cuda").bfloat16()
+    xs, w, dys = memory[:320].view(20, 16), memory[320:832].view(2, 16, 16), memory[832:1152].view(20, 16)
+    o = torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda")
+    free = memory[1152:1472].view(20, 16)
+    L.expert_product_forward(xs, w, o, out=free)
+    for out in (xs, memory[8:328].view(20, 16), memory[824:1144].view(20, 16), memory[310:630].view(20, 16)):
+        with pytest.raises(L.LapsumError):
+            L.expert_product_forward(xs, w, o, out=out)
+    for out in (memory[312:824].view(2, 16, 16), memory[1144:1656].view(2, 16, 16), memory[:512].view(2, 16, 16)):
+        with pytest.raises(L.LapsumError):
+            L.expert_product_backward_weights(dys, xs, w, o, out=out)
+    L.expert_product_backward_weights(dys, xs, w, o, out=w)  # w itself is not read
+    assert (memory == 0).all()
 
 
 def test_differentiable(L):
@@ -296,7 +319,7 @@ def test_both_fronts(L, monkeypatch):
         if hard._native is None:
             pytest.skip("the native front is not built")
         assert hard._native.expert_product_forward(xs, w, offsets) is not None
-        assert hard._native.expert_product_forward(xs.float(), w, offsets) is None
+        assert hard._native.expert_product_forward(xs.double(), w, offsets) is None
         with monkeypatch.context() as m:
             m.setattr(hard, "_native", None)
             slow = (L.expert_product_forward(xs, w, offsets), *L.expert_product_backward(dys, xs, w, offsets))

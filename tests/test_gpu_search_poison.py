@@ -20,9 +20,9 @@ import test_gpu_expert_product as e, test_gpu_beam_select as b
 assert L.LIB_PATH.endswith("liblapsum_ldspoison.so"), L.LIB_PATH
 L.load_library()
 for stored in ("in_out", "out_in"):
-    for dtype in ("bf16", "fp16"):
+    for dtype in ("bf16", "fp16", "fp32"):
         e.test_ragged(L, 264, 136, stored, dtype)
-    e.test_sizes_of_no_whole_16_bytes(L, 65, 127, stored)
+    e.test_sizes_of_no_whole_16_bytes(L, 65, 127, stored, "bf16")
     e.test_one_expert(L, 65, stored)
     e.test_many_rows(L, [300, 900, 0, 511], 512, 768, stored)
     e.test_tiles_of_every_kind(L, stored)

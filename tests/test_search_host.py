@@ -27,13 +27,13 @@ def test_struct_sizes():
 
 
 def products(lib):
-    def forward(w, x=P, stride=16, rows=10, offsets=P, out=P):
+    def forward(w, x=16 * P, stride=16, rows=10, offsets=P, out=32 * P):
         return lib.lapsum_expert_product_forward(x, stride, rows, w, offsets, out, None)
 
-    def rows_(w, x=P, stride=24, rows=10, offsets=P, out=P):
+    def rows_(w, x=16 * P, stride=24, rows=10, offsets=P, out=32 * P):
         return lib.lapsum_expert_product_backward_rows(x, stride, rows, w, offsets, out, None)
 
-    def weights(w, x=P, stride=16, rows=10, offsets=P, out=P, dy_stride=24):
+    def weights(w, x=16 * P, stride=16, rows=10, offsets=P, out=32 * P, dy_stride=24):
         return lib.lapsum_expert_product_backward_weights(x, stride, out, dy_stride, rows, offsets, w, None)
     return forward, rows_, weights
 
@@ -41,7 +41,7 @@ def products(lib):
 def test_product_checks(lib):
     for call in products(lib):
         assert call(None) == NULL
-        for bad, want in ((dict(dtype=hard.F32), OPTION), (dict(experts=0), SHAPE), (dict(experts=1025), SHAPE),
+        for bad, want in ((dict(dtype=3), OPTION), (dict(dtype=-1), OPTION), (dict(experts=0), SHAPE), (dict(experts=1025), SHAPE),
                           (dict(inputs=0), SHAPE), (dict(outputs=0), SHAPE),
                           (dict(inputs=2 ** 20 + 1, so=1, si=24), SHAPE), (dict(si=23), LAYOUT), (dict(so=2), LAYOUT),
                           (dict(si=1, so=15), LAYOUT), (dict(si=1, so=1), LAYOUT), (dict(si=2 ** 21 + 1), LAYOUT),
@@ -51,13 +51,16 @@ def test_product_checks(lib):
         for missing in ("x", "offsets", "out"):
             assert call(experts(), **{missing: None}) == NULL
         assert call(experts(), stride=15) == LAYOUT and call(experts(), stride=2 ** 21 + 1) == LAYOUT
+        assert call(experts(w=32 * P)) == LAYOUT  # in one place with what the call writes, or reads
+    for call in products(lib)[:2]:
+        assert call(experts(), out=16 * P) == LAYOUT and call(experts(), out=16 * P + 100) == LAYOUT
     weights = products(lib)[2]
     assert weights(experts(), dy_stride=23) == LAYOUT
     assert weights(experts(se=383)) == LAYOUT and weights(experts(se=0)) == LAYOUT  # matrices that share memory
 
 
 def test_beam_checks(lib):
-    def call(x=P, dtype=0, batch=2, beams=4, vocab=100, stride=100, scores=P, ended=None, end=-1, k=4, out=P, parents=P,
+    def call(x=P, dtype=0, batch=2, beams=4, vocab=100, stride=100, scores=2 * P, ended=None, end=-1, k=4, out=P, parents=P,
              tokens=P, ws=P, nbytes=2 ** 40):
         return lib.lapsum_beam_select(x, dtype, batch, beams, vocab, stride, scores, ended, end, k, out, parents, tokens,
                                       ws, nbytes, None)
@@ -67,7 +70,7 @@ def test_beam_checks(lib):
                 dict(batch=2 ** 24)):
         assert call(**bad) == SHAPE, bad
     assert call(k=0) == OPTION and call(k=65) == OPTION
-    assert call(stride=99) == LAYOUT
+    assert call(stride=99) == LAYOUT and call(scores=P) == LAYOUT
     assert call(ended=P) == OPTION and call(ended=P, end=100) == OPTION
     for missing in ("x", "scores", "out", "parents", "tokens"):
         assert call(**{missing: None}) == NULL
