@@ -210,6 +210,15 @@ def test_bad_offsets_stay_inside(L):
     falling = torch.tensor([80, 20, 60, 10, 5], dtype=torch.int32, device="cuda")
     L.expert_product_forward(xs, w, falling), L.expert_product_backward(dys, xs, w, falling)
     torch.cuda.synchronize()
+    # ranges over one another, of many rows: more tiles than there could be
+    xs, w, _, dys = inputs(5000, 264, 1032, list(range(21)), "bf16")
+    over = torch.tensor([0, 5000] * 10 + [0], dtype=torch.int32, device="cuda")
+    L.expert_product_forward(xs, w, over)
+    _, dw = L.expert_product_backward(dys, xs, w, over)
+    x, dy = xs.double(), dys.double()
+    want = ((x.t() @ dy).cpu(), (x.t().abs() @ dy.abs()).cpu(), 5000)
+    plain.check_product(dw[0], want), plain.check_product(dw[18], want)
+    assert (dw[1::2] == 0).all()
 
 
 def test_nothing_to_do(L):
