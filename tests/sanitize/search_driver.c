@@ -72,7 +72,7 @@ static void beams(void) {
                     EXPECT((bytes > 0) == (fine && k >= 1 && k <= LAPSUM_MAX_BEAMS), "bytes %zu", bytes);
                     const lapsum_status st =
                         lapsum_beam_select(at, LAPSUM_BF16, batch, beam, vocab, vocab, (const float *)at, NULL, 0, k,
-                                           (float *)at, (int32_t *)at, (int32_t *)at, NULL, 0, NULL);
+                                           (float *)(at + 1024), (int32_t *)at, (int32_t *)at, NULL, 0, NULL);
                     EXPECT(st == (!fine ? LAPSUM_ERR_SHAPE : (k < 1 || k > LAPSUM_MAX_BEAMS ? LAPSUM_ERR_OPTION
                                                                                              : LAPSUM_ERR_NULL)),
                            "select %lld %lld %lld %d: %d", (long long)batch, (long long)beam, (long long)vocab, k, (int)st);
