@@ -209,13 +209,20 @@ constexpr int kStreamed = 2;  // not kept in the caches: the products are anothe
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every window
 
 // 64 x 16 bytes from the lanes' offsets to consecutive places of LDS from `to` on (bytes).  Written out, since the compiler
-// would have every later read of LDS wait for it; whoever reads waits by arrived().
+// would have every later read of LDS wait for it; whoever reads waits by arrived().  The compiler does not look into it
+// either, so it keeps the distances itself: one wait state from a write of m0 to a load to LDS, five from a vector
+// instruction's write of a scalar register (the window's) to a load that reads it.
 LDEV void load_to_lds(window_t w, uint32_t to, uint32_t offset) {
   uint32_t m0;  // the compiler's; the place goes there
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-               : "=&s"(m0)
-               : "s"(to), "v"(offset), "s"(w)
-               : "memory");
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 2\n\t"
+      "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(to), "v"(offset), "s"(w)
+      : "memory");
 }
 LDEV uint32_t lds_at(const void *p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
@@ -361,7 +368,9 @@ struct Tile {
   // Places [0, m) x [0, n) of the tile.  Always kStores stores of a wave, so that they can be counted.
   static constexpr int kStores = kFrags * 4;
   LDEV void store(T *out, int64_t stride, int m, int n) const {
-    const int lane = lane_id(), wave = threadIdx.x / 64, wm = wave / WAVES_N, wn = wave % WAVES_N;
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));  // places are formed again for each tile, not held (and spilled) through the steps
+    const int wave = threadIdx.x / 64, wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int col = wn * 128 + lane % 16 * 8, step = (int)stride;
     m = m < kM ? m : kM;
     n = n < kN ? n : kN;
