@@ -31,15 +31,28 @@ LDEV f32x4 mfma(pack_t<f16> a, pack_t<f16> b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+LDEV int in_rows(const ProductArgs &p, int64_t o) { return (int)(o < 0 ? 0 : (o > p.rows ? p.rows : o)); }
+// An offset that the whole wave asks for: a scalar load, since a vector one would wait for all loads that are under way.
 LDEV int offset_of(const ProductArgs &p, int i) {
-  const int64_t o = p.offsets[i];
-  return (int)(o < 0 ? 0 : (o > p.rows ? p.rows : o));
+  using scalars = const __attribute__((address_space(4))) int32_t *;
+  return in_rows(p, ((scalars)(uintptr_t)p.offsets)[__builtin_amdgcn_readfirstlane(i)]);
 }
 
 // The rows in order are those before the first expert's, every expert's, and those behind the
-// last one's: experts + 2 ranges, of which the first and the last are no expert's.
+// last one's: experts + 2 ranges, of which the first and the last are no expert's.  `offset`: of g - 1, or any other
+// where there is none.
+LDEV int range_begin(const ProductArgs &p, int g, int offset) {
+  return g == 0 ? 0 : (g <= p.experts + 1 ? offset : (int)p.rows);
+}
+LDEV int offset_before(const ProductArgs &p, int g) { return g < 1 ? 0 : (g <= p.experts + 1 ? g - 1 : p.experts); }
+// a lane's own range
 LDEV int range_begin(const ProductArgs &p, int g) {
-  return g == 0 ? 0 : (g <= p.experts + 1 ? offset_of(p, g - 1) : (int)p.rows);
+  return range_begin(p, g, in_rows(p, p.offsets[offset_before(p, g)]));
+}
+// the whole wave's
+LDEV int range_begin_all(const ProductArgs &p, int g) {
+  g = __builtin_amdgcn_readfirstlane(g);
+  return range_begin(p, g, offset_of(p, offset_before(p, g)));
 }
 
 struct RowTile {
@@ -97,7 +110,7 @@ struct RowTiles {
     for (int i = 0; i < kBounds; ++i)
       if (i < per && here(first + i, read_lane(bound[i], at), read_lane(bound[i + 1], at))) return true;
     for (int i = kBounds; i < per; ++i)
-      if (here(first + i, range_begin(p, first + i), range_begin(p, first + i + 1))) return true;
+      if (here(first + i, range_begin_all(p, first + i), range_begin_all(p, first + i + 1))) return true;
     return false;
   }
 };
@@ -494,8 +507,7 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 2) void product_tile_kernel(
       const int rows = __builtin_amdgcn_readfirstlane(table.before[g + 1]) - before, in_range = t - before * tiles_n;
       const int first = in_range / (kGroup * tiles_n) * kGroup, group = rows - first < kGroup ? rows - first : kGroup;
       const int in = in_range - first * tiles_n;
-      const int begin = __builtin_amdgcn_readfirstlane(range_begin(p, g));
-      const int end = __builtin_amdgcn_readfirstlane(range_begin(p, g + 1));
+      const int begin = range_begin_all(p, g), end = range_begin_all(p, g + 1);
       RowTile r;
       r.expert = g >= 1 && g <= p.experts ? g - 1 : -1;
       r.first = begin + (first + in % group) * Work::kM;
@@ -523,9 +535,9 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 2) void product_tile_kernel(
   const int place_a = decltype(Work::Operands::a)::place(wave / WAVES_N * WM);
   const int place_b = kA + decltype(Work::Operands::b)::place(wave % WAVES_N * 128);
   bool more = true, half = false;  // half: a tile's second step of two is next
+  TilePlace<T> x = now;            // the tile that is loaded, the (ahead - 1)-th
   const auto begin = [&] {
     if (asked <= 0 && !half && more) {
-      TilePlace<T> x;
       do {
         more = place(ahead++, x);
       } while (more && x.sum <= 0);
@@ -581,23 +593,26 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N, 2) void product_tile_kernel(
     to = after(to);
   }
   begin();
-  typename Work::Operands x, y;
+  typename Work::Operands u, v;
   arrived<(kStages - 1) * Work::kLoads>();
 #pragma unroll
-  for (int i = 0; i < Work::kReadsA; ++i) x.a.read(i, lds + place_a);
+  for (int i = 0; i < Work::kReadsA; ++i) u.a.read(i, lds + place_a);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x.b.read(i, lds + place_b);
+  for (int i = 0; i < 8; ++i) u.b.read(i, lds + place_b);
 #pragma unroll 1
   for (int index = 1;; ++index) {
     w.clear();
 #pragma unroll 1
     for (int sum = now.sum; sum > 0; sum -= 2 * kDepth) {
-      step(x, y);
-      step(y, x);
+      step(u, v);
+      step(v, u);
     }
     w.store(now.out, p.cm, now.m, now.n);
     fresh = kStages - 1;
-    if (!place(index, now)) break;
+    if (more && ahead == index + 1)
+      now = x;  // mostly
+    else if (!place(index, now))
+      break;
   }
   // no load may reach LDS that is another workgroup's
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
