@@ -82,12 +82,7 @@ struct RowTiles {
       const int g = first + i;
       if (g < ranges) mine += tiles_of(range_begin(p, g), range_begin(p, g + 1), size);
     }
-    upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int x = __shfl_up(upto, d, 64);
-      if (lane_id() >= d) upto += x;
-    }
+    upto = (int)wave_incl_scan((uint32_t)mine);
   }
   LDEV int total() const { return read_lane(upto, 63); }
   // the index-th of them; false: there are no more
