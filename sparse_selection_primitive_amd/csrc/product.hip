@@ -742,33 +742,41 @@ bool whole(const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; }
 bool whole(int64_t n) { return n % 8 == 0; }
 
 // Which kernel takes the rows: by how long each would take, as far as the host knows sizes (not how the rows are
-// spread: experts that rows meet by chance have x rows each, x / size + 1/2 tiles).  Figures of bf16, in us.
-//  - 16 rows a workgroup: a start, then what its tiles draw through the caches.  4 experts of 2048 x 1024 with 12
-//    rows each: 9.4 (tiles of 128 x 256: 28), with 400 48 (30); 32 experts of 1024 x 4096 with a row each 27 (33), with
-//    24 68 (46).
-//  - 32 rows: a longer start, the caches' draw halved.  4 experts of 1024 x 4096, 96 rows each: 14.8 (16 rows 25.5,
-//    tiles 18.0); 256 experts of 2048 x 1024 with 24 rows 230 (tiles 205).
+// spread: experts that rows meet by chance have x rows each, x / size + 1/2 tiles).  Figures of bf16, in us.  On a grid
+// of 4, 32 and 256 experts of 512 x 512, 2048 x 1024 and 1024 x 4096 with 1 to 400 rows each, both ways of storing, what the
+// rule takes is within 1.2 us or 10% of the fastest of the four.
+//  - 16 rows a workgroup: a start, then what its tiles draw, from the caches faster than from memory.  4 experts of 2048 x 1024
+//    with 12 rows each: 8.8 (32 rows a workgroup 9.5, tiles of 128 x 256 31.8), with 400 44 (34, 33.5); 32 experts of 1024 x
+//    4096 with a row each 26.6 (24.8, 32.8), with 48 80 (84, 45).
+//  - 32 rows: the caches' draw halved, a start that grows with the sum, which four waves share.  4 experts of 1024 x 4096,
+//    48 rows each: 12.0 (16 rows 16.7, tiles 19.4); 256 experts of 2048 x 1024 with 24 rows 257 (241, 205).
 //  - 128 x 256: 0.42 a step where every workgroup has a compute unit to itself, else a round of 512; or the matrices' way
 //    from memory.
 //  - 256 x 256 takes as long as 1.85 of those; where the sum lies next to each other in a matrix, so that its lines come in halves,
-//    1.6.  8 experts of 4096 x 14336 with 2048 rows 1740 for 1830, 256 experts of 2048 x 1024 with 256 510 for 443, of 1024
-//    x 2048, lines in halves, 440 for 489, 64 experts of 2056 x 1416 with 469 rows 328 for 366; their matrices' gradients
-//    468 for 515 (256) and 360 for 394 (64).
+//    1.6; few rounds are whole ones.  8 experts of 4096 x 14336 with 2048 rows 1710 for 1830, 256 experts of 2048 x 1024 with
+//    256 510 for 430, of 1024 x 2048, lines in halves, 437 for 470, 64 experts of 2056 x 1416 with 469 rows 306 for 366, 32 of
+//    2048 x 1024 with 400, two rounds for one, 91 for 69; their matrices' gradients 430 for 490 (256) and 320 for 345 (64).
 enum Kind { kFew16, kFew32, kTile128, kTile256 };
 Kind tile_kind(double tiles128, double tiles256, bool halves) {
-  return tiles128 > 256 && tiles256 * (halves ? 1.6 : 1.85) < tiles128 ? kTile256 : kTile128;
+  if (tiles128 <= 256) return kTile128;
+  const auto rounds = [](double tiles, double each) { return tiles > 3 * each ? tiles / each : std::ceil(tiles / each); };
+  const double as_long = halves ? 1.6 : 1.85;
+  return tiles256 * as_long < tiles128 && rounds(tiles256, 256) * as_long < 2 * rounds(tiles128, 512) ? kTile256 : kTile128;
 }
 Kind rows_kind(const ProductArgs &p) {
+  const bool halves = p.bk == 1;
   const double rows = (double)p.rows, met = p.experts * (1.0 - std::exp(-rows / p.experts)), x = rows / met;
   const auto tiles = [&](int size) { return met * std::fmax(1.0, x / size + 0.5); };
-  const double matrix = (double)p.k * p.n * 2e-6, columns = std::ceil(p.n / 256.0), tiles128 = tiles(128) * columns;
-  const double few16 = 4.5 + tiles(16) * matrix / 6;
-  const double few32 = 6 + std::fmax(tiles(32) * matrix / 11, met * matrix / 4.5);
-  const double step = tiles128 <= 256 ? 0.42 : 0.95 * std::ceil(tiles128 / 512);
-  const double tile = 3 + std::fmax(step * p.k / 32, met * matrix / 5.2);
+  const double matrix = (double)p.k * p.n * 2e-6, all = met * matrix;  // MB
+  const double rate16 = all > 200 ? 5.5 : halves ? 5.2 : 9.0, rate32 = halves ? 7.0 : 8.5;
+  const double few16 = 4.5 + std::fmax(tiles(16) * matrix / rate16, all / 5.8);
+  const double few32 = 4 + p.k / (halves ? 256.0 : 512.0) + std::fmax(tiles(32) * matrix / rate32, all / 4.5);
+  const double columns = std::ceil(p.n / 256.0), tiles128 = tiles(128) * columns;
+  const double steps = (tiles128 <= 256 ? 0.42 : 0.95 * std::ceil(tiles128 / 512)) * p.k / 32, memory = all / 6.2;
+  const double tile = 4 + std::fmax(steps, memory) + 0.1 * std::fmin(steps, memory);
   if (few16 <= few32 && few16 < tile) return kFew16;
   if (few32 < tile) return kFew32;
-  return tile_kind(tiles128, tiles(256) * columns, p.bk == 1);
+  return tile_kind(tiles128, tiles(256) * columns, halves);
 }
 
 template <class T, bool B_NEXT>
