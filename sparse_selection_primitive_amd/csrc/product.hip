@@ -7,12 +7,12 @@
 // expert and rows from the offsets: tiles are counted through the experts in order, one wave's lanes a
 // few experts each.
 //
-// Few rows are bounded by reading the matrices: 192 rows of 135 experts of 2048 x 1024 take 71 us (566 MB, 7.9 TB/s
-// with what the last call left in the memory-side cache), 8 rows of 8 experts 8 to 9.4 us (34 MB).  Many rows are
-// bounded by the matrix instructions and the power that they and LDS draw: 16384 rows of 8 experts of 4096 x 14336 take 1.70 ms
-// (1.13 PFLOP/s, the clock at 1.6 to 2.0 of 2.4 GHz; the library's product of one expert after another 1.84 ms).  In
+// Few rows are bounded by reading the matrices: 192 rows of 135 experts of 2048 x 1024 take 70 us (566 MB, 8.1 TB/s
+// with what the last call left in the memory-side cache), 8 rows of 8 experts 7.8 to 8.0 us (34 MB).  Many rows are
+// bounded by the matrix instructions and the power that they and LDS draw: 16384 rows of 8 experts of 4096 x 14336 take 1.69 ms
+// (1.14 PFLOP/s, the clock at 1.6 to 2.0 of 2.4 GHz; the library's product of one expert after another 1.84 ms).  In
 // between the matrices' way from memory and the ragged ends count as well: 65536 rows of 256 experts of 2048 x 1024
-// 0.43 ms, the same for the rows' gradient, 0.45 for the matrices' (of which 0.17 ms are writing 1.1 GB).
+// 0.38 to 0.43 ms, the same for the rows' gradient, 0.43 to 0.49 for the matrices' (of which 0.17 ms are writing 1.1 GB).
 #include <cmath>
 #include <type_traits>
 
