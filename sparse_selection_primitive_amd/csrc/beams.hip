@@ -87,8 +87,9 @@ __global__ __launch_bounds__(256) void beam_parts_kernel(BeamArgs a) {
 #pragma unroll
       for (int j = 0; j < N; ++j) top = fmaxf(top, v[i][j]);
     float sum = 0.0f;
-    if (top > -1e30f && top < 1e30f) {
-      // e^(x - top) = 2^(x c - h) 2^-l with h + l the product top c in two parts
+    // e^(x - top) = 2^(x c - h) 2^-l with h + l the product top c in two parts, without a subtraction a token.  l is up to half
+    // a step of h and both powers hold it: below 2^24 it is at most 1, at 10^10 it is 440, and 2^l 2^-l is no number.
+    if (top > -16777216.0f && top < 16777216.0f) {
       const float h = top * kLog2e, l = __builtin_fmaf(top, kLog2e, -h);
 #pragma unroll
       for (int i = 0; i < L; ++i) {
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(256) void beam_parts_kernel(BeamArgs a) {
         sum += part_sum;
       }
       sum *= __builtin_amdgcn_exp2f(-l);
-    } else {  // nothing, only masked tokens (of the type's lowest value, too), or infinities
+    } else {  // nothing, masked tokens alone (by any finite value, too), large logits, or infinities
 #pragma unroll
       for (int i = 0; i < L; ++i)
 #pragma unroll
