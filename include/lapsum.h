@@ -513,7 +513,8 @@ lapsum_status lapsum_expert_product_backward_weights(const void *xs, int64_t xs_
  *   ended      device [batch, beams] bytes, or NULL: a beam whose byte is not 0 has one continuation,
  *              end_token (in 0 .. vocab - 1), at its own score; its logits are not read
  *   k          1 .. LAPSUM_MAX_BEAMS, also beyond `beams` (twice as many, say)
- *   scores_out device [batch, k] fp32, not scores itself (LAPSUM_ERR_LAYOUT);  parents, tokens device [batch, k] int32
+ *   scores_out device [batch, k] fp32;  parents, tokens device [batch, k] int32; these and the workspace in no memory of
+ *              each other's or of what the call reads (LAPSUM_ERR_LAYOUT)
  * Scores are compared in fp64 (the sum of exponentials is an fp32 sum) and rounded to fp32 once.  A
  * token whose logit is -inf is no continuation; logits of +inf share the
  * probability equally, the others have none.  A beam with a NaN among its logits, without a logit above -inf,

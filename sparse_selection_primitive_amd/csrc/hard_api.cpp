@@ -175,6 +175,55 @@ int64_t experts_bytes(const lapsum_experts &w) {  // strides that no memory hold
   return (int64_t)(bytes < most ? bytes : most);
 }
 
+// A layout of memory: `width` bytes next to each other, at every sum of up to three strides (the largest first).
+struct Layout {
+  struct Dim {
+    int64_t stride, size;  // bytes, more than one place each
+  };
+  const void *at;
+  int64_t width;
+  int dims;
+  Dim dim[3];
+
+  __int128 extent(int from) const {  // of what the dimensions from `from` on span
+    __int128 bytes = width;
+    for (int i = from; i < dims; ++i) bytes += (__int128)dim[i].stride * (dim[i].size - 1);
+    return bytes;
+  }
+  // Whether a byte of it lies in [lo, hi), from `at` on.  Only places whose extent meets the stretch are looked at, and one that
+  // lies in it whole ends the search, so a dimension has a few to look at whatever its size.
+  bool meets(__int128 lo, __int128 hi, int from = 0) const {
+    if (from == dims) return lo < width && hi > 0;
+    const __int128 stride = dim[from].stride, inner = extent(from + 1);
+    __int128 last = hi > 0 ? (hi - 1) / stride : -1;
+    if (last > dim[from].size - 1) last = dim[from].size - 1;
+    for (__int128 i = lo < inner ? 0 : (lo - inner) / stride + 1; i <= last; ++i)
+      if (meets(lo - i * stride, hi - i * stride, from + 1)) return true;
+    return false;
+  }
+};
+struct Block {
+  const void *at;  // or NULL: none
+  int64_t bytes;
+};
+bool meet(const Block &a, const Block &b) { return a.at && b.at && meet(a.at, a.bytes, b.at, b.bytes); }
+bool meet(const Layout &a, const Block &b) {
+  if (!b.at) return false;
+  const __int128 lo = (__int128) reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at);
+  return a.meets(lo, lo + b.bytes);
+}
+// Whether a block that is written meets another one that is, or one that is read.
+template <int W, int R>
+bool any_meet(const Block (&written)[W], const Block (&read)[R]) {
+  for (int i = 0; i < W; ++i) {
+    for (int j = i + 1; j < W; ++j)
+      if (meet(written[i], written[j])) return true;
+    for (const Block &b : read)
+      if (meet(written[i], b)) return true;
+  }
+  return false;
+}
+
 ProductArgs product_args(const lapsum_experts &w, int64_t rows, const int32_t *offsets) {
   ProductArgs a{};
   a.rows = rows;
@@ -503,9 +552,18 @@ lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batc
   if (row_stride < vocab) return LAPSUM_ERR_LAYOUT;
   if (ended && (end_token < 0 || end_token >= vocab)) return LAPSUM_ERR_OPTION;
   if (!logits || !scores || !scores_out || !parents || !tokens) return LAPSUM_ERR_NULL;
-  if (scores_out == scores) return LAPSUM_ERR_LAYOUT;  // of several searches one is read when another is written
-  st = check_workspace(workspace, workspace_bytes, beam_bytes(batch, beams, vocab));
+  const size_t need = beam_bytes(batch, beams, vocab);
+  st = check_workspace(workspace, workspace_bytes, need);
   if (st != LAPSUM_OK) return st;
+  // one search is read when another is written
+  const int64_t rows = batch * beams, places = batch * k * 4;
+  const Block written[] = {{scores_out, places}, {parents, places}, {tokens, places}, {workspace, (int64_t)need}};
+  const Block read[] = {{scores, rows * 4}, {ended, rows}};
+  if (any_meet(written, read)) return LAPSUM_ERR_LAYOUT;
+  const __int128 step = (__int128)row_stride * type_bytes(dtype), most = (__int128)1 << 62;
+  const Layout x{logits, vocab * type_bytes(dtype), rows > 1, {{(int64_t)(step < most ? step : most), rows}}};
+  for (const Block &b : written)
+    if (meet(x, b)) return LAPSUM_ERR_LAYOUT;
   BeamArgs a{};
   a.logits = logits;
   a.batch = batch;
