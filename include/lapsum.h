@@ -530,7 +530,8 @@ lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batc
  * sequence b * beams + parents[b, j] was, in place, without a second cache: the entries below the parent's
  * length, and with them the accounts and positions.  Entries at that length and behind stay as they are.
  *   cache    batch a multiple of beams (at most LAPSUM_MAX_BEAMS); no two entries may share memory
- *            (LAPSUM_ERR_LAYOUT), as for the eviction; v may be k (the same pointer and strides), else they share none
+ *            (LAPSUM_ERR_LAYOUT), as for the eviction; v may be k (the same pointer
+ *            and strides, but for those of sizes of one), else they share none
  *   parents  device [batch / beams, beams] int32; one outside 0 .. beams - 1 leaves its sequence
  *            as it is, with length 0
  *   lengths  device [batch] int32, taken as 0 .. capacity

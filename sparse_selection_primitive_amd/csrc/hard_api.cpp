@@ -133,6 +133,12 @@ bool apart(const lapsum_cache &c, int64_t batch, int64_t head, int64_t entry) {
   return true;
 }
 
+// Whether keys and values lie alike; the stride of a size of one is any.
+bool same_strides(const lapsum_cache &c) {
+  return (c.batch == 1 || c.k_stride_batch == c.v_stride_batch) && (c.heads == 1 || c.k_stride_head == c.v_stride_head) &&
+         (c.capacity == 1 || c.k_stride_entry == c.v_stride_entry);
+}
+
 lapsum_status check_attend(const lapsum_cache *c, int64_t news, int64_t q_heads) {
   const lapsum_status st = check_cache(c);
   if (st != LAPSUM_OK) return st;
@@ -601,8 +607,7 @@ lapsum_status lapsum_cache_reorder(const lapsum_cache *cache, int64_t beams, con
   if (st != LAPSUM_OK) return st;
   ReorderArgs a{};
   // keys that are the values as well move once
-  a.one = cache->k == cache->v && cache->k_stride_batch == cache->v_stride_batch &&
-          cache->k_stride_head == cache->v_stride_head && cache->k_stride_entry == cache->v_stride_entry;
+  a.one = cache->k == cache->v && same_strides(*cache);
   a.k = cache->k;
   a.v = cache->v;
   a.kb = cache->k_stride_batch;
