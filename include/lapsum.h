@@ -531,12 +531,14 @@ lapsum_status lapsum_beam_select(const void *logits, int32_t dtype, int64_t batc
  * length, and with them the accounts and positions.  Entries at that length and behind stay as they are.
  *   cache    batch a multiple of beams (at most LAPSUM_MAX_BEAMS); no two entries may share memory
  *            (LAPSUM_ERR_LAYOUT), as for the eviction; v may be k (the same pointer
- *            and strides, but for those of sizes of one), else they share none
+ *            and strides, but for those of sizes of one), else they share none (LAPSUM_ERR_LAYOUT where both lie alike or
+ *            one of them has no gaps; of others that is the caller's to see to)
  *   parents  device [batch / beams, beams] int32; one outside 0 .. beams - 1 leaves its sequence
  *            as it is, with length 0
  *   lengths  device [batch] int32, taken as 0 .. capacity
  *   account, positions  device [batch, heads, capacity], each may be NULL
- *   lengths_out         device [batch]: the parents' lengths; not lengths itself (LAPSUM_ERR_LAYOUT) */
+ *   lengths_out         device [batch]: the parents' lengths
+ * No array in the memory of another (LAPSUM_ERR_LAYOUT), but for lengths and parents, which are only read. */
 lapsum_status lapsum_cache_reorder(const lapsum_cache *cache, int64_t beams, const int32_t *parents,
                                    const int32_t *lengths, float *account, int32_t *positions, int32_t *lengths_out,
                                    void *stream);

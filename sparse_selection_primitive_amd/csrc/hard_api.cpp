@@ -199,9 +199,10 @@ struct Layout {
   // Whether a byte of it lies in [lo, hi), from `at` on.  Only places whose extent meets the stretch are looked at, and one that
   // lies in it whole ends the search, so a dimension has a few to look at whatever its size.
   bool meets(__int128 lo, __int128 hi, int from = 0) const {
-    if (from == dims) return lo < width && hi > 0;
+    if (lo >= extent(from) || hi <= 0) return false;  // as nearly always
+    if (from == dims) return true;
     const __int128 stride = dim[from].stride, inner = extent(from + 1);
-    __int128 last = hi > 0 ? (hi - 1) / stride : -1;
+    __int128 last = (hi - 1) / stride;
     if (last > dim[from].size - 1) last = dim[from].size - 1;
     for (__int128 i = lo < inner ? 0 : (lo - inner) / stride + 1; i <= last; ++i)
       if (meets(lo - i * stride, hi - i * stride, from + 1)) return true;
@@ -228,6 +229,42 @@ bool any_meet(const Block (&written)[W], const Block (&read)[R]) {
       if (meet(written[i], b)) return true;
   }
   return false;
+}
+
+// The keys or the values of a cache whose entries are apart.
+Layout side_of(const lapsum_cache &c, const void *at, int64_t batch, int64_t head, int64_t entry) {
+  Layout x{at, (int64_t)c.width * 2, 0, {}};
+  for (const Layout::Dim &d : {Layout::Dim{batch, c.batch}, Layout::Dim{head, c.heads}, Layout::Dim{entry, c.capacity}}) {
+    if (d.size == 1) continue;
+    const __int128 stride = (__int128)d.stride * 2, most = (__int128)1 << 62;
+    int i = x.dims++;
+    for (; i > 0 && x.dim[i - 1].stride < stride; --i) x.dim[i] = x.dim[i - 1];
+    x.dim[i] = {(int64_t)(stride < most ? stride : most), d.size};
+  }
+  return x;
+}
+// Whether an entry's keys share memory with an entry's values, for caches that are not one and whose entries are apart: known where
+// both lie alike, begin together, or one of them fills what it spans.  (Unlike layouts, both with gaps, that are woven into each
+// other are not looked at further.)
+bool keys_meet_values(const lapsum_cache &c) {
+  if (c.k == c.v) return true;
+  const Layout k = side_of(c, c.k, c.k_stride_batch, c.k_stride_head, c.k_stride_entry);
+  const Layout v = side_of(c, c.v, c.v_stride_batch, c.v_stride_head, c.v_stride_entry);
+  const __int128 all = (__int128)c.batch * c.heads * c.capacity * k.width, most = (__int128)1 << 62;
+  if (all < most && k.extent(0) == all) return meet(v, {c.k, (int64_t)all});
+  if (all < most && v.extent(0) == all) return meet(k, {c.v, (int64_t)all});
+  if (!same_strides(c)) return false;
+  const __int128 ahead = (__int128) reinterpret_cast<uintptr_t>(c.v) - reinterpret_cast<uintptr_t>(c.k);
+  // An entry's values are at ahead + x from the first keys, another's keys at y.  y - x over all pairs is a layout of twice as
+  // many places less one a dimension, which starts at minus its half; they meet where ahead is less than an entry from it.
+  Layout apart = k;
+  apart.width = 1;
+  __int128 half = 0;
+  for (int i = 0; i < k.dims; ++i) {
+    half += (__int128)k.dim[i].stride * (k.dim[i].size - 1);
+    apart.dim[i].size = 2 * k.dim[i].size - 1;
+  }
+  return apart.meets(half + ahead - k.width + 1, half + ahead + k.width);
 }
 
 ProductArgs product_args(const lapsum_experts &w, int64_t rows, const int32_t *offsets) {
@@ -602,12 +639,23 @@ lapsum_status lapsum_cache_reorder(const lapsum_cache *cache, int64_t beams, con
       !apart(*cache, cache->v_stride_batch, cache->v_stride_head, cache->v_stride_entry))
     return LAPSUM_ERR_LAYOUT;
   if (!parents || !lengths || !lengths_out) return LAPSUM_ERR_NULL;
-  if (lengths_out == lengths) return LAPSUM_ERR_LAYOUT;
   st = check_cache_pointers(cache);
   if (st != LAPSUM_OK) return st;
   ReorderArgs a{};
   // keys that are the values as well move once
   a.one = cache->k == cache->v && same_strides(*cache);
+  if (!a.one && keys_meet_values(*cache)) return LAPSUM_ERR_LAYOUT;
+  // one workgroup writes when another still reads
+  const int64_t per_cache = cache->batch * 4;
+  const __int128 entries = (__int128)cache->batch * cache->heads * cache->capacity * 4, most = (__int128)1 << 62;
+  const int64_t per_entry = (int64_t)(entries < most ? entries : most);
+  const Block written[] = {{lengths_out, per_cache}, {account, per_entry}, {positions, per_entry}};
+  const Block read[] = {{lengths, per_cache}, {parents, per_cache}};
+  if (any_meet(written, read)) return LAPSUM_ERR_LAYOUT;
+  const Layout k = side_of(*cache, cache->k, cache->k_stride_batch, cache->k_stride_head, cache->k_stride_entry);
+  const Layout v = side_of(*cache, cache->v, cache->v_stride_batch, cache->v_stride_head, cache->v_stride_entry);
+  for (const Block &b : {written[0], written[1], written[2], read[0], read[1]})
+    if (meet(k, b) || meet(v, b)) return LAPSUM_ERR_LAYOUT;
   a.k = cache->k;
   a.v = cache->v;
   a.kb = cache->k_stride_batch;
