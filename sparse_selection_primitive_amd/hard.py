@@ -760,7 +760,7 @@ def cache_reorder(k, v, parents, lengths, account=None, positions=None):
     if positions is not None:
         positions = _out(positions, "positions", torch.int32, shape, dev)
     after = torch.empty_like(lengths)
-    if k.numel() == 0:
+    if 0 in shape:
         there = (parents >= 0) & (parents < beams)
         return torch.where(there, lengths.view(searches, beams).clamp(0, shape[2]).gather(
             1, parents.long().clamp(0, max(beams - 1, 0))), 0).flatten() if shape[0] else after

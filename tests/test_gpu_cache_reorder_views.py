@@ -45,3 +45,18 @@ def test_one_tensor_through_two_views(L, monkeypatch, kind, beams, front):
         parents = i32([[(i + 1) % beams for i in range(beams)]])
         after = L.cache_reorder(k, v, parents, i32([capacity] * beams))
         assert after.tolist() == [capacity] * beams and torch.equal(x, before.roll(-turn, 0))
+
+
+def test_entries_without_width_are_refused(L):
+    """Accounts and positions have places then, which would have to move."""
+    k, account = torch.zeros(2, 3, 8, 0, device="cuda").bfloat16(), torch.arange(48.0, device="cuda").view(2, 3, 8)
+    before = account.clone()
+    with pytest.raises(L.LapsumError):
+        L.cache_reorder(k, k.clone(), i32([[1, 0]]), i32([8, 8]), account)
+    assert torch.equal(account, before)
+    # no cache, head or entry at all: there is nothing to move
+    for shape in ((0, 3, 8, 64), (2, 0, 8, 64), (2, 3, 0, 64)):
+        k = torch.zeros(shape, device="cuda").bfloat16()
+        n = shape[0]
+        assert L.cache_reorder(k, k.clone(), i32([[1, 0]]) if n else torch.zeros(0, 2, device="cuda", dtype=torch.int32),
+                               i32([8, 5][:n])).tolist() == [min(5, shape[2]), min(8, shape[2])][:n]
