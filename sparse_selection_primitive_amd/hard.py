@@ -33,6 +33,7 @@ import ctypes
 import functools
 import importlib.util
 import os
+import warnings
 
 from . import EXPORTED, LapsumError, _check, _workspace, load_library
 
@@ -117,8 +118,11 @@ def _bind():
         spec = importlib.util.spec_from_file_location(__package__ + "._binding", _NATIVE_PATH)
         native = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(native)
-        if not all(hasattr(native, name) or name.endswith("_bytes") for name in _NATIVE_CALLS):
-            return  # built before these calls were there
+        missing = [n for n in _NATIVE_CALLS if not hasattr(native, n) and not n.endswith("_bytes")]
+        if missing:  # built before these calls were there
+            warnings.warn(f"{_NATIVE_PATH} is out of date (no {missing[0]}) and not used: calls of the hard selections take "
+                          "about 4 us more each; python -m sparse_selection_primitive_amd.build builds it again", RuntimeWarning)
+            return
         native.bind(*[ctypes.cast(getattr(lib, "lapsum_" + name), ctypes.c_void_p).value for name in _NATIVE_CALLS])
         native.on_failure(_check)
         _native = native
