@@ -48,6 +48,9 @@ LDEV void load_tokens(const T *row, int t, int vocab, float (&x)[Pack<T>::N]) {
   }
 }
 
+// An exponential, a product and an addition to a join: up to 4 2^-24 of the sum.  With the rounded arguments, which weigh as much as
+// the row's entropy, a row of V tokens errs by (33 + 2.3 ln V + 4 joins) 2^-24 at most, 106 for 50000; ascending maxima 5.
+//
 // joins (m, s) with (m2, s2): sums of e^(x - maximum), of -inf alone (-inf, 0); where the maximum is
 // +inf, s counts what is +inf
 LDEV void join(float &m, float &s, float m2, float s2) {
