@@ -6,8 +6,9 @@
 // not written, a cache that nobody else takes is not read.
 //
 // Bound by memory: every cache that is taken over read once, every changed one written once.  16 searches of 4 beams, 8
-// heads of up to 8192 entries of 128, with accounts and positions: 345 to 370 us for 1.88 GB (5.1 to 5.4 TB/s; a copy
-// reaches 5.2); 12 of 5 beams, 2 heads of up to 3001 of 96: 23 us; one search of 4 beams of 1000 entries 7.0 us.  From
+// heads of up to 8192 entries of 128, with accounts and positions, by the parents: 1.55 to 2.23 GB in 311 to 460 us (4.8 to
+// 5.4 TB/s; a copy reaches 5.2); 12 of 5 beams, 2 heads of up to 3001 of 96: 110 to 141 MB in 19 to 26 us; one search of 4 beams of 1000
+// entries 5.0 to 7.5 us for 8 to 33 MB.  From
 // 17 beams on a thread holds 8 bytes of each beam's, and few threads fit: 40 beams of 4000 entries 3.0 TB/s.
 #include "hard_dev.hpp"
 #include "hard_internal.hpp"
